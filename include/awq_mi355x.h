@@ -449,6 +449,146 @@ awq_status awq_linear_w4a16_group_bf16(const awq_linear_item* items, int32_t cou
                                        int64_t m, int64_t k, int32_t g, void* workspace,
                                        size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The 8-bit paged KV cache: awq_rope_table, awq_kv8_append, awq_attn_kv8.
+ * What stands between a layer's q, k, v projections (awq_linear_w4a16_group)
+ * and its o projection.  A decode step reads its weights and its cache; these
+ * entries hold the cache in 8 bits with a scale per block of tokens and head,
+ * as the packed linears hold the weights in 4 bits with a scale per group.
+ *
+ * awq_kv8_cache describes the cache and the batch of one call (host struct of
+ * device pointers):
+ *   k       [pages][hkv][page][d]  e4m3 codes (OCP: 4 exponent bits, 3 mantissa
+ *           bits, largest 448, NaN 0x7F / 0xFF, no infinity), 16-byte aligned;
+ *   v       [pages][hkv][d][page]  e4m3 codes, token contiguous, 16-byte aligned;
+ *   k_scale, v_scale [pages][hkv]  fp32: the value of a code c is scale * c;
+ *   block_table [b][max_pages]     int32: the page of the cache that holds
+ *           positions j * page .. (j + 1) * page - 1 of sequence i;
+ *   cu_q    [b + 1] int32, ascending from 0, or NULL: rows cu_q[i] ..
+ *           cu_q[i + 1] - 1 of q, k, v and the outputs are sequence i's new
+ *           tokens.  NULL: row i is sequence i's one new token (rows >= b);
+ *   ctx     [b] int32: tokens of sequence i, the new ones among them.  New row
+ *           r of n stands at position ctx - n + r.
+ *   A page belongs to one sequence while that sequence appends to it; whole
+ *   pages before it may be shared.  Rows behind the last sequence are neither
+ *   read nor written.  Sequences may have no rows, or no tokens at all.
+ *   The arrays are device data and are not checked on the host: whatever they
+ *   hold, nothing outside the tensors described here is read or written.  A
+ *   page number outside 0 .. pages - 1, or a position past max_pages pages,
+ *   is dropped by the append and gives NaN where the attention would see it.
+ *   Limits: page in {64, 128, 256}; d in {64, 128}; 1 <= hkv <= 1024; hq a
+ *   multiple of hkv; 0 <= b <= 65536; 0 <= rows <= 2^24 and rows * hq <= 2^30.
+ *   q, k, v and the outputs are [rows][heads][d] with rows `stride` elements
+ *   apart (a multiple of 8, 16-byte aligned, so slices of the stacked q, k, v
+ *   projection do).
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* block_table;
+  const int32_t* cu_q;
+  const int32_t* ctx;
+  int64_t pages;
+  int64_t max_pages;
+  int64_t b;
+  int32_t page;
+  int32_t hkv;
+  int32_t d;
+} awq_kv8_cache;
+
+/* ---------------------------------------------------------------------------
+ * awq_rope_table -- cosines and sines of rotary positions.
+ *   table [positions][rot] fp32 out: table[p][j] = m cos(p f_j) and
+ *   table[p][rot/2 + j] = m sin(p f_j), j < rot/2, within 2 ulp of m; angles
+ *   are reduced in float64.  f_j = base^(-2j/rot), changed for long contexts by
+ *     AWQ_ROPE_NONE    nothing (the other parameters are not read), m = 1;
+ *     AWQ_ROPE_LINEAR  f / factor, m = 1;
+ *     AWQ_ROPE_BANDS   w f + (1 - w) f / factor, m = 1, with
+ *                      w = clamp((trained f / 2 pi - low) / (high - low), 0, 1):
+ *                      pairs of more than `high` turns over the `trained`
+ *                      positions stay, those below `low` turns are stretched;
+ *     AWQ_ROPE_YARN    (1 - w) f + w f / factor, w linear in j from
+ *                      max(floor(n(high)), 0) to min(ceil(n(low)), rot - 1),
+ *                      n(t) = rot ln(trained / (2 pi t)) / (2 ln base);
+ *                      m = 0.1 ln(factor) + 1.
+ *   Limits: rot even in 2..256; positions <= 2^31 - 1; base > 1; factor > 0;
+ *   0 < low < high and trained > 0 where they are read.
+ * ------------------------------------------------------------------------- */
+enum { AWQ_ROPE_NONE = 0, AWQ_ROPE_LINEAR = 1, AWQ_ROPE_BANDS = 2, AWQ_ROPE_YARN = 3 };
+awq_status awq_rope_table(int64_t positions, int32_t rot, double base, int32_t scaling,
+                          double factor, double low, double high, double trained,
+                          float* table, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * awq_kv8_append, awq_kv8_append_bf16 -- rotate the new tokens' queries and
+ * keys, quantize keys and values and append them to the cache (fp16 or bf16
+ * q, k, v, q_out).
+ *   rope [positions][rot] (awq_rope_table; NULL: no rotation): channels x_a, x_b
+ *   of a pair become x_a c - x_b s and x_b c + x_a s in fp32, each product and
+ *   sum rounded once; pair j is channels (j, rot/2 + j), or (2j, 2j + 1) when
+ *   interleaved; channels from rot on pass.  q_out = the rotated q rounded to
+ *   its type (q NULL: queries are left alone); q_out may be q itself with the
+ *   same stride.  Rotated k goes to the cache from fp32.
+ *   Scale of a page and head: 2^e with the least e >= -64 for which the largest
+ *   magnitude appended to the page by this call is at most 448 * 2^e.  Where
+ *   the page holds older tokens of the sequence the scale never falls: it is
+ *   the larger of the old one and that, and older codes are requantized to
+ *   e4m3_rn(code * old / new), exact but for results below 2^-6.  New codes are
+ *   e4m3_rn(x / scale) (ties to even).  Slots behind the sequence's end keep
+ *   what they held.
+ *   A token whose rotated k or v holds inf or NaN, or whose position is not in
+ *   the table, is stored as a k of NaN codes and a v of zeros and does not
+ *   count for the scales: who may see it gets NaN, and nobody else does.  Its
+ *   query is NaN where the position is not in the table.
+ *   rot: a multiple of 16 up to d.  Positions below 0 (ctx < n) are dropped.
+ * ------------------------------------------------------------------------- */
+awq_status awq_kv8_append(const awq_kv8_cache* cache, int64_t rows, const uint16_t* q,
+                          int64_t q_stride, int32_t hq, const uint16_t* k,
+                          int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                          const float* rope, int64_t positions, int32_t rot,
+                          int32_t interleaved, uint16_t* q_out, int64_t q_out_stride,
+                          void* stream);
+awq_status awq_kv8_append_bf16(const awq_kv8_cache* cache, int64_t rows, const uint16_t* q,
+                               int64_t q_stride, int32_t hq, const uint16_t* k,
+                               int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                               const float* rope, int64_t positions, int32_t rot,
+                               int32_t interleaved, uint16_t* q_out,
+                               int64_t q_out_stride, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * awq_attn_kv8, awq_attn_kv8_bf16 -- causal attention of the new tokens over
+ * the cache (append them first): query head a reads key/value head a / (hq/hkv).
+ *   out[r][a] = sum_t softmax_t(scale q[r][a] . k[t]) v[t] over the positions t
+ *   up to the row's own; zeros for a row that sees none.  lse [rows][hq] fp32
+ *   (may be NULL): the natural logarithm of sum_t exp(scale q . k[t]), -inf
+ *   for such a row (results of parts of a context can be joined with it).
+ *   Codes enter the products exactly; scores, statistics and sums are fp32,
+ *   the softmax weights of the value product fp16 (relative rounding 2^-11).
+ *   Scales: positive, finite, the value scales of one context within 2^90 of
+ *   each other; values |scale * code| within fp32.  v codes of visible tokens
+ *   must not be NaN (awq_kv8_append writes none).
+ *   max_q >= 1: the most new tokens that one sequence has, as far as the host
+ *   knows.  It chooses between kernels; results are right for any value.
+ *   workspace: awq_attn_kv8_workspace_size(b, rows, hq, hkv, d, page,
+ *            max_pages, max_q) bytes, 256-byte aligned (NULL if that is 0):
+ *            partial results where a long context is split over work-groups.
+ *            Contents on entry are ignored.
+ *   Limits: those of the cache; scale > 0.
+ * ------------------------------------------------------------------------- */
+size_t awq_attn_kv8_workspace_size(int64_t b, int64_t rows, int32_t hq, int32_t hkv,
+                                   int32_t d, int32_t page, int64_t max_pages,
+                                   int64_t max_q);
+awq_status awq_attn_kv8(const awq_kv8_cache* cache, int64_t rows, int64_t max_q,
+                        const uint16_t* q, int64_t q_stride, int32_t hq, float scale,
+                        uint16_t* out, int64_t out_stride, float* lse, void* workspace,
+                        size_t ws_bytes, void* stream);
+awq_status awq_attn_kv8_bf16(const awq_kv8_cache* cache, int64_t rows, int64_t max_q,
+                             const uint16_t* q, int64_t q_stride, int32_t hq, float scale,
+                             uint16_t* out, int64_t out_stride, float* lse,
+                             void* workspace, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -11,6 +11,9 @@ the library's HIP kernels; there is no fallback.
     awq_pack_int4(w, s16, g)                    -> (qweight, scales, qzeros, nonfinite int32 [1])
     awq_linear_w4a16(x, qweight, scales, qzeros, inv_s16, g) -> y fp16 [m, n]
     awq_linear_w4a16_group([(x, qweight, scales, qzeros, inv_s16, out), ...], g) -> [y, ...]
+    awq_rope_table(positions, rot)              -> table fp32 [positions, rot]
+    awq_kv8_append(k, v, *cache, block_table, ctx, q=q, rope=table) -> rotated q
+    awq_attn_kv8(q, *cache, block_table, ctx)   -> out [rows, hq, d]
 
 The linear calls take an optional ``workspace`` (a uint8 device tensor of at
 least the size the library's query returns); without one the binding
@@ -28,7 +31,8 @@ __all__ = ["awq_calib_stats", "awq_search_workspace_size", "awq_search_scale", "
            "awq_linear_w4a16_bf16", "awq_linear_w4a16_group_bf16",
            "awq_salient_channels", "awq_channel_mask", "awq_gather_channels", "awq_mixed_loss",
            "awq_linear_mixed", "awq_fold_inv_scale_rows", "awq_linear_w4a16_group_noalloc",
-           "AWQError", "load"]
+           "awq_rope_table", "awq_kv8_append", "awq_kv8_append_bf16", "awq_attn_kv8", "awq_attn_kv8_bf16",
+           "awq_attn_kv8_workspace_size", "kv8_cache", "AWQError", "load"]
 
 
 def load():
@@ -514,3 +518,221 @@ def awq_linear_mixed(x, qweight, scales, qzeros, keep16, w_s, idx, g=128, out=No
     _lib.check("awq_linear_mixed", st)
     return y
 
+
+
+# ---------------------------------------------------------------- 8-bit paged KV cache
+
+_ROPE = {"none": 0, "linear": 1, "bands": 2, "yarn": 3}
+
+
+def awq_rope_table(positions, rot, base=10000.0, scaling="none", factor=1.0, low=1.0, high=32.0, trained=8192,
+                   out=None, device=None):
+    """Cosines and sines of rotary positions 0 .. positions - 1: fp32
+    [positions, rot], the cosines of the rot / 2 pairs first.  ``scaling``:
+    "none", "linear" (frequencies / factor), "bands" (by the turns a pair makes
+    over ``trained`` positions, between ``low`` and ``high``) or "yarn" (see the
+    C header for the formulas)."""
+    torch = _torch()
+    if scaling not in _ROPE:
+        raise ValueError(f"scaling must be one of {sorted(_ROPE)} (got {scaling!r})")
+    if out is None:
+        if positions < 1 or rot < 2:
+            raise ValueError("positions and rot must be at least 1 and 2")
+        out = torch.empty((positions, rot), dtype=torch.float32, device="cuda" if device is None else device)
+    _out_tensor(out, torch.float32, (positions, rot), "table")
+    with _on(out):
+        st = _lib.load().awq_rope_table(positions, rot, base, _ROPE[scaling], factor, low, high, trained,
+                                        _ptr(out), _stream())
+    _lib.check("awq_rope_table", st)
+    return out
+
+
+def kv8_cache(pages, hkv, d, page=64, device="cuda"):
+    """An empty 8-bit cache: (k_cache float8_e4m3fn [pages, hkv, page, d], v_cache
+    float8_e4m3fn [pages, hkv, d, page], k_scale and v_scale fp32 [pages, hkv]).
+    Nothing needs to be cleared: the append sets the scale of every page it
+    begins, and the attention reads no slot behind a sequence's end."""
+    torch = _torch()
+    f8 = torch.float8_e4m3fn
+    return (torch.empty((pages, hkv, page, d), dtype=f8, device=device),
+            torch.empty((pages, hkv, d, page), dtype=f8, device=device),
+            torch.empty((pages, hkv), dtype=torch.float32, device=device),
+            torch.empty((pages, hkv), dtype=torch.float32, device=device))
+
+
+class _on:
+    """Makes a tensor's device the current one where it is not."""
+    __slots__ = ("dev", "ctx")
+
+    def __init__(self, t):
+        self.dev = t.device.index
+        self.ctx = None
+
+    def __enter__(self):
+        cuda = _torch().cuda
+        if cuda.current_device() != self.dev:
+            self.ctx = cuda.device(self.dev)
+            self.ctx.__enter__()
+
+    def __exit__(self, *e):
+        if self.ctx is not None:
+            self.ctx.__exit__(*e)
+
+
+def _kv8(k_cache, v_cache, k_scale, v_scale, block_table, ctx, cu_q):
+    """The C struct of a cache and a batch, its tensors checked."""
+    torch = _torch()
+    f8, f32, i32 = torch.float8_e4m3fn, torch.float32, torch.int32
+    _dev_tensor(k_cache, f8, "k_cache", 4)
+    _dev_tensor(v_cache, f8, "v_cache", 4)
+    pages, hkv, page, d = k_cache.shape
+    if v_cache.shape != (pages, hkv, d, page):
+        raise ValueError(f"v_cache must have shape {(pages, hkv, d, page)} (got {tuple(v_cache.shape)})")
+    _out_tensor(k_scale, f32, (pages, hkv), "k_scale")
+    _out_tensor(v_scale, f32, (pages, hkv), "v_scale")
+    _dev_tensor(block_table, i32, "block_table", 2)
+    b, max_pages = block_table.shape
+    _out_tensor(ctx, i32, (b,), "ctx")
+    dev = k_cache.device
+    for t, name in ((v_cache, "v_cache"), (k_scale, "k_scale"), (v_scale, "v_scale"),
+                    (block_table, "block_table"), (ctx, "ctx")):
+        if t.device != dev:
+            raise ValueError(f"{name} must be on {dev} (got {t.device})")
+    cu = None
+    if cu_q is not None:
+        _out_tensor(cu_q, i32, (b + 1,), "cu_q")
+        if cu_q.device != dev:
+            raise ValueError(f"cu_q must be on {dev} (got {cu_q.device})")
+        cu = cu_q.data_ptr()
+    return _lib.Kv8Cache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                         block_table.data_ptr(), cu, ctx.data_ptr(), pages, max_pages, b, page, hkv, d)
+
+
+def _rows(t, dtype, name, heads, d, rows, dev):
+    """A [rows, heads, d] tensor whose heads and channels are packed; its row stride."""
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev} (got {t.device})")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads) \
+            or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} must have shape ({'rows' if rows is None else rows}, "
+                         f"{'heads' if heads is None else heads}, {d}) (got {tuple(t.shape)})")
+    stride, h, c = t.stride()
+    if (c != 1 and d > 1) or (h != d and t.shape[1] > 1):
+        raise ValueError(f"{name} must have packed heads (strides {t.stride()})")
+    return stride if t.shape[0] > 1 else max(stride, t.shape[1] * d)
+
+
+def awq_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, ctx, cu_q=None, q=None, rope=None,
+                   interleaved=False, out=None):
+    """Rotates the new tokens' queries and keys, quantizes keys and values to
+    e4m3 with a scale per page and head, and appends them to the paged cache
+    (layout: ``kv8_cache``).
+
+    k, v: fp16 [rows, hkv, d]; q: fp16 [rows, hq, d] or None; rows may lie apart
+    (slices of one stacked projection).  block_table int32 [b, max_pages]; ctx
+    int32 [b]: every sequence's tokens, the new ones among them; cu_q int32
+    [b + 1]: the rows of each sequence (None: one row each).  rope: the table of
+    awq_rope_table (None: no rotation).  The cache is updated in place; returns
+    the rotated queries (in ``out`` when given, which may be q), None without q."""
+    return _kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, ctx, cu_q, q, rope, interleaved,
+                       out, False)
+
+
+def awq_kv8_append_bf16(k, v, k_cache, v_cache, k_scale, v_scale, block_table, ctx, cu_q=None, q=None, rope=None,
+                        interleaved=False, out=None):
+    """awq_kv8_append with bf16 q, k and v."""
+    return _kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, ctx, cu_q, q, rope, interleaved,
+                       out, True)
+
+
+def _kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, ctx, cu_q, q, rope, interleaved, out, bf):
+    torch = _torch()
+    dt = torch.bfloat16 if bf else torch.float16
+    c = _kv8(k_cache, v_cache, k_scale, v_scale, block_table, ctx, cu_q)
+    dev = k_cache.device
+    ks = _rows(k, dt, "k", c.hkv, c.d, None, dev)
+    rows = k.shape[0]
+    vs = _rows(v, dt, "v", c.hkv, c.d, rows, dev)
+    if cu_q is None and rows < c.b:
+        raise ValueError("without cu_q there must be a row for every sequence")
+    hq = qs = os = 0
+    if q is not None:
+        qs = _rows(q, dt, "q", None, c.d, rows, dev)
+        hq = q.shape[1]
+        if out is None:
+            out = torch.empty((rows, hq, c.d), dtype=dt, device=dev)
+        os = _rows(out, dt, "out", hq, c.d, rows, dev)
+    elif out is not None:
+        raise ValueError("out without q")
+    positions = rot = 0
+    if rope is not None:
+        _dev_tensor(rope, torch.float32, "rope", 2)
+        if rope.device != dev:
+            raise ValueError(f"rope must be on {dev} (got {rope.device})")
+        positions, rot = rope.shape
+    fn = "awq_kv8_append_bf16" if bf else "awq_kv8_append"
+    with _on(k_cache):
+        st = getattr(_lib.load(), fn)(_lib.byref(c), rows, _ptr(q), qs, hq, k.data_ptr(), ks, v.data_ptr(), vs,
+                                      _ptr(rope), positions, rot, 1 if interleaved else 0, _ptr(out), os, _stream())
+    _lib.check(fn, st)
+    return out
+
+
+def awq_attn_kv8_workspace_size(b, rows, hq, hkv, d, page, max_pages, max_q=1):
+    """Device scratch bytes of awq_attn_kv8 (0 where no context can be split)."""
+    return int(_lib.load().awq_attn_kv8_workspace_size(b, rows, hq, hkv, d, page, max_pages, max_q))
+
+
+def awq_attn_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx, cu_q=None, max_q=None, scale=None,
+                 out=None, lse=None, workspace=None):
+    """Causal attention of the new tokens over the 8-bit paged cache (append them
+    first): q fp16 [rows, hq, d] -> out fp16 [rows, hq, d].
+
+    block_table, ctx and cu_q as in awq_kv8_append.  max_q: the most rows of one
+    sequence as far as the caller knows (default: 1 without cu_q, else all
+    rows); it chooses between kernels and never changes what is computed.
+    scale: softmax scale (default d ** -0.5).  lse: fp32 [rows, hq] to fill with
+    the logarithms of the softmax denominators, or None."""
+    return _attn_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx, cu_q, max_q, scale, out, lse,
+                     workspace, False)
+
+
+def awq_attn_kv8_bf16(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx, cu_q=None, max_q=None, scale=None,
+                      out=None, lse=None, workspace=None):
+    """awq_attn_kv8 with bf16 q and out."""
+    return _attn_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx, cu_q, max_q, scale, out, lse,
+                     workspace, True)
+
+
+def _attn_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx, cu_q, max_q, scale, out, lse, workspace,
+              bf):
+    torch = _torch()
+    dt = torch.bfloat16 if bf else torch.float16
+    c = _kv8(k_cache, v_cache, k_scale, v_scale, block_table, ctx, cu_q)
+    dev = k_cache.device
+    qs = _rows(q, dt, "q", None, c.d, None, dev)
+    rows, hq = q.shape[0], q.shape[1]
+    if cu_q is None and rows < c.b:
+        raise ValueError("without cu_q there must be a row for every sequence")
+    if max_q is None:
+        max_q = 1 if cu_q is None else max(rows, 1)
+    if out is None:
+        out = torch.empty((rows, hq, c.d), dtype=dt, device=dev)
+    os = _rows(out, dt, "out", hq, c.d, rows, dev)
+    if lse is not None:
+        _out_tensor(lse, torch.float32, (rows, hq), "lse")
+        if lse.device != dev:
+            raise ValueError(f"lse must be on {dev} (got {lse.device})")
+    fn = "awq_attn_kv8_bf16" if bf else "awq_attn_kv8"
+    with _on(k_cache):
+        wp, wb = _workspace(awq_attn_kv8_workspace_size(c.b, rows, hq, c.hkv, c.d, c.page, c.max_pages, max_q),
+                            dev, workspace)
+        st = getattr(_lib.load(), fn)(_lib.byref(c), rows, max_q, q.data_ptr(), qs, hq,
+                                      c.d ** -0.5 if scale is None else scale, out.data_ptr(), os, _ptr(lse), wp,
+                                      wb, _stream())
+    _lib.check(fn, st)
+    return out

@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes as C
 import pathlib
+from ctypes import byref  # noqa: F401
 
 LIB_PATH = pathlib.Path(__file__).resolve().parent / "libawq_mi355x.so"
 
@@ -74,6 +75,28 @@ SIGNATURES["awq_linear_w4a16_group_bf16"] = SIGNATURES["awq_linear_w4a16_group"]
 SIGNATURES["awq_linear_noalloc_scratch_bytes"] = (C.c_size_t, [])
 SIGNATURES["awq_linear_w4a16_group_noalloc"] = (C.c_int, [C.c_void_p, C.c_int32, C.c_int64, C.c_int64,
                                                           C.c_int32, C.c_void_p])
+
+
+class Kv8Cache(C.Structure):
+    """awq_kv8_cache of the C header."""
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("block_table", C.c_void_p), ("cu_q", C.c_void_p), ("ctx", C.c_void_p),
+                ("pages", C.c_int64), ("max_pages", C.c_int64), ("b", C.c_int64),
+                ("page", C.c_int32), ("hkv", C.c_int32), ("d", C.c_int32)]
+
+
+SIGNATURES["awq_rope_table"] = (C.c_int, [C.c_int64, C.c_int32, C.c_double, C.c_int32, C.c_double, C.c_double,
+                                          C.c_double, C.c_double, C.c_void_p, C.c_void_p])
+SIGNATURES["awq_kv8_append"] = (C.c_int, [C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int32, C.c_void_p,
+                                          C.c_int64, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int32,
+                                          C.c_int32, C.c_void_p, C.c_int64, C.c_void_p])
+SIGNATURES["awq_kv8_append_bf16"] = SIGNATURES["awq_kv8_append"]
+SIGNATURES["awq_attn_kv8_workspace_size"] = (C.c_size_t, [C.c_int64, C.c_int64, C.c_int32, C.c_int32, C.c_int32,
+                                                          C.c_int32, C.c_int64, C.c_int64])
+SIGNATURES["awq_attn_kv8"] = (C.c_int, [C.c_void_p, C.c_int64, C.c_int64, C.c_void_p, C.c_int64, C.c_int32,
+                                        C.c_float, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_size_t,
+                                        C.c_void_p])
+SIGNATURES["awq_attn_kv8_bf16"] = SIGNATURES["awq_attn_kv8"]
 
 _lib = None
 

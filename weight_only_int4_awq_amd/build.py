@@ -19,7 +19,8 @@ ROOT = PKG.parent
 CSRC = PKG / "csrc"
 BUILD = ROOT / "_build"
 LIB = PKG / "libawq_mi355x.so"
-SOURCES = ("api.hip", "calib_stats.hip", "search.hip", "pack.hip", "linear.hip", "linear_wbit.hip", "mixed.hip")
+SOURCES = ("api.hip", "calib_stats.hip", "search.hip", "pack.hip", "linear.hip", "linear_wbit.hip", "mixed.hip",
+           "kv8_append.hip", "attn_kv8.hip")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17", "-ffp-contract=off",

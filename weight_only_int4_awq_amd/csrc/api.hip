@@ -532,4 +532,188 @@ awq_status awq_linear_w4a16_group_noalloc(const awq_linear_item* items, int32_t 
   return AWQ_OK;
 }
 
+// ---------------------------------------------------------------- 8-bit paged KV cache
+
+awq_status awq_rope_table(int64_t positions, int32_t rot, double base, int32_t scaling, double factor,
+                          double low, double high, double trained, float* table, void* stream) {
+  g_err[0] = 0;
+  if (!table) return fail(AWQ_ERR_NULL, "awq_rope_table: null pointer");
+  if (positions < 1 || positions > 0x7FFFFFFF)
+    return fail(AWQ_ERR_SHAPE, "awq_rope_table: positions=%lld outside 1..2^31-1", positions);
+  if (rot < 2 || rot > 256 || rot % 2) return fail(AWQ_ERR_SHAPE, "awq_rope_table: rot=%lld not even in 2..256", rot);
+  if (!(base > 1.0) || !(base < 1e30)) return fail(AWQ_ERR_SHAPE, "awq_rope_table: base must be above 1 and finite");
+  if (scaling < AWQ_ROPE_NONE || scaling > AWQ_ROPE_YARN)
+    return fail(AWQ_ERR_SHAPE, "awq_rope_table: scaling=%lld not in 0..3", scaling);
+  if (scaling != AWQ_ROPE_NONE && (!(factor > 0.0) || !(factor < 1e30)))
+    return fail(AWQ_ERR_SHAPE, "awq_rope_table: factor must be positive and finite");
+  if (scaling >= AWQ_ROPE_BANDS &&
+      (!(low > 0.0) || !(high > low) || !(high < 1e30) || !(trained > 0.0) || !(trained < 1e30)))
+    return fail(AWQ_ERR_SHAPE, "awq_rope_table: needs 0 < low < high and trained > 0, finite");
+  if (!aligned(table, 4)) return fail(AWQ_ERR_ALIGN, "awq_rope_table: table must be 4-byte aligned");
+  const awq::RopeScaling sc = {scaling, factor, low, high, trained};
+  hipError_t e = awq::launch_rope_table(positions, rot, base, sc, table, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "awq_rope_table launch");
+  return AWQ_OK;
+}
+
+// Checks shared by the append and the attention; fills `a`.
+static awq_status kv8_args(const char* fn, const awq_kv8_cache* c, int64_t rows, awq::Kv8Args* a) {
+  char msg[128];
+  auto err = [&](awq_status st, const char* what, long long x = 0, long long y = 0) {
+    snprintf(msg, sizeof(msg), "%s: %s", fn, what);
+    return fail(st, msg, x, y);
+  };
+  if (!c) return err(AWQ_ERR_NULL, "null cache");
+  if (c->page != 64 && c->page != 128 && c->page != 256)
+    return err(AWQ_ERR_SHAPE, "page=%lld not in {64,128,256}", c->page);
+  if (c->d != 64 && c->d != 128) return err(AWQ_ERR_SHAPE, "d=%lld not in {64,128}", c->d);
+  if (c->hkv < 1 || c->hkv > 1024) return err(AWQ_ERR_SHAPE, "hkv=%lld outside 1..1024", c->hkv);
+  if (c->pages < 1 || c->pages > 0x7FFFFFFF) return err(AWQ_ERR_SHAPE, "pages=%lld outside 1..2^31-1", c->pages);
+  if (c->max_pages < 0 || c->max_pages > 0x7FFFFFFF / c->page)
+    return err(AWQ_ERR_SHAPE, "max_pages=%lld out of range", c->max_pages);
+  if (c->b < 0 || c->b > 65536) return err(AWQ_ERR_SHAPE, "b=%lld outside 0..65536", c->b);
+  if (rows < 0 || rows > (1 << 24)) return err(AWQ_ERR_SHAPE, "rows=%lld outside 0..2^24", rows);
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale) return err(AWQ_ERR_NULL, "null pointer");
+  if (c->b > 0 && (!c->ctx || (c->max_pages > 0 && !c->block_table))) return err(AWQ_ERR_NULL, "null pointer");
+  if (!aligned(c->k, 16) || !aligned(c->v, 16)) return err(AWQ_ERR_ALIGN, "k and v must be 16-byte aligned");
+  if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) || !aligned(c->block_table, 4) ||
+      !aligned(c->cu_q, 4) || !aligned(c->ctx, 4))
+    return err(AWQ_ERR_ALIGN, "scales, block_table, cu_q and ctx must be 4-byte aligned");
+  *a = awq::Kv8Args{c->k, c->v, c->k_scale, c->v_scale, c->block_table, c->cu_q, c->ctx,
+                    c->pages, c->max_pages, c->b, rows, c->page, c->hkv, c->d};
+  return AWQ_OK;
+}
+
+// A [rows][heads][d] 16-bit tensor whose rows are `stride` elements apart.
+static awq_status kv8_rows(const char* fn, const char* name, const void* p, int64_t stride, int64_t heads,
+                           int32_t d) {
+  char msg[128];
+  auto err = [&](awq_status st, const char* what) {
+    snprintf(msg, sizeof(msg), "%s: %s %s", fn, name, what);
+    return fail(st, msg);
+  };
+  if (!p) return err(AWQ_ERR_NULL, "is a null pointer");
+  if (stride < heads * d || stride > (1ll << 31)) return err(AWQ_ERR_SHAPE, "has rows that overlap or lie too far apart");
+  if (stride % 8 || !aligned(p, 16)) return err(AWQ_ERR_ALIGN, "must have 16-byte aligned rows");
+  return AWQ_OK;
+}
+
+static awq_status kv8_heads(const char* fn, int32_t hq, int32_t hkv, int64_t rows) {
+  char msg[128];
+  if (hq < 1 || hq > 65536 || hq % hkv) {
+    snprintf(msg, sizeof(msg), "%s: hq=%%lld not a positive multiple of hkv=%%lld", fn);
+    return fail(AWQ_ERR_SHAPE, msg, hq, hkv);
+  }
+  if (rows * hq > (1ll << 30)) {
+    snprintf(msg, sizeof(msg), "%s: rows * hq above 2^30", fn);
+    return fail(AWQ_ERR_SHAPE, msg);
+  }
+  return AWQ_OK;
+}
+
+static awq_status kv8_append_impl(const char* fn, const awq_kv8_cache* cache, int64_t rows, const uint16_t* q,
+                                  int64_t q_stride, int32_t hq, const uint16_t* k, int64_t k_stride,
+                                  const uint16_t* v, int64_t v_stride, const float* rope, int64_t positions,
+                                  int32_t rot, int32_t interleaved, uint16_t* q_out, int64_t q_out_stride,
+                                  bool bf, void* stream) {
+  g_err[0] = 0;
+  awq::Kv8Args a;
+  awq_status st = kv8_args(fn, cache, rows, &a);
+  if (st != AWQ_OK) return st;
+  char msg[128];
+  auto err = [&](awq_status s, const char* what, long long x = 0, long long y = 0) {
+    snprintf(msg, sizeof(msg), "%s: %s", fn, what);
+    return fail(s, msg, x, y);
+  };
+  if (rope) {
+    if (rot < 16 || rot > a.d || rot % 16) return err(AWQ_ERR_SHAPE, "rot=%lld not a multiple of 16 up to d=%lld", rot, a.d);
+    if (positions < 1 || positions > 0x7FFFFFFF) return err(AWQ_ERR_SHAPE, "positions=%lld outside 1..2^31-1", positions);
+    if (!aligned(rope, 16)) return err(AWQ_ERR_ALIGN, "rope must be 16-byte aligned");
+  }
+  if (rows > 0) {
+    if ((st = kv8_rows(fn, "k", k, k_stride, a.hkv, a.d)) != AWQ_OK) return st;
+    if ((st = kv8_rows(fn, "v", v, v_stride, a.hkv, a.d)) != AWQ_OK) return st;
+    if (q) {
+      if ((st = kv8_heads(fn, hq, a.hkv, rows)) != AWQ_OK) return st;
+      if ((st = kv8_rows(fn, "q", q, q_stride, hq, a.d)) != AWQ_OK) return st;
+      if ((st = kv8_rows(fn, "q_out", q_out, q_out_stride, hq, a.d)) != AWQ_OK) return st;
+    }
+  }
+  hipError_t e = awq::launch_kv8_append(a, q, q_stride, k, k_stride, v, v_stride, hq, rope, positions, rot,
+                                        interleaved != 0, bf, q_out, q_out_stride, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return AWQ_OK;
+}
+
+awq_status awq_kv8_append(const awq_kv8_cache* cache, int64_t rows, const uint16_t* q, int64_t q_stride,
+                          int32_t hq, const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                          const float* rope, int64_t positions, int32_t rot, int32_t interleaved,
+                          uint16_t* q_out, int64_t q_out_stride, void* stream) {
+  return kv8_append_impl("awq_kv8_append", cache, rows, q, q_stride, hq, k, k_stride, v, v_stride, rope,
+                         positions, rot, interleaved, q_out, q_out_stride, false, stream);
+}
+
+awq_status awq_kv8_append_bf16(const awq_kv8_cache* cache, int64_t rows, const uint16_t* q, int64_t q_stride,
+                               int32_t hq, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                               int64_t v_stride, const float* rope, int64_t positions, int32_t rot,
+                               int32_t interleaved, uint16_t* q_out, int64_t q_out_stride, void* stream) {
+  return kv8_append_impl("awq_kv8_append_bf16", cache, rows, q, q_stride, hq, k, k_stride, v, v_stride, rope,
+                         positions, rot, interleaved, q_out, q_out_stride, true, stream);
+}
+
+size_t awq_attn_kv8_workspace_size(int64_t b, int64_t rows, int32_t hq, int32_t hkv, int32_t d, int32_t page,
+                                   int64_t max_pages, int64_t max_q) {
+  if (b < 1 || b > 65536 || rows < 1 || rows > (1 << 24) || hkv < 1 || hkv > 1024 || hq < 1 || hq > 65536 ||
+      hq % hkv || rows * hq > (1ll << 30) || (d != 64 && d != 128) || (page != 64 && page != 128 && page != 256) ||
+      max_pages < 0 || max_pages > 0x7FFFFFFF / page || max_q < 1)
+    return 0;
+  return awq::attn_kv8_scratch_bytes(b, rows, hq, hkv, d, page, max_pages, max_q);
+}
+
+static awq_status attn_kv8_impl(const char* fn, const awq_kv8_cache* cache, int64_t rows, int64_t max_q,
+                                const uint16_t* q, int64_t q_stride, int32_t hq, float scale, uint16_t* out,
+                                int64_t out_stride, float* lse, void* workspace, size_t ws_bytes, bool bf,
+                                void* stream) {
+  g_err[0] = 0;
+  awq::Kv8Args a;
+  awq_status st = kv8_args(fn, cache, rows, &a);
+  if (st != AWQ_OK) return st;
+  char msg[128];
+  auto err = [&](awq_status s, const char* what, long long x = 0, long long y = 0) {
+    snprintf(msg, sizeof(msg), "%s: %s", fn, what);
+    return fail(s, msg, x, y);
+  };
+  if ((st = kv8_heads(fn, hq, a.hkv, rows)) != AWQ_OK) return st;
+  if (max_q < 1) return err(AWQ_ERR_SHAPE, "max_q=%lld < 1", max_q);
+  if (!(scale > 0.0f) || !(scale < 1e30f)) return err(AWQ_ERR_SHAPE, "scale must be positive and finite");
+  if (rows == 0 || a.b == 0) return AWQ_OK;
+  if ((st = kv8_rows(fn, "q", q, q_stride, hq, a.d)) != AWQ_OK) return st;
+  if ((st = kv8_rows(fn, "out", out, out_stride, hq, a.d)) != AWQ_OK) return st;
+  if (!aligned(lse, 4)) return err(AWQ_ERR_ALIGN, "lse must be 4-byte aligned");
+  const size_t need = awq::attn_kv8_scratch_bytes(a.b, rows, hq, a.hkv, a.d, a.page, a.max_pages, max_q);
+  if (need > 0) {
+    if (!workspace || ws_bytes < need)
+      return err(AWQ_ERR_WORKSPACE, "workspace of %lld bytes < %lld needed", (long long)ws_bytes, (long long)need);
+    if (!aligned(workspace, 256)) return err(AWQ_ERR_ALIGN, "workspace must be 256-byte aligned");
+  }
+  hipError_t e = awq::launch_attn_kv8(a, q, q_stride, hq, max_q, scale, bf, out, out_stride, lse, workspace,
+                                      (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return AWQ_OK;
+}
+
+awq_status awq_attn_kv8(const awq_kv8_cache* cache, int64_t rows, int64_t max_q, const uint16_t* q,
+                        int64_t q_stride, int32_t hq, float scale, uint16_t* out, int64_t out_stride, float* lse,
+                        void* workspace, size_t ws_bytes, void* stream) {
+  return attn_kv8_impl("awq_attn_kv8", cache, rows, max_q, q, q_stride, hq, scale, out, out_stride, lse,
+                       workspace, ws_bytes, false, stream);
+}
+
+awq_status awq_attn_kv8_bf16(const awq_kv8_cache* cache, int64_t rows, int64_t max_q, const uint16_t* q,
+                             int64_t q_stride, int32_t hq, float scale, uint16_t* out, int64_t out_stride,
+                             float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  return attn_kv8_impl("awq_attn_kv8_bf16", cache, rows, max_q, q, q_stride, hq, scale, out, out_stride, lse,
+                       workspace, ws_bytes, true, stream);
+}
+
 }  // extern "C"

@@ -108,4 +108,34 @@ hipError_t launch_linear_wbit(const uint16_t* x, const uint32_t* qweight, const 
                               int64_t n, int64_t k, int32_t g, int32_t w_bit, uint16_t* y,
                               void* scratch, hipStream_t stream);
 
+// The 8-bit paged KV cache (kv8_append.hip, attn_kv8.hip): the cache, its
+// batch and their sizes, validated by the caller.
+struct Kv8Args {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* block_table;
+  const int32_t* cu_q;
+  const int32_t* ctx;
+  int64_t pages, max_pages, b, rows;
+  int32_t page, hkv, d;
+};
+// rope scaling kinds of awq_rope_table
+struct RopeScaling {
+  int32_t kind;
+  double factor, low, high, trained;
+};
+hipError_t launch_rope_table(int64_t positions, int32_t rot, double base, const RopeScaling& sc,
+                             float* table, hipStream_t stream);
+hipError_t launch_kv8_append(const Kv8Args& a, const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                             int64_t k_stride, const uint16_t* v, int64_t v_stride, int32_t hq,
+                             const float* rope, int64_t positions, int32_t rot, bool interleaved,
+                             bool bf, uint16_t* q_out, int64_t q_out_stride, hipStream_t stream);
+size_t attn_kv8_scratch_bytes(int64_t b, int64_t rows, int32_t hq, int32_t hkv, int32_t d, int32_t page,
+                              int64_t max_pages, int64_t max_q);
+hipError_t launch_attn_kv8(const Kv8Args& a, const uint16_t* q, int64_t q_stride, int32_t hq,
+                           int64_t max_q, float scale, bool bf, uint16_t* out, int64_t out_stride,
+                           float* lse, void* scratch, hipStream_t stream);
+
 }  // namespace awq

@@ -1,0 +1,112 @@
+// Shared by the kernels of the 8-bit paged KV cache (kv8_append.hip,
+// attn_kv8.hip): the cache's description on the device, the batch's metadata,
+// and the conversions of e4m3 codes.
+//
+// Layout: page id `pid` of head h holds P tokens:
+//   k codes  kc[((pid * hkv + h) * P + slot) * D + d]     (channels contiguous)
+//   v codes  vc[((pid * hkv + h) * D + d) * P + slot]     (tokens contiguous)
+//   scales   ks[pid * hkv + h], vs[pid * hkv + h]
+// K rows feed the score product and V columns the output product straight from
+// global memory as MFMA operands: both products contract over the axis that is
+// contiguous in memory, so no transposition stands between the cache and the
+// matrix instruction.
+#pragma once
+
+#include "awq_common.h"
+
+namespace awq {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+
+struct Kv8View {
+  uint8_t* kc;
+  uint8_t* vc;
+  float* ks;
+  float* vs;
+  const int32_t* bt;       // [b][max_pages]
+  const int32_t* cu;       // [b + 1] or null: one row per sequence
+  const int32_t* ctx;      // [b]
+  int64_t pages;           // pages of the cache
+  int64_t rows;            // rows of q, k, v
+  int32_t max_pages, shift, hkv, b;   // page = 1 << shift
+};
+
+// Rows [r0, r0 + n) and tokens with them of sequence i.  Whatever the arrays
+// hold, r0 and n stay within the rows there are.
+struct SeqRows {
+  int32_t r0, n, ctx;
+};
+__device__ __forceinline__ SeqRows seq_rows(const Kv8View& v, int i) {
+  SeqRows s;
+  if (v.cu) {
+    const int rows = (int)v.rows;
+    int a = v.cu[i], z = v.cu[i + 1];
+    a = a < 0 ? 0 : (a > rows ? rows : a);
+    z = z < a ? a : (z > rows ? rows : z);
+    s.r0 = a;
+    s.n = z - a;
+  } else {
+    s.r0 = i;
+    s.n = i < v.rows ? 1 : 0;
+  }
+  const int c = v.ctx[i];
+  s.ctx = c < 0 ? 0 : c;
+  return s;
+}
+
+// Inclusive sum over the lanes of a wave.
+__device__ __forceinline__ int wave_scan(int x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int y = __shfl_up(x, o, 64);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// 8 e4m3 codes (two 32-bit words) as the MFMA operand type: exact in fp16 and
+// in bf16 (4 significant bits, |code| <= 448, least 2^-9); NaN codes stay NaN.
+template <bool BF>
+struct Mma;
+template <>
+struct Mma<false> {
+  typedef half8_t frag;
+  static __device__ __forceinline__ frag from_fp8(uint32_t lo, uint32_t hi) {
+    const half2_t a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
+    const half2_t b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
+    const half2_t c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
+    const half2_t d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+    return frag{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+  }
+  static __device__ __forceinline__ floatx4_t mma16(frag a, frag b, floatx4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ floatx16_t mma32(frag a, frag b, floatx16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+  }
+};
+template <>
+struct Mma<true> {
+  typedef bf16x8_t frag;
+  static __device__ __forceinline__ frag from_fp8(uint32_t lo, uint32_t hi) {
+    const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+    const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+    const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+    const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+    return frag{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+  }
+  static __device__ __forceinline__ floatx4_t mma16(frag a, frag b, floatx4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ floatx16_t mma32(frag a, frag b, floatx16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+};
+
+template <bool BF>
+__device__ __forceinline__ float act2f(uint16_t b) {
+  return BF ? bf2f(b) : h2f(b);
+}
+
+}  // namespace awq
