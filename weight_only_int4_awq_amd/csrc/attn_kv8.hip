@@ -327,6 +327,221 @@ __global__ __launch_bounds__(256, 2) void attn_kv8_cols_kernel(AttnP p) {
   }
 }
 
+// The state of one wave's 32 columns, and its steps st, st + stride, ... < st1:
+// MFMA 32x32x16, lane (c = l % 32, half = l / 32) holds column c and, of each
+// step's two 32-token tiles t, the tokens 32 t + 16 half .. + 15:
+//   score tile t, A row r = token 32 t + 16 (r / 4 % 2) + 4 (r / 8) + r % 4, so result i
+//                           of a half is token 32 t + 16 half + i;
+//   score k-step 2 x + e  = channels 32 x + 16 half + 8 e .. + 7;
+//   output k-step 2 t + e = tokens 32 t + 16 half + 8 e .. + 7.
+// The next step's keys are asked for as soon as this step's scores have used
+// theirs, and its values while those scores run, so a load has half a step to
+// arrive.
+template <int D, bool BF>
+struct Wave32 {
+  typedef Mma<BF> MQ;
+  typedef Mma<false> MV;
+  static constexpr int NX = D / 32, ND = D / 32;
+  typename MQ::frag qf[NX][2];
+  floatx16_t o[ND];
+  float m, l;
+
+  __device__ __forceinline__ void load_q(const uint16_t* qp, int half) {
+#pragma unroll
+    for (int x = 0; x < NX; ++x)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        qf[x][e] = __builtin_bit_cast(typename MQ::frag, *(const uint4*)(qp + 32 * x + 16 * half + 8 * e));
+  }
+
+  // pos: the last position this lane's column sees; first: the least of them in
+  // the wave (-1: some column sees nothing at all).
+  __device__ __forceinline__ void run(const Kv8View& v, float scale2, int h, int b, int ctx, bool over, int pos,
+                                      int first, int st, int st1, int stride, int lane) {
+    const int c = lane & 31, half = lane >> 5;
+    const int krow = 16 * (c >> 2 & 1) + 4 * (c >> 3) + (c & 3);
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
+    m = kNone;
+    l = 0.0f;
+    if (st >= st1) return;
+    const int32_t* bt = v.bt + (int64_t)b * v.max_pages;
+    const int smask = (1 << v.shift) - 1;
+    uint4 kr[2][NX], vr[ND][2];
+    float ks, vs;
+    bool bad;
+    const uint8_t* vp;
+    auto locate = [&](int s) {
+      const int t0 = s * kStep;
+      int pid = uniform(bt[t0 >> v.shift]);
+      bad = over || (uint32_t)pid >= (uint64_t)v.pages;
+      pid = bad ? 0 : pid;
+      const int64_t ph = (int64_t)pid * v.hkv + h;
+      const uint8_t* kp = v.kc + ((ph << v.shift) + (t0 & smask)) * D;
+      vp = v.vc + ((ph * D) << v.shift) + (t0 & smask);
+      ks = bad ? __builtin_nanf("") : v.ks[ph] * scale2;
+      vs = v.vs[ph];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int x = 0; x < NX; ++x) kr[t][x] = *(const uint4*)(kp + (32 * t + krow) * D + 32 * x + 16 * half);
+    };
+    locate(st);
+    for (; st < st1; st += stride) {
+      const int t0 = st * kStep;
+#pragma unroll
+      for (int i = 0; i < ND; ++i)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          vr[i][t] = *(const uint4*)(vp + ((32 * i + c) << v.shift) + 32 * t + 16 * half);
+      floatx16_t s[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) s[t][j] = 0.0f;
+#pragma unroll
+        for (int x = 0; x < NX; ++x) {
+          s[t] = MQ::mma32(MQ::from_fp8(kr[t][x].x, kr[t][x].y), qf[x][0], s[t]);
+          s[t] = MQ::mma32(MQ::from_fp8(kr[t][x].z, kr[t][x].w), qf[x][1], s[t]);
+        }
+      }
+      float a = ks, z = __builtin_amdgcn_logf(vs);
+      const float rv = 1.0f / vs;
+      const int held = bad ? 0 : ctx;
+      if (st + stride < st1) locate(st + stride);
+      if (t0 + kStep - 1 > first || held == 0) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            s[t][j] = t0 + 32 * t + 16 * half + j <= pos ? __builtin_fmaf(s[t][j], a, z) : -__builtin_inff();
+        a = 1.0f;
+        z = 0.0f;
+      }
+      float mx = s[0][0];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) mx = __builtin_fmaxf(mx, s[t][j]);
+      mx = __builtin_fmaf(mx, a, z);
+      if (__ballot(mx > m + kLazy)) {
+        mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32, 64));
+        const float mn = __builtin_fmaxf(m, mx);
+        const float f = __builtin_amdgcn_exp2f(m - mn);
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < ND; ++i) o[i] *= f;
+      }
+      z -= m;
+      float sum = 0.0f;
+      half8_t pf[4];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][j], a, z));
+          sum += e;
+          pf[2 * t + (j >> 3)][j & 7] = (half_t)e;
+        }
+      l = __builtin_fmaf(sum, rv, l);
+      // slots behind the sequence's end, and the page read in place of one that is
+      // not in the cache, may hold anything, NaN codes too: 0 * NaN
+      if (t0 + kStep > held) {
+#pragma unroll
+        for (int i = 0; i < ND; ++i)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            uint32_t* x = (uint32_t*)&vr[i][t];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int left = held - (t0 + 32 * t + 16 * half + 4 * j);
+              x[j] &= left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+            }
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < ND; ++i)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          o[i] = MV::mma32(MV::from_fp8(vr[i][t].x, vr[i][t].y), pf[2 * t], o[i]);
+          o[i] = MV::mma32(MV::from_fp8(vr[i][t].z, vr[i][t].w), pf[2 * t + 1], o[i]);
+        }
+    }
+    l += __shfl_xor(l, 32, 64);
+  }
+};
+
+// Tiles of 128 columns: each of the four waves has 32 of them and walks all of
+// the unit's steps.  The waves read the same pages within a short time of each
+// other, so all but the first of these reads come from the CU's own cache.
+template <int D, bool BF>
+__global__ __launch_bounds__(256, 2) void attn_kv8_tile_kernel(AttnP p) {
+  constexpr int TC = 128, ND = D / 32;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int h = blockIdx.x % p.v.hkv;
+  Unit w;
+  if (!find_unit<TC, false>(p, blockIdx.x / p.v.hkv, lane, w)) return;
+  const Kv8View& v = p.v;
+  const int b = uniform(w.b), S = uniform(w.S), sidx = uniform(w.s), tile = uniform(w.tile);
+  const int n = uniform(w.r.n), r0 = uniform(w.r.r0), ctx = uniform(w.r.ctx);
+  const int G = p.G, c0 = tile * TC + 32 * wave;
+  const int cols = n * G - c0 < 32 ? n * G - c0 : 32;
+  if (cols <= 0) return;
+  const int c = lane & 31, half = lane >> 5, col = c0 + c;
+  const int pos = c < cols ? ctx - n + col / G : -1;
+  const int first = cols < 32 ? -1 : ctx - n + c0 / G;
+  // the unit's share of the tile's steps; this wave stops at what its own rows see
+  const int tcols = n * G - tile * TC < TC ? n * G - tile * TC : TC;
+  const int last = ctx - n + (tile * TC + tcols - 1) / G, wlast = ctx - n + (c0 + cols - 1) / G;
+  const int cap = (int)(((int64_t)v.max_pages << v.shift) / kStep);
+  int steps = last < 0 ? 0 : last / kStep + 1, wsteps = wlast < 0 ? 0 : wlast / kStep + 1;
+  steps = steps < cap ? steps : cap;
+  const int st0 = (int)((int64_t)steps * sidx / S);
+  int st1 = (int)((int64_t)steps * (sidx + 1) / S);
+  st1 = st1 < wsteps ? st1 : wsteps;
+
+  Wave32<D, BF> a;
+  const int cc = c < cols ? col : c0;
+  a.load_q(p.q + (int64_t)(r0 + cc / G) * p.q_stride + (int64_t)(h * G + cc % G) * D, half);
+  a.run(v, p.scale2, h, b, ctx, ctx > (int64_t)v.max_pages << v.shift, pos, first, st0, st1, 1, lane);
+  if (c >= cols) return;
+  if (S == 1) {
+    const int row = r0 + col / G, head = h * G + col % G;
+    const float inv = a.l == 0.0f ? 0.0f : 1.0f / a.l;
+    uint16_t* op = p.out + row * p.out_stride + (int64_t)head * D + 4 * half;
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t x[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          x[e] = (uint32_t)f2act(a.o[i][4 * j + 2 * e] * inv, BF) |
+                 (uint32_t)f2act(a.o[i][4 * j + 2 * e + 1] * inv, BF) << 16;
+        *(uint2*)(op + 32 * i + 8 * j) = make_uint2(x[0], x[1]);
+      }
+    if (p.lse && half == 0)
+      p.lse[(int64_t)row * p.hq + head] =
+          a.l == 0.0f ? -__builtin_inff() : (a.m + __builtin_amdgcn_logf(a.l)) * kLn2;
+  } else {
+    const int64_t at = ((int64_t)w.slot * v.hkv + h) * TC + 32 * wave + c;
+    float* op = p.part + at * D + 4 * half;
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *(float4*)(op + 32 * i + 8 * j) =
+            make_float4(a.o[i][4 * j], a.o[i][4 * j + 1], a.o[i][4 * j + 2], a.o[i][4 * j + 3]);
+    if (half == 0) {
+      p.part_ml[2 * at] = a.m;
+      p.part_ml[2 * at + 1] = a.l;
+    }
+  }
+}
+
 // Joins the S partial results of every column of the split sequences: one wave
 // per column, the lanes' channels in the order of the units (a fixed order).
 template <int D, int TC, bool BF>
@@ -372,10 +587,11 @@ struct Plan {
   size_t off_ml, bytes;
 };
 
-Plan plan_of(int64_t b, int64_t rows, int32_t hq, int32_t hkv, int32_t d, int32_t page, int64_t max_pages) {
+Plan plan_of(int64_t b, int64_t rows, int32_t hq, int32_t hkv, int32_t d, int32_t page, int64_t max_pages,
+             int64_t max_q) {
   Plan p;
   const int64_t G = hq / hkv;
-  p.tc = 16;
+  p.tc = max_q * G > 64 ? 128 : 16;
   const int64_t by_rows = rows * ((G + p.tc - 1) / p.tc), by_cols = rows * G / p.tc + b;
   p.tiles = by_rows < by_cols ? by_rows : by_cols;
   const int64_t total = 512;
@@ -396,24 +612,27 @@ Plan plan_of(int64_t b, int64_t rows, int32_t hq, int32_t hkv, int32_t d, int32_
 
 size_t attn_kv8_scratch_bytes(int64_t b, int64_t rows, int32_t hq, int32_t hkv, int32_t d, int32_t page,
                               int64_t max_pages, int64_t max_q) {
-  (void)max_q;
-  return plan_of(b, rows, hq, hkv, d, page, max_pages).bytes;
+  return plan_of(b, rows, hq, hkv, d, page, max_pages, max_q).bytes;
 }
 
 template <int D, bool BF>
 static hipError_t launch(const AttnP& p, const Plan& pl, hipStream_t stream) {
-  attn_kv8_cols_kernel<D, BF><<<(unsigned)(pl.units * p.v.hkv), 256, 0, stream>>>(p);
-  if (pl.slots)
-    attn_kv8_join_kernel<D, 16, BF><<<(unsigned)(pl.tiles * p.v.hkv * 4), 256, 0, stream>>>(p);
+  const unsigned grid = (unsigned)(pl.units * p.v.hkv), joins = (unsigned)(pl.tiles * p.v.hkv * (pl.tc / 4));
+  if (pl.tc == 128) {
+    attn_kv8_tile_kernel<D, BF><<<grid, 256, 0, stream>>>(p);
+    if (pl.slots) attn_kv8_join_kernel<D, 128, BF><<<joins, 256, 0, stream>>>(p);
+  } else {
+    attn_kv8_cols_kernel<D, BF><<<grid, 256, 0, stream>>>(p);
+    if (pl.slots) attn_kv8_join_kernel<D, 16, BF><<<joins, 256, 0, stream>>>(p);
+  }
   return hipGetLastError();
 }
 
 hipError_t launch_attn_kv8(const Kv8Args& a, const uint16_t* q, int64_t q_stride, int32_t hq, int64_t max_q,
                            float scale, bool bf, uint16_t* out, int64_t out_stride, float* lse,
                            void* scratch, hipStream_t stream) {
-  (void)max_q;
   if (a.rows < 1 || a.b < 1) return hipSuccess;
-  const Plan pl = plan_of(a.b, a.rows, hq, a.hkv, a.d, a.page, a.max_pages);
+  const Plan pl = plan_of(a.b, a.rows, hq, a.hkv, a.d, a.page, a.max_pages, max_q);
   AttnP p;
   p.v = Kv8View{a.k, a.v, a.k_scale, a.v_scale, a.block_table, a.cu_q, a.ctx, a.pages, a.rows,
                 (int32_t)a.max_pages, __builtin_ctz((unsigned)a.page), a.hkv, (int32_t)a.b};
