@@ -40,10 +40,463 @@ struct AttnP {
   float scale2;                      // softmax scale * log2 e
   int32_t target;                    // units per head the plan aims at
   int32_t min_steps;                 // least steps of a unit
+  int32_t whole;                     // a context of so many steps is not split
   int32_t slots;                     // partial slots per head in the workspace
   float* part;                       // partial O [slot][hkv][TC][D], then their (m, l)
   float* part_ml;
 };
+
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// Results of one column's channels d .. d + 3: O / l, and the lse from channel 0.
+// No visible token: zeros and -inf (a NaN sum is kept).
+template <bool BF>
+__device__ __forceinline__ void store4(const AttnP& p, int row, int head, int D, int d, float4 a, float top,
+                                       float sum) {
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const uint32_t lo = (uint32_t)f2act(a.x * inv, BF) | (uint32_t)f2act(a.y * inv, BF) << 16;
+  const uint32_t hi = (uint32_t)f2act(a.z * inv, BF) | (uint32_t)f2act(a.w * inv, BF) << 16;
+  *(uint2*)(p.out + row * p.out_stride + (int64_t)head * D + d) = make_uint2(lo, hi);
+  if (p.lse && d == 0)
+    p.lse[(int64_t)row * p.hq + head] = sum == 0.0f ? -__builtin_inff() : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
+// The partial results of one tile: slots first, next, next + step, ...
+struct Parts {
+  int first, next, step, count, tile;
+  SeqRows r;
+};
+
+// 16 bytes of the cache.  ONCE: nothing else of the launch reads them, so they
+// are not kept in the caches (one sequence of 128 K tokens: 53.5 us against 58).
+template <bool ONCE>
+__device__ __forceinline__ uint4 load16(const uint8_t* p) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  if (ONCE) return __builtin_bit_cast(uint4, __builtin_nontemporal_load((const u32x4*)p));
+  return *(const uint4*)p;
+}
+
+// What a wave needs of the sequence whose columns it works on.
+struct Seq {
+  const int32_t* bt;       // its row of the block table
+  int ctx, pos, first;     // pos: the last position that this lane's column sees (-1: none);
+                           // first: the least pos of the wave's columns
+  bool over;               // longer than its row of the block table: NaN
+};
+
+// One wave's columns of one key/value head, a step at a time: keys and values go
+// from the cache to registers, with no LDS and no barrier.  ask(st) asks for a
+// step's keys; loop() runs the steps st, st + stride, ... < st1, the first of
+// them asked for.  The next step's keys are asked for as soon as the scores have
+// used this one's, and the values while the scores run.
+//
+// C = 16, MFMA 16x16x32: lane (c = l % 16, g = l / 16) holds column c and the 16 tokens
+// 16 g .. 16 g + 15 of a step:
+//   score tile t, A row r  = token 16 (r / 4) + 4 t + r % 4 (the rows of an MFMA may be
+//                            any tokens), so result i of group g is token 16 g + 4 t + i;
+//   score k-step 2 x + e   = channels 64 x + 16 g + 8 e .. + 7;
+//   output k-step e        = tokens 16 g + 8 e .. + 7.
+// C = 32, MFMA 32x32x16: lane (c = l % 32, g = l / 32) holds column c and, of each 32-token
+// tile t, the tokens 32 t + 16 g .. + 15:
+//   score tile t, A row r  = token 32 t + 16 (r / 4 % 2) + 4 (r / 8) + r % 4, so result i
+//                            of group g is token 32 t + 16 g + i;
+//   score k-step 2 x + e   = channels 32 x + 16 g + 8 e .. + 7;
+//   output k-step 2 t + e  = tokens 32 t + 16 g + 8 e .. + 7.
+// So every operand of the cache is a 16-byte load that feeds two MFMAs.
+template <int D, bool BF, int C, bool ONCE>
+struct Wave {
+  typedef Mma<BF> MQ;
+  typedef Mma<false> MV;
+  static constexpr bool W = C == 32;
+  static constexpr int GR = 64 / C;              // lane groups
+  static constexpr int NT = W ? 2 : 4;           // score tiles of a step
+  static constexpr int NJ = W ? 16 : 4;          // results of a lane in a tile
+  static constexpr int NX = D / (16 * GR);       // key loads of a tile
+  static constexpr int NV = W ? 2 : 1;           // value loads of C channels
+  static constexpr int ND = D / C;
+  typedef float acc_t __attribute__((ext_vector_type(W ? 16 : 4)));
+
+  typename MQ::frag qf[NX][2];
+  acc_t o[ND];
+  float m, l;
+  uint4 kr[NT][NX];
+  float ks, vs;
+  bool bad;
+  const uint8_t* vp;
+
+  static __device__ __forceinline__ acc_t mma_q(typename MQ::frag a, typename MQ::frag b, acc_t c) {
+    if constexpr (W) return MQ::mma32(a, b, c);
+    else return MQ::mma16(a, b, c);
+  }
+  static __device__ __forceinline__ acc_t mma_v(half8_t a, half8_t b, acc_t c) {
+    if constexpr (W) return MV::mma32(a, b, c);
+    else return MV::mma16(a, b, c);
+  }
+  // token of result j of score tile t in group g
+  static __device__ __forceinline__ int token(int t, int j, int g) { return W ? 32 * t + 16 * g + j : 16 * g + 4 * t + j; }
+  // channel of result j of output tile i in group g
+  static __device__ __forceinline__ int channel(int i, int j, int g) {
+    return W ? 32 * i + 8 * (j >> 2) + 4 * g + (j & 3) : 16 * i + 4 * g + j;
+  }
+
+  __device__ __forceinline__ void load_q(const uint16_t* qp, int lane) {
+    const int g = lane / C;
+#pragma unroll
+    for (int x = 0; x < NX; ++x)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        qf[x][e] = __builtin_bit_cast(typename MQ::frag, *(const uint4*)(qp + 16 * GR * x + 16 * g + 8 * e));
+  }
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) o[i][j] = 0.0f;
+    m = kNone;
+    l = 0.0f;
+  }
+
+  __device__ __forceinline__ void ask(const Kv8View& v, float scale2, const Seq& q, int h, int st, int lane) {
+    const int c = lane % C, g = lane / C, t0 = st * kStep;
+    const int krow = W ? 16 * (c >> 2 & 1) + 4 * (c >> 3) + (c & 3) : 16 * (c >> 2) + (c & 3);
+    int pid = uniform(q.bt[t0 >> v.shift]);
+    bad = q.over || (uint32_t)pid >= (uint64_t)v.pages;
+    pid = bad ? 0 : pid;
+    const int64_t ph = (int64_t)pid * v.hkv + h;
+    const int slot0 = t0 & ((1 << v.shift) - 1);
+    const uint8_t* kp = v.kc + ((ph << v.shift) + slot0) * D;
+    vp = v.vc + ((ph * D) << v.shift) + slot0;
+    ks = bad ? __builtin_nanf("") : v.ks[ph] * scale2;
+    vs = v.vs[ph];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int x = 0; x < NX; ++x)
+        kr[t][x] = load16<ONCE>(kp + ((W ? 32 : 4) * t + krow) * D + 16 * GR * x + 16 * g);
+  }
+
+  __device__ __forceinline__ void loop(const Kv8View& v, float scale2, const Seq& q, int h, int st, int st1,
+                                       int stride, int lane) {
+    const int c = lane % C, g = lane / C;
+    for (; st < st1; st += stride) {
+      const int t0 = st * kStep;
+      uint4 vr[ND][NV];
+#pragma unroll
+      for (int i = 0; i < ND; ++i)
+#pragma unroll
+        for (int t = 0; t < NV; ++t)
+          vr[i][t] = load16<ONCE>(vp + ((C * i + c) << v.shift) + 32 * t + 16 * g);
+      acc_t s[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) s[t][j] = 0.0f;
+#pragma unroll
+        for (int x = 0; x < NX; ++x) {
+          s[t] = mma_q(MQ::from_fp8(kr[t][x].x, kr[t][x].y), qf[x][0], s[t]);
+          s[t] = mma_q(MQ::from_fp8(kr[t][x].z, kr[t][x].w), qf[x][1], s[t]);
+        }
+      }
+      float a = ks, z = __builtin_amdgcn_logf(vs);
+      const float rv = 1.0f / vs;
+      const int held = bad ? 0 : q.ctx;
+      if (st + stride < st1) ask(v, scale2, q, h, st + stride, lane);
+      if (t0 + kStep - 1 > q.first || held == 0) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+            s[t][j] = t0 + token(t, j, g) <= q.pos ? __builtin_fmaf(s[t][j], a, z) : -__builtin_inff();
+        a = 1.0f;
+        z = 0.0f;
+      }
+      float mx = s[0][0];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) mx = __builtin_fmaxf(mx, s[t][j]);
+      mx = __builtin_fmaf(mx, a, z);
+      if (__ballot(mx > m + kLazy)) {
+#pragma unroll
+        for (int x = C; x < 64; x <<= 1) mx = __builtin_fmaxf(mx, __shfl_xor(mx, x, 64));
+        const float mn = __builtin_fmaxf(m, mx);
+        const float f = __builtin_amdgcn_exp2f(m - mn);
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < ND; ++i) o[i] *= f;
+      }
+      z -= m;
+      float sum = 0.0f;
+      half8_t pf[NT * NJ / 8];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][j], a, z));
+          sum += e;
+          pf[(t * NJ + j) / 8][(t * NJ + j) % 8] = (half_t)e;
+        }
+      l = __builtin_fmaf(sum, rv, l);
+      // slots behind the sequence's end, and the page read in place of one that is
+      // not in the cache, may hold anything, NaN codes too: 0 * NaN
+      if (t0 + kStep > held) {
+#pragma unroll
+        for (int i = 0; i < ND; ++i)
+#pragma unroll
+          for (int t = 0; t < NV; ++t) {
+            uint32_t* x = (uint32_t*)&vr[i][t];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int left = held - (t0 + 32 * t + 16 * g + 4 * j);
+              x[j] &= left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+            }
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < ND; ++i)
+#pragma unroll
+        for (int t = 0; t < NV; ++t) {
+          o[i] = mma_v(MV::from_fp8(vr[i][t].x, vr[i][t].y), pf[2 * t], o[i]);
+          o[i] = mma_v(MV::from_fp8(vr[i][t].z, vr[i][t].w), pf[2 * t + 1], o[i]);
+        }
+    }
+  }
+
+  // l over the lane groups
+  __device__ __forceinline__ void finish() {
+#pragma unroll
+    for (int x = C; x < 64; x <<= 1) l += __shfl_xor(l, x, 64);
+  }
+};
+
+// ---------------------------------------------------------------- few columns
+
+// The work of a head lies on a line: the tiles of C columns one after another, each
+// as long as its sequence has steps (at least one, so that rows that see nothing are
+// written too).  Work-group k of the head takes the stretch from start(k) to
+// start(k + 1): equal stretches whatever the lengths are, so all work-groups,
+// one on each CU, end together.  A stretch's ends move off a tile that is too
+// short to be worth sharing, and off a tile's last few steps.
+struct Line {
+  uint32_t per;            // length of a stretch
+  uint32_t all;            // length of the line
+};
+struct Place {             // a tile on the line
+  uint32_t at;             // its first step
+  int steps, b, tile;
+  SeqRows r;
+};
+
+template <int C>
+struct Stretch {
+  const AttnP& p;
+  const int lane, cap;
+  SeqRows r;               // of sequence i0 + lane, held for up to 64 sequences
+  int tiles, steps;
+  Line line;
+
+  __device__ __forceinline__ void load(int i) {
+    r = SeqRows{0, 0, 0};
+    tiles = steps = 0;
+    if (i < p.v.b) {
+      r = seq_rows(p.v, i);
+      tiles = (int)(((uint32_t)r.n * (uint32_t)p.G + C - 1) / C);      // rows * hq <= 2^30
+      steps = r.ctx / kStep + (r.ctx % kStep ? 1 : 0);
+      steps = steps < cap ? steps : cap;
+      steps = steps < 1 ? 1 : steps;
+    }
+  }
+
+  __device__ __forceinline__ Stretch(const AttnP& p, int lane)
+      : p(p), lane(lane), cap((int)(((int64_t)p.v.max_pages << p.v.shift) / kStep)) {
+    // below 2^31 for ascending cu (the host has seen to it)
+    uint32_t sum = 0;
+    for (int i0 = 0; i0 < p.v.b; i0 += 64) {
+      load(i0 + lane);
+      sum += (uint32_t)tiles * (uint32_t)steps;
+    }
+    line.all = __builtin_amdgcn_readlane(wave_scan((int)sum), 63);
+    const uint32_t per = (uint32_t)(((uint64_t)line.all + p.target - 1) / (uint32_t)p.target);
+    line.per = per > (uint32_t)p.min_steps ? per : p.min_steps;
+  }
+
+  // the tile that holds x < line.all
+  __device__ __forceinline__ Place place(uint32_t x) {
+    uint32_t before = 0;
+    Place w;
+    w.b = -1;
+    for (int i0 = 0; i0 < p.v.b; i0 += 64) {
+      if (p.v.b > 64) load(i0 + lane);
+      const uint32_t mine = (uint32_t)tiles * (uint32_t)steps;
+      const uint32_t incl = wave_scan((int)mine);
+      const uint32_t sum = __builtin_amdgcn_readlane((int)incl, 63);
+      if (x - before < sum) {
+        int l = __popcll(__ballot(incl <= x - before));
+        l = l < 63 ? l : 63;
+        before += __builtin_amdgcn_readlane((int)(incl - mine), l);
+        // always so for ascending cu; whatever else the array holds ends here
+        if (x - before >= (uint32_t)__builtin_amdgcn_readlane((int)mine, l)) return w;
+        w.b = i0 + l;
+        w.steps = __builtin_amdgcn_readlane(steps, l);
+        w.r.r0 = __builtin_amdgcn_readlane(r.r0, l);
+        w.r.n = __builtin_amdgcn_readlane(r.n, l);
+        w.r.ctx = __builtin_amdgcn_readlane(r.ctx, l);
+        w.tile = (int)((x - before) / (uint32_t)w.steps);
+        w.at = before + (uint32_t)w.tile * w.steps;
+        return w;
+      }
+      before += sum;
+    }
+    return w;
+  }
+
+  // where work-group k begins; with the tile that holds it where it is inside one
+  __device__ __forceinline__ uint32_t start(int k) {
+    const uint64_t x64 = (uint64_t)k * line.per;
+    if (k == 0 || x64 >= line.all) return k == 0 ? 0 : line.all;
+    const uint32_t x = (uint32_t)x64;
+    const Place w = place(x);
+    if (w.b < 0) return line.all;
+    const uint32_t in = x - w.at, left = w.steps - in;
+    if (in == 0) return x;
+    if (w.steps <= p.whole || left < 4) return w.at + w.steps;
+    return in < 4 ? w.at : x;
+  }
+};
+
+// Tiles of C columns; the NW waves of a work-group take a tile's steps in turn and
+// are joined in LDS at the tile's end, or at the stretch's: a tile that a stretch
+// covers only in part leaves its O, m and l in the workspace, in slot 2 k of work-group k
+// if the part begins the stretch, else in 2 k + 1.
+template <int D, bool BF, int C, bool ONCE>
+__global__ __launch_bounds__(512, 2) void attn_kv8_line_kernel(AttnP p) {
+  constexpr int NW = 8;
+  typedef Wave<D, BF, C, ONCE> E;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const Kv8View& v = p.v;
+  const int h = blockIdx.x % v.hkv, k = blockIdx.x / v.hkv, G = p.G;
+  Stretch<C> y(p, lane);
+  const uint32_t x0 = y.start(k), x1 = y.start(k + 1);
+  if (x0 >= x1) return;
+  const int64_t cap = (int64_t)v.max_pages << v.shift;
+  const int c = lane % C, g = lane / C;
+  __shared__ __attribute__((aligned(16))) float so[NW * C * (D + 4)];     // O [wave][column][channel]
+  __shared__ float sm[NW * C], sl[NW * C];
+
+  E e;
+  Seq q;
+  Place w = y.place(x0);
+  uint32_t x = x0;
+  int st, st1, cols;
+  // the tile's columns and this stretch's steps of it
+  auto begin = [&]() {
+    const int n = w.r.n, ctx = w.r.ctx, col = w.tile * C + c;
+    cols = n * G - w.tile * C < C ? n * G - w.tile * C : C;
+    q.bt = v.bt + (int64_t)w.b * v.max_pages;
+    q.ctx = ctx;
+    q.over = ctx > cap;
+    q.pos = c < cols ? ctx - n + col / G : -1;
+    q.first = cols < C ? -1 : ctx - n + (w.tile * C) / G;
+    const int held = ctx / kStep + (ctx % kStep ? 1 : 0), there = held < y.cap ? held : y.cap;
+    const uint32_t z = w.at + w.steps < x1 ? w.at + w.steps : x1;
+    st = (int)(x - w.at) + wave;
+    st1 = (int)(z - w.at) < there ? (int)(z - w.at) : there;
+    if (st < st1) e.ask(v, p.scale2, q, h, st, lane);
+    const int cc = c < cols ? col : w.tile * C;
+    e.load_q(p.q + (int64_t)(w.r.r0 + cc / G) * p.q_stride + (int64_t)(h * G + cc % G) * D, lane);
+  };
+  if (w.b < 0) return;
+  begin();
+  for (;;) {
+    e.clear();
+    e.loop(v, p.scale2, q, h, st, st1, NW, lane);
+    e.finish();
+    const Place done = w;
+    const int dcols = cols;
+    const uint32_t from = x;
+    x = w.at + w.steps;
+    if (c < cols) {
+#pragma unroll
+      for (int i = 0; i < E::ND; ++i)
+#pragma unroll
+        for (int j = 0; j < E::NJ; j += 4)
+          *(float4*)&so[(wave * C + c) * (D + 4) + E::channel(i, j, g)] =
+              make_float4(e.o[i][j], e.o[i][j + 1], e.o[i][j + 2], e.o[i][j + 3]);
+      if (g == 0) {
+        sm[wave * C + c] = e.m;
+        sl[wave * C + c] = e.l;
+      }
+    }
+    // the next tile's first keys and queries travel while this one's waves are joined
+    const bool more = x < x1 && x > from;
+    if (more) {
+      w = y.place(x);
+      if (w.b < 0) return;
+      begin();
+    }
+    __syncthreads();
+    const bool whole = from == done.at && x <= x1;
+    // a thread: 4 channels of one column
+    for (int it = threadIdx.x; it < dcols * (D / 4); it += 64 * NW) {
+      const int jc = it / (D / 4), d = it % (D / 4) * 4;
+      float top = kNone, sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) top = __builtin_fmaxf(top, sm[i * C + jc]);
+      float4 a = make_float4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        const float f = __builtin_amdgcn_exp2f(sm[i * C + jc] - top);
+        const float4 b = *(const float4*)&so[(i * C + jc) * (D + 4) + d];
+        sum = __builtin_fmaf(f, sl[i * C + jc], sum);
+        a.x = __builtin_fmaf(f, b.x, a.x);
+        a.y = __builtin_fmaf(f, b.y, a.y);
+        a.z = __builtin_fmaf(f, b.z, a.z);
+        a.w = __builtin_fmaf(f, b.w, a.w);
+      }
+      if (whole) {
+        const int col = done.tile * C + jc, row = done.r.r0 + col / G, head = h * G + col % G;
+        store4<BF>(p, row, head, D, d, a, top, sum);
+      } else {
+        const int64_t at = ((int64_t)(2 * k + (from == x0 ? 0 : 1)) * v.hkv + h) * C + jc;
+        *(float4*)(p.part + at * D + d) = a;
+        if (d == 0) {
+          p.part_ml[2 * at] = top;
+          p.part_ml[2 * at + 1] = sum;
+        }
+      }
+    }
+    if (!more) return;
+    __syncthreads();
+  }
+}
+
+// The parts of a tile that stretches share: start(k) lies inside it and start(k - 1)
+// does not.  Its parts are work-group k - 1's last and the first ones of k, k + 1, ...
+// that begin before its end.
+template <int C>
+__device__ __forceinline__ bool line_parts(const AttnP& p, int k, int lane, Parts& w) {
+  Stretch<C> y(p, lane);
+  const uint32_t x = y.start(k);
+  if (x >= y.line.all) return false;
+  const Place t = y.place(x);
+  if (t.b < 0 || x == t.at) return false;
+  const uint32_t before = y.start(k - 1);
+  if (before > t.at) return false;
+  const uint32_t end = t.at + t.steps;
+  int last = (int)((end - 1) / y.line.per);
+  if (y.start(last) >= end) --last;
+  w.first = 2 * (k - 1) + (before == t.at ? 0 : 1);
+  w.next = 2 * k;
+  w.step = 2;
+  w.count = last - k + 2;
+  w.tile = t.tile;
+  w.r = t.r;
+  return last < p.target;
+}
+
+// ---------------------------------------------------------------- many columns
 
 // The part of the work one work-group does: steps s of S of tile `tile` of
 // sequence `b`.
@@ -58,8 +511,9 @@ struct Unit {
 // Units of sequences with S > 1 have partial slots, numbered in the same
 // order; there are fewer than 2 * target of them, as S > 1 needs
 // steps > chunk and then ceil(steps / chunk) < 2 steps / chunk.
-// TILE_ONLY: unit numbers count tiles (the pass that joins partials).
-template <int TC, bool TILE_ONLY>
+// JOIN: u counts the tiles of the split sequences (fewer than target) instead.
+// Everything returned is the same in all lanes.
+template <int TC, bool JOIN>
 __device__ __forceinline__ bool find_unit(const AttnP& p, int u, int lane, Unit& w) {
   const Kv8View& v = p.v;
   const int cap = (int)(((int64_t)v.max_pages << v.shift) / kStep);
@@ -68,7 +522,7 @@ __device__ __forceinline__ bool find_unit(const AttnP& p, int u, int lane, Unit&
     tiles = steps = 0;
     if (i < v.b) {
       r = seq_rows(v, i);
-      tiles = (int)(((int64_t)r.n * p.G + TC - 1) / TC);
+      tiles = (int)(((uint32_t)r.n * (uint32_t)p.G + TC - 1) / TC);   // rows * hq <= 2^30
       steps = r.ctx / kStep + (r.ctx % kStep ? 1 : 0);
       steps = steps < cap ? steps : cap;
     }
@@ -80,399 +534,47 @@ __device__ __forceinline__ bool find_unit(const AttnP& p, int u, int lane, Unit&
     load(i0 + lane, r, tiles, steps);
     total += (uint64_t)tiles * steps;
   }
-  if (v.b > 1) {
-#pragma unroll
-    for (int o = 32; o; o >>= 1) total += __shfl_xor(total, o, 64);
-  } else {
-    total = __shfl(total, 0, 64);
-  }
-  const uint64_t per = (total + p.target - 1) / (uint64_t)p.target;
-  const int chunk = per > (uint64_t)p.min_steps ? (per < 0x40000000u ? (int)per : 0x40000000) : p.min_steps;
+  // below 2^51 for ascending cu: two sums of 32 bits
+  const uint32_t lo = __builtin_amdgcn_readlane(wave_scan((int)(total & 0x1FFFFFFu)), 63);
+  const uint32_t hi = __builtin_amdgcn_readlane(wave_scan((int)(total >> 25)), 63);
+  const double per = __builtin_ceil(((double)hi * 33554432.0 + (double)lo) / (double)p.target);
+  const int chunk = per > (double)p.min_steps ? (per < 1e9 ? (int)per : 1000000000) : p.min_steps;
+  auto units_of = [&](int steps) {
+    // a short context is not worth a second launch's work
+    const int S = steps <= p.whole ? 1 : (steps + chunk - 1) / chunk;
+    return S < 1 ? 1 : S;
+  };
   int before = 0, slots = 0;
   for (int i0 = 0; i0 < v.b; i0 += 64) {
     if (v.b > 64) load(i0 + lane, r, tiles, steps);
-    int S = (steps + chunk - 1) / chunk;
-    S = S < 1 ? 1 : S;
-    const int mine = TILE_ONLY ? tiles : tiles * S;
+    const int S = units_of(steps);
     const int held = S > 1 ? tiles * S : 0;
-    int incl = mine, hincl = held;
-    if (v.b > 1) {
-      incl = wave_scan(mine, lane);
-      hincl = wave_scan(held, lane);
-    }
-    const int all = v.b > 1 ? __shfl(incl, 63, 64) : __shfl(incl, 0, 64);
+    const int mine = JOIN ? (S > 1 ? tiles : 0) : tiles * S;
+    const int incl = wave_scan(mine), hincl = wave_scan(held);
+    const int all = __builtin_amdgcn_readlane(incl, 63);
     if (u - before < all) {
-      const uint64_t past = __ballot(incl <= u - before);
-      int l = v.b > 1 ? __popcll(past) : 0;
+      int l = __popcll(__ballot(incl <= u - before));
       l = l < 63 ? l : 63;
-      const int at = u - before - __shfl(incl - mine, l, 64);
+      const int at = u - before - __builtin_amdgcn_readlane(incl - mine, l);
       w.b = i0 + l;
-      w.S = __shfl(S, l, 64);
-      w.r.r0 = __shfl(r.r0, l, 64);
-      w.r.n = __shfl(r.n, l, 64);
-      w.r.ctx = __shfl(r.ctx, l, 64);
-      const int nt = __shfl(tiles, l, 64);
-      const int order = TILE_ONLY ? at : at / w.S;
-      w.s = TILE_ONLY ? 0 : at % w.S;
+      w.S = __builtin_amdgcn_readlane(S, l);
+      w.r.r0 = __builtin_amdgcn_readlane(r.r0, l);
+      w.r.n = __builtin_amdgcn_readlane(r.n, l);
+      w.r.ctx = __builtin_amdgcn_readlane(r.ctx, l);
+      const int nt = __builtin_amdgcn_readlane(tiles, l);
+      const int order = JOIN ? at : at / w.S;
+      w.s = JOIN ? 0 : at % w.S;
       w.tile = nt - 1 - order;               // later rows see more: the longest first
-      w.slot = slots + __shfl(hincl - held, l, 64) + order * w.S + w.s;
+      w.slot = slots + __builtin_amdgcn_readlane(hincl - held, l) + order * w.S + w.s;
       // always so for ascending cu; whatever else the array holds stays in bounds
-      const int top = w.S > 1 ? (TILE_ONLY ? w.slot + w.S : w.slot + 1) : 0;
+      const int top = w.S > 1 ? (JOIN ? w.slot + w.S : w.slot + 1) : 0;
       return w.tile >= 0 && w.tile < nt && w.slot >= 0 && top <= p.slots;
     }
     before += all;
-    slots += v.b > 1 ? __shfl(hincl, 63, 64) : 0;
+    slots += __builtin_amdgcn_readlane(hincl, 63);
   }
   return false;
 }
-
-__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
-
-// One 16-column tile, four waves taking steps in turn, each wave on its own
-// from cache to registers: no LDS and no barrier until the waves' results are
-// joined.  MFMA 16x16x32: lane (c = l % 16, g = l / 16) holds column c and the
-// 16 tokens 16 g .. 16 g + 15 of a step, so that its V operand is one 16-byte
-// load per 16 channels and its K operand two, one per 64 channels:
-//   score tile t, A row r   = token 16 (r / 4) + 4 t + r % 4 (the rows of an MFMA
-//                             may be any tokens), so result i of lane group g
-//                             is token 16 g + 4 t + i;
-//   score k-step 2 x + e    = channels 64 x + 16 g + 8 e .. + 7;
-//   output k-step e         = tokens 16 g + 8 e .. + 7.
-template <int D, bool BF>
-__global__ __launch_bounds__(256, 2) void attn_kv8_cols_kernel(AttnP p) {
-  typedef Mma<BF> MQ;
-  typedef Mma<false> MV;
-  constexpr int TC = 16, NX = D / 64, ND = D / 16;
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int h = blockIdx.x % p.v.hkv;
-  Unit w;
-  if (!find_unit<TC, false>(p, blockIdx.x / p.v.hkv, lane, w)) return;
-  const Kv8View& v = p.v;
-  const int b = uniform(w.b), S = uniform(w.S), sidx = uniform(w.s), tile = uniform(w.tile);
-  const int n = uniform(w.r.n), r0 = uniform(w.r.r0), ctx = uniform(w.r.ctx);
-  const int G = p.G, cols = n * G - tile * TC < TC ? n * G - tile * TC : TC;
-  const int c = lane & 15, g = lane >> 4;
-  const int col = tile * TC + c;
-  // position of this lane's column (-1: sees nothing); of the tile's first and last
-  const int pos = c < cols ? ctx - n + col / G : -1;
-  const int first = ctx - n + (tile * TC) / G, last = ctx - n + (tile * TC + cols - 1) / G;
-  const int64_t cap = (int64_t)v.max_pages << v.shift;
-  const bool over = ctx > cap;               // longer than its row of the block table: NaN
-  int steps = last < 0 ? 0 : last / kStep + 1;
-  if (steps > (int)(cap / kStep)) steps = (int)(cap / kStep);
-  const int st0 = (int)((int64_t)steps * sidx / S), st1 = (int)((int64_t)steps * (sidx + 1) / S);
-
-  typename MQ::frag qf[NX][2];
-  {
-    const int cc = c < cols ? col : tile * TC;
-    const uint16_t* qp = p.q + (int64_t)(r0 + cc / G) * p.q_stride + (int64_t)(h * G + cc % G) * D;
-#pragma unroll
-    for (int x = 0; x < NX; ++x)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        qf[x][e] = __builtin_bit_cast(typename MQ::frag, *(const uint4*)(qp + 64 * x + 16 * g + 8 * e));
-  }
-  floatx4_t o[ND];
-#pragma unroll
-  for (int i = 0; i < ND; ++i) o[i] = floatx4_t{0, 0, 0, 0};
-  float m = kNone, l = 0.0f;
-
-  const int krow = 16 * (c >> 2) + (c & 3);      // + 4 t
-  for (int st = st0 + wave; st < st1; st += 4) {
-    const int t0 = st * kStep;
-    int pid = uniform(v.bt[(int64_t)b * v.max_pages + (t0 >> v.shift)]);
-    const bool bad = over || (uint32_t)pid >= (uint64_t)v.pages;
-    pid = bad ? 0 : pid;
-    const int64_t ph = (int64_t)pid * v.hkv + h;
-    const int slot0 = t0 & ((1 << v.shift) - 1);
-    const uint8_t* kp = v.kc + ((ph << v.shift) + slot0) * D;
-    const uint8_t* vp = v.vc + ((ph * D) << v.shift) + slot0;
-    const float ks = bad ? __builtin_nanf("") : v.ks[ph] * p.scale2;
-    const float vs = v.vs[ph];
-    uint4 kr[4][NX], vr[ND];
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int x = 0; x < NX; ++x) kr[t][x] = *(const uint4*)(kp + (krow + 4 * t) * D + 64 * x + 16 * g);
-#pragma unroll
-    for (int i = 0; i < ND; ++i) vr[i] = *(const uint4*)(vp + ((16 * i + c) << v.shift) + 16 * g);
-
-    floatx4_t s[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      s[t] = floatx4_t{0, 0, 0, 0};
-#pragma unroll
-      for (int x = 0; x < NX; ++x) {
-        s[t] = MQ::mma16(MQ::from_fp8(kr[t][x].x, kr[t][x].y), qf[x][0], s[t]);
-        s[t] = MQ::mma16(MQ::from_fp8(kr[t][x].z, kr[t][x].w), qf[x][1], s[t]);
-      }
-    }
-    const float lv = __builtin_amdgcn_logf(vs), rv = 1.0f / vs;
-    const int tok = t0 + 16 * g;
-    float mx = -__builtin_inff();
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[t][i] = __builtin_fmaf(s[t][i], ks, lv);
-    if (t0 + kStep - 1 > first || cols < TC) {
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[t][i] = tok + 4 * t + i <= pos ? s[t][i] : -__builtin_inff();
-    }
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) mx = __builtin_fmaxf(mx, s[t][i]);
-    if (__ballot(mx > m + kLazy)) {
-      mx = __builtin_fmaxf(mx, __shfl_xor(mx, 16, 64));
-      mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32, 64));
-      const float mn = __builtin_fmaxf(m, mx);
-      const float f = __builtin_amdgcn_exp2f(m - mn);
-      m = mn;
-      l *= f;
-#pragma unroll
-      for (int i = 0; i < ND; ++i) o[i] *= f;
-    }
-    float sum = 0.0f;
-    half8_t pf[2];
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float e = __builtin_amdgcn_exp2f(s[t][i] - m);
-        sum += e;
-        pf[t >> 1][4 * (t & 1) + i] = (half_t)e;
-      }
-    l = __builtin_fmaf(sum, rv, l);
-    // slots behind the sequence's end, and the page read in place of one that is
-    // not in the cache, may hold anything, NaN codes too: 0 * NaN
-    const int held = bad ? 0 : ctx;
-    if (t0 + kStep > held) {
-#pragma unroll
-      for (int i = 0; i < ND; ++i) {
-        uint32_t* x = (uint32_t*)&vr[i];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int left = held - (tok + 4 * j);
-          x[j] &= left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < ND; ++i) {
-      o[i] = MV::mma16(MV::from_fp8(vr[i].x, vr[i].y), pf[0], o[i]);
-      o[i] = MV::mma16(MV::from_fp8(vr[i].z, vr[i].w), pf[1], o[i]);
-    }
-  }
-  l += __shfl_xor(l, 16, 64);
-  l += __shfl_xor(l, 32, 64);
-
-  // join the waves: O [wave][channel][column], m and l per column
-  __shared__ float so[4][D][TC + 1];
-  __shared__ float sm[4][TC], sl[4][TC];
-#pragma unroll
-  for (int i = 0; i < ND; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) so[wave][16 * i + 4 * g + j][c] = o[i][j];
-  if (g == 0) {
-    sm[wave][c] = m;
-    sl[wave][c] = l;
-  }
-  __syncthreads();
-  // thread: column t / 16, channels (t % 16) + 16 x
-  const int jc = threadIdx.x >> 4;
-  if (jc >= cols) return;
-  float top = kNone, sum = 0.0f, f[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, sm[i][jc]);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[i] = __builtin_amdgcn_exp2f(sm[i][jc] - top);
-    sum += f[i] * sl[i][jc];
-  }
-  const int d0 = threadIdx.x & 15;
-  const int jcol = tile * TC + jc;
-  if (S == 1) {
-    const int row = r0 + jcol / G, head = h * G + jcol % G;
-    // no visible token: zeros and lse = -inf (a NaN sum is kept)
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    uint16_t* op = p.out + row * p.out_stride + (int64_t)head * D;
-#pragma unroll
-    for (int i = 0; i < ND; ++i) {
-      const int d = d0 + 16 * i;
-      float a = 0.0f;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) a += f[x] * so[x][d][jc];
-      op[d] = f2act(a * inv, BF);
-    }
-    if (p.lse && d0 == 0)
-      p.lse[(int64_t)row * p.hq + head] =
-          sum == 0.0f ? -__builtin_inff() : (top + __builtin_amdgcn_logf(sum)) * kLn2;
-  } else {
-    const int64_t at = ((int64_t)w.slot * v.hkv + h) * TC + jc;
-    float* op = p.part + at * D;
-#pragma unroll
-    for (int i = 0; i < ND; ++i) {
-      const int d = d0 + 16 * i;
-      float a = 0.0f;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) a += f[x] * so[x][d][jc];
-      op[d] = a;
-    }
-    if (d0 == 0) {
-      p.part_ml[2 * at] = top;
-      p.part_ml[2 * at + 1] = sum;
-    }
-  }
-}
-
-// The state of one wave's 32 columns, and its steps st, st + stride, ... < st1:
-// MFMA 32x32x16, lane (c = l % 32, half = l / 32) holds column c and, of each
-// step's two 32-token tiles t, the tokens 32 t + 16 half .. + 15:
-//   score tile t, A row r = token 32 t + 16 (r / 4 % 2) + 4 (r / 8) + r % 4, so result i
-//                           of a half is token 32 t + 16 half + i;
-//   score k-step 2 x + e  = channels 32 x + 16 half + 8 e .. + 7;
-//   output k-step 2 t + e = tokens 32 t + 16 half + 8 e .. + 7.
-// The next step's keys are asked for as soon as this step's scores have used
-// theirs, and its values while those scores run, so a load has half a step to
-// arrive.
-template <int D, bool BF>
-struct Wave32 {
-  typedef Mma<BF> MQ;
-  typedef Mma<false> MV;
-  static constexpr int NX = D / 32, ND = D / 32;
-  typename MQ::frag qf[NX][2];
-  floatx16_t o[ND];
-  float m, l;
-
-  __device__ __forceinline__ void load_q(const uint16_t* qp, int half) {
-#pragma unroll
-    for (int x = 0; x < NX; ++x)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        qf[x][e] = __builtin_bit_cast(typename MQ::frag, *(const uint4*)(qp + 32 * x + 16 * half + 8 * e));
-  }
-
-  // pos: the last position this lane's column sees; first: the least of them in
-  // the wave (-1: some column sees nothing at all).
-  __device__ __forceinline__ void run(const Kv8View& v, float scale2, int h, int b, int ctx, bool over, int pos,
-                                      int first, int st, int st1, int stride, int lane) {
-    const int c = lane & 31, half = lane >> 5;
-    const int krow = 16 * (c >> 2 & 1) + 4 * (c >> 3) + (c & 3);
-#pragma unroll
-    for (int i = 0; i < ND; ++i)
-#pragma unroll
-      for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
-    m = kNone;
-    l = 0.0f;
-    if (st >= st1) return;
-    const int32_t* bt = v.bt + (int64_t)b * v.max_pages;
-    const int smask = (1 << v.shift) - 1;
-    uint4 kr[2][NX], vr[ND][2];
-    float ks, vs;
-    bool bad;
-    const uint8_t* vp;
-    auto locate = [&](int s) {
-      const int t0 = s * kStep;
-      int pid = uniform(bt[t0 >> v.shift]);
-      bad = over || (uint32_t)pid >= (uint64_t)v.pages;
-      pid = bad ? 0 : pid;
-      const int64_t ph = (int64_t)pid * v.hkv + h;
-      const uint8_t* kp = v.kc + ((ph << v.shift) + (t0 & smask)) * D;
-      vp = v.vc + ((ph * D) << v.shift) + (t0 & smask);
-      ks = bad ? __builtin_nanf("") : v.ks[ph] * scale2;
-      vs = v.vs[ph];
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int x = 0; x < NX; ++x) kr[t][x] = *(const uint4*)(kp + (32 * t + krow) * D + 32 * x + 16 * half);
-    };
-    locate(st);
-    for (; st < st1; st += stride) {
-      const int t0 = st * kStep;
-#pragma unroll
-      for (int i = 0; i < ND; ++i)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          vr[i][t] = *(const uint4*)(vp + ((32 * i + c) << v.shift) + 32 * t + 16 * half);
-      floatx16_t s[2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) s[t][j] = 0.0f;
-#pragma unroll
-        for (int x = 0; x < NX; ++x) {
-          s[t] = MQ::mma32(MQ::from_fp8(kr[t][x].x, kr[t][x].y), qf[x][0], s[t]);
-          s[t] = MQ::mma32(MQ::from_fp8(kr[t][x].z, kr[t][x].w), qf[x][1], s[t]);
-        }
-      }
-      float a = ks, z = __builtin_amdgcn_logf(vs);
-      const float rv = 1.0f / vs;
-      const int held = bad ? 0 : ctx;
-      if (st + stride < st1) locate(st + stride);
-      if (t0 + kStep - 1 > first || held == 0) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            s[t][j] = t0 + 32 * t + 16 * half + j <= pos ? __builtin_fmaf(s[t][j], a, z) : -__builtin_inff();
-        a = 1.0f;
-        z = 0.0f;
-      }
-      float mx = s[0][0];
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) mx = __builtin_fmaxf(mx, s[t][j]);
-      mx = __builtin_fmaf(mx, a, z);
-      if (__ballot(mx > m + kLazy)) {
-        mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32, 64));
-        const float mn = __builtin_fmaxf(m, mx);
-        const float f = __builtin_amdgcn_exp2f(m - mn);
-        m = mn;
-        l *= f;
-#pragma unroll
-        for (int i = 0; i < ND; ++i) o[i] *= f;
-      }
-      z -= m;
-      float sum = 0.0f;
-      half8_t pf[4];
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][j], a, z));
-          sum += e;
-          pf[2 * t + (j >> 3)][j & 7] = (half_t)e;
-        }
-      l = __builtin_fmaf(sum, rv, l);
-      // slots behind the sequence's end, and the page read in place of one that is
-      // not in the cache, may hold anything, NaN codes too: 0 * NaN
-      if (t0 + kStep > held) {
-#pragma unroll
-        for (int i = 0; i < ND; ++i)
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            uint32_t* x = (uint32_t*)&vr[i][t];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int left = held - (t0 + 32 * t + 16 * half + 4 * j);
-              x[j] &= left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
-            }
-          }
-      }
-#pragma unroll
-      for (int i = 0; i < ND; ++i)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          o[i] = MV::mma32(MV::from_fp8(vr[i][t].x, vr[i][t].y), pf[2 * t], o[i]);
-          o[i] = MV::mma32(MV::from_fp8(vr[i][t].z, vr[i][t].w), pf[2 * t + 1], o[i]);
-        }
-    }
-    l += __shfl_xor(l, 32, 64);
-  }
-};
 
 // Tiles of 128 columns: each of the four waves has 32 of them and walks all of
 // the unit's steps.  The waves read the same pages within a short time of each
@@ -485,8 +587,7 @@ __global__ __launch_bounds__(256, 2) void attn_kv8_tile_kernel(AttnP p) {
   Unit w;
   if (!find_unit<TC, false>(p, blockIdx.x / p.v.hkv, lane, w)) return;
   const Kv8View& v = p.v;
-  const int b = uniform(w.b), S = uniform(w.S), sidx = uniform(w.s), tile = uniform(w.tile);
-  const int n = uniform(w.r.n), r0 = uniform(w.r.r0), ctx = uniform(w.r.ctx);
+  const int b = w.b, S = w.S, sidx = w.s, tile = w.tile, n = w.r.n, r0 = w.r.r0, ctx = w.r.ctx;
   const int G = p.G, c0 = tile * TC + 32 * wave;
   const int cols = n * G - c0 < 32 ? n * G - c0 : 32;
   if (cols <= 0) return;
@@ -503,10 +604,14 @@ __global__ __launch_bounds__(256, 2) void attn_kv8_tile_kernel(AttnP p) {
   int st1 = (int)((int64_t)steps * (sidx + 1) / S);
   st1 = st1 < wsteps ? st1 : wsteps;
 
-  Wave32<D, BF> a;
+  Wave<D, BF, 32, false> a;
+  const Seq q = {v.bt + (int64_t)b * v.max_pages, ctx, pos, first, ctx > (int64_t)v.max_pages << v.shift};
+  if (st0 < st1) a.ask(v, p.scale2, q, h, st0, lane);
   const int cc = c < cols ? col : c0;
-  a.load_q(p.q + (int64_t)(r0 + cc / G) * p.q_stride + (int64_t)(h * G + cc % G) * D, half);
-  a.run(v, p.scale2, h, b, ctx, ctx > (int64_t)v.max_pages << v.shift, pos, first, st0, st1, 1, lane);
+  a.load_q(p.q + (int64_t)(r0 + cc / G) * p.q_stride + (int64_t)(h * G + cc % G) * D, lane);
+  a.clear();
+  a.loop(v, p.scale2, q, h, st0, st1, 1, lane);
+  a.finish();
   if (c >= cols) return;
   if (S == 1) {
     const int row = r0 + col / G, head = h * G + col % G;
@@ -542,66 +647,138 @@ __global__ __launch_bounds__(256, 2) void attn_kv8_tile_kernel(AttnP p) {
   }
 }
 
-// Joins the S partial results of every column of the split sequences: one wave
-// per column, the lanes' channels in the order of the units (a fixed order).
-template <int D, int TC, bool BF>
-__global__ __launch_bounds__(256) void attn_kv8_join_kernel(AttnP p) {
-  constexpr int V = D / 64;
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int part = blockIdx.x % (p.v.hkv * (TC / 4));
-  const int h = part % p.v.hkv, jc = (part / p.v.hkv) * 4 + wave;
-  Unit w;
-  if (!find_unit<TC, true>(p, blockIdx.x / (p.v.hkv * (TC / 4)), lane, w)) return;
-  const int S = uniform(w.S), G = p.G, col = uniform(w.tile) * TC + jc;
-  if (S == 1 || col >= uniform(w.r.n) * G) return;
-  const int64_t at0 = ((int64_t)uniform(w.slot) * p.v.hkv + h) * TC + jc, stride = (int64_t)p.v.hkv * TC;
-  float top = kNone;
-  for (int i = lane; i < S; i += 64) top = __builtin_fmaxf(top, p.part_ml[2 * (at0 + i * stride)]);
-#pragma unroll
-  for (int o = 32; o; o >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, o, 64));
-  float acc[V] = {}, sum = 0.0f;
-#pragma unroll 8
-  for (int i = 0; i < S; ++i) {
-    const int64_t at = at0 + i * stride;
-    const float f = __builtin_amdgcn_exp2f(p.part_ml[2 * at] - top);
-    sum = __builtin_fmaf(f, p.part_ml[2 * at + 1], sum);
-#pragma unroll
-    for (int x = 0; x < V; ++x) acc[x] = __builtin_fmaf(f, p.part[at * D + lane * V + x], acc[x]);
-  }
-  const int row = uniform(w.r.r0) + col / G, head = h * G + col % G;
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  uint16_t* op = p.out + row * p.out_stride + (int64_t)head * D + lane * V;
-#pragma unroll
-  for (int x = 0; x < V; ++x) op[x] = f2act(acc[x] * inv, BF);
-  if (p.lse && lane == 0)
-    p.lse[(int64_t)row * p.hq + head] =
-        sum == 0.0f ? -__builtin_inff() : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+template <int TC>
+__device__ __forceinline__ bool unit_parts(const AttnP& p, int u, int lane, Parts& w) {
+  Unit t;
+  if (!find_unit<TC, true>(p, u, lane, t)) return false;
+  w = Parts{t.slot, t.slot + 1, 1, t.S, t.tile, t.r};
+  return true;
 }
 
-// The host's side of the plan: what the device's plan cannot exceed.
+// Joins the partial results of a split tile's columns in the order of their
+// steps.  Work-group (tile, head, z of Z): a wave takes a column, or the four
+// waves a quarter of its parts each where there are many; two parts' rows of D
+// floats to a load (four for D = 64).
+template <int D, int TC, bool BF>
+__global__ __launch_bounds__(256) void attn_kv8_join_kernel(AttnP p, int Z) {
+  constexpr int LPR = D / 4, RPL = 64 / LPR;       // lanes per row, rows per load
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int hkv = p.v.hkv, h = blockIdx.x % hkv, z = blockIdx.x / hkv % Z;
+  Parts w;
+  if (!(TC == 128 ? unit_parts<TC>(p, blockIdx.x / hkv / Z, lane, w)
+                  : line_parts<TC == 128 ? 16 : TC>(p, blockIdx.x / hkv / Z + 1, lane, w)))
+    return;
+  const int S = w.count, G = p.G;
+  auto slot = [&](int i) { return ((int64_t)(i ? w.next + (i - 1) * w.step : w.first) * hkv + h) * TC; };
+  const int cols = w.r.n * G - w.tile * TC < TC ? w.r.n * G - w.tile * TC : TC;
+  const bool shared = S > 16;
+  const int per = shared ? (S + 3) / 4 : S, s0 = shared ? wave * per : 0;
+  const int s1 = s0 + per < S ? s0 + per : S;
+  __shared__ float so[4][D], sml[4][2];
+  const int rowl = lane / LPR, d0 = (lane % LPR) * 4;
+  for (int j0 = shared ? z : 4 * z; j0 < cols; j0 += shared ? Z : 4 * Z) {
+    const int jc = shared ? j0 : j0 + wave;
+    const bool mine = jc < cols;
+    float top = kNone, sum = 0.0f;
+    float4 acc = make_float4(0, 0, 0, 0);
+    if (mine) {
+      for (int i = s0 + lane; i < s1; i += 64) top = __builtin_fmaxf(top, p.part_ml[2 * (slot(i) + jc)]);
+#pragma unroll
+      for (int o = 32; o; o >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, o, 64));
+#pragma unroll 4
+      for (int i = s0 + rowl; i < s1; i += RPL) {
+        const int64_t at = slot(i) + jc;
+        const float f = __builtin_amdgcn_exp2f(p.part_ml[2 * at] - top);
+        const float4 x = *(const float4*)(p.part + at * D + d0);
+        sum = __builtin_fmaf(f, p.part_ml[2 * at + 1], sum);
+        acc.x = __builtin_fmaf(f, x.x, acc.x);
+        acc.y = __builtin_fmaf(f, x.y, acc.y);
+        acc.z = __builtin_fmaf(f, x.z, acc.z);
+        acc.w = __builtin_fmaf(f, x.w, acc.w);
+      }
+#pragma unroll
+      for (int o = LPR; o < 64; o <<= 1) {
+        sum += __shfl_xor(sum, o, 64);
+        acc.x += __shfl_xor(acc.x, o, 64);
+        acc.y += __shfl_xor(acc.y, o, 64);
+        acc.z += __shfl_xor(acc.z, o, 64);
+        acc.w += __shfl_xor(acc.w, o, 64);
+      }
+    }
+    if (shared) {
+      if (rowl == 0) *(float4*)&so[wave][d0] = acc;
+      if (lane == 0) {
+        sml[wave][0] = top;
+        sml[wave][1] = sum;
+      }
+      __syncthreads();
+      top = __builtin_fmaxf(__builtin_fmaxf(sml[0][0], sml[1][0]), __builtin_fmaxf(sml[2][0], sml[3][0]));
+      sum = 0.0f;
+      acc = make_float4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float f = __builtin_amdgcn_exp2f(sml[i][0] - top);
+        const float4 x = *(const float4*)&so[i][d0];
+        sum = __builtin_fmaf(f, sml[i][1], sum);
+        acc.x = __builtin_fmaf(f, x.x, acc.x);
+        acc.y = __builtin_fmaf(f, x.y, acc.y);
+        acc.z = __builtin_fmaf(f, x.z, acc.z);
+        acc.w = __builtin_fmaf(f, x.w, acc.w);
+      }
+      __syncthreads();
+    }
+    if (mine && rowl == 0 && (!shared || wave == 0)) {
+      const int col = w.tile * TC + jc, row = w.r.r0 + col / G, head = h * G + col % G;
+      store4<BF>(p, row, head, D, d0, acc, top, sum);
+    }
+  }
+}
+
+// The host's side of the plan: what the device's plans cannot exceed.
 struct Plan {
-  int tc, target, min_steps;
-  int64_t tiles;                     // tiles per head, at most
-  int64_t units;                     // units per head, at most
-  int64_t slots;                     // partial slots per head, at most (0: nothing is split)
+  int tc;                            // columns of a tile: 16 and 32 lie on a line, 128 in units
+  int target, min_steps, whole;
+  bool once;                         // a sequence has one tile: its cache is read once
+  int64_t groups;                    // work-groups per head
+  int64_t slots;                     // partial slots per head (0: nothing can be split)
+  int joins, z;                      // tiles per head to join, at most; work-groups for each
   size_t off_ml, bytes;
 };
 
 Plan plan_of(int64_t b, int64_t rows, int32_t hq, int32_t hkv, int32_t d, int32_t page, int64_t max_pages,
              int64_t max_q) {
   Plan p;
-  const int64_t G = hq / hkv;
-  p.tc = max_q * G > 64 ? 128 : 16;
-  const int64_t by_rows = rows * ((G + p.tc - 1) / p.tc), by_cols = rows * G / p.tc + b;
-  p.tiles = by_rows < by_cols ? by_rows : by_cols;
-  const int64_t total = 512;
-  p.target = (int)((total + hkv - 1) / hkv);
+  const int64_t G = hq / hkv, steps = max_pages * (page / kStep) > 1 ? max_pages * (page / kStep) : 1;
+  // 128-column tiles share what they read among four waves, and need 128 columns
+  // for it: up to 64 the eight waves of a work-group share the steps instead
+  p.tc = max_q > 64 || max_q * G > 64 ? 128 : max_q * G > 16 ? 32 : 16;
+  auto tiles_of = [&](int tc) {
+    const int64_t by_rows = rows * ((G + tc - 1) / tc), by_cols = rows * G / tc + b;
+    return by_rows < by_cols ? by_rows : by_cols;
+  };
+  if (p.tc < 128 && tiles_of(p.tc) * steps >= (1ll << 31)) p.tc = 128;    // the line is 32 bits long
+  const int64_t tiles = tiles_of(p.tc);
+  p.whole = 16;
   p.min_steps = 8;
-  const int64_t steps = max_pages * (page / kStep);
-  const int64_t most = (steps + p.min_steps - 1) / p.min_steps;       // units of one tile, at most
-  p.units = p.target + p.tiles;
-  if (most <= p.units / (p.tiles ? p.tiles : 1)) p.units = p.tiles * (most > 0 ? most : 1);
-  p.slots = most > 1 ? (2 * (int64_t)p.target < p.tiles * most ? 2 * (int64_t)p.target : p.tiles * most) : 0;
+  if (p.tc < 128) {
+    // one work-group of eight waves on each CU
+    p.target = hkv < 256 ? 256 / hkv : 1;
+    p.groups = p.target;
+    p.slots = steps > p.whole && p.target > 1 ? 2 * p.target : 0;
+    p.joins = p.target - 1;
+    p.z = (int)(max_q * G < 4 ? max_q * G : 4);
+  } else {
+    // units of causal tiles differ in length: four per CU even that out (prompt
+    // chunks: 249 us, 304 with two, 250 with eight)
+    p.target = hkv < 1024 ? 1024 / hkv : 1;
+    const int64_t most = steps <= p.whole ? 1 : (steps + p.min_steps - 1) / p.min_steps;
+    p.groups = p.target + tiles;
+    if (most <= p.groups / tiles) p.groups = tiles * most;
+    p.slots = most > 1 ? (2 * (int64_t)p.target < tiles * most ? 2 * (int64_t)p.target : tiles * most) : 0;
+    p.joins = (int)(tiles < p.slots / 2 ? tiles : p.slots / 2);
+    p.z = 4;
+  }
+  p.once = max_q * G <= p.tc;
   const size_t cols = (size_t)p.slots * hkv * p.tc;
   p.off_ml = cols * d * sizeof(float);
   p.bytes = (p.off_ml + cols * 2 * sizeof(float) + 255) / 256 * 256;
@@ -615,15 +792,23 @@ size_t attn_kv8_scratch_bytes(int64_t b, int64_t rows, int32_t hq, int32_t hkv, 
   return plan_of(b, rows, hq, hkv, d, page, max_pages, max_q).bytes;
 }
 
+template <int D, bool BF, int C>
+static void launch_line(const AttnP& p, const Plan& pl, unsigned grid, unsigned joins, hipStream_t stream) {
+  if (pl.once) attn_kv8_line_kernel<D, BF, C, true><<<grid, 512, 0, stream>>>(p);
+  else attn_kv8_line_kernel<D, BF, C, false><<<grid, 512, 0, stream>>>(p);
+  if (pl.slots) attn_kv8_join_kernel<D, C, BF><<<joins, 256, 0, stream>>>(p, pl.z);
+}
+
 template <int D, bool BF>
 static hipError_t launch(const AttnP& p, const Plan& pl, hipStream_t stream) {
-  const unsigned grid = (unsigned)(pl.units * p.v.hkv), joins = (unsigned)(pl.tiles * p.v.hkv * (pl.tc / 4));
-  if (pl.tc == 128) {
-    attn_kv8_tile_kernel<D, BF><<<grid, 256, 0, stream>>>(p);
-    if (pl.slots) attn_kv8_join_kernel<D, 128, BF><<<joins, 256, 0, stream>>>(p);
+  const unsigned grid = (unsigned)(pl.groups * p.v.hkv), joins = (unsigned)pl.joins * p.v.hkv * pl.z;
+  if (pl.tc == 16) {
+    launch_line<D, BF, 16>(p, pl, grid, joins, stream);
+  } else if (pl.tc == 32) {
+    launch_line<D, BF, 32>(p, pl, grid, joins, stream);
   } else {
-    attn_kv8_cols_kernel<D, BF><<<grid, 256, 0, stream>>>(p);
-    if (pl.slots) attn_kv8_join_kernel<D, 16, BF><<<joins, 256, 0, stream>>>(p);
+    attn_kv8_tile_kernel<D, BF><<<grid, 256, 0, stream>>>(p);
+    if (pl.slots) attn_kv8_join_kernel<D, 128, BF><<<joins, 256, 0, stream>>>(p, pl.z);
   }
   return hipGetLastError();
 }
@@ -646,6 +831,7 @@ hipError_t launch_attn_kv8(const Kv8Args& a, const uint16_t* q, int64_t q_stride
   p.scale2 = scale * kLog2e;
   p.target = pl.target;
   p.min_steps = pl.min_steps;
+  p.whole = pl.whole;
   p.slots = (int32_t)pl.slots;
   p.part = (float*)scratch;
   p.part_ml = (float*)((char*)scratch + pl.off_ml);
