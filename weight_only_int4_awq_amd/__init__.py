@@ -540,10 +540,8 @@ def awq_rope_table(positions, rot, base=10000.0, scaling="none", factor=1.0, low
             raise ValueError("positions and rot must be at least 1 and 2")
         out = torch.empty((positions, rot), dtype=torch.float32, device="cuda" if device is None else device)
     _out_tensor(out, torch.float32, (positions, rot), "table")
-    with _on(out):
-        st = _lib.load().awq_rope_table(positions, rot, base, _ROPE[scaling], factor, low, high, trained,
-                                        _ptr(out), _stream())
-    _lib.check("awq_rope_table", st)
+    _call("awq_rope_table", out.get_device(), positions, rot, base, _ROPE[scaling], factor, low, high, trained,
+          out.data_ptr())
     return out
 
 
@@ -560,70 +558,80 @@ def kv8_cache(pages, hkv, d, page=64, device="cuda"):
             torch.empty((pages, hkv), dtype=torch.float32, device=device))
 
 
-class _on:
-    """Makes a tensor's device the current one where it is not."""
-    __slots__ = ("dev", "ctx")
-
-    def __init__(self, t):
-        self.dev = t.device.index
-        self.ctx = None
-
-    def __enter__(self):
-        cuda = _torch().cuda
-        if cuda.current_device() != self.dev:
-            self.ctx = cuda.device(self.dev)
-            self.ctx.__enter__()
-
-    def __exit__(self, *e):
-        if self.ctx is not None:
-            self.ctx.__exit__(*e)
+def _call(fn, device, *args):
+    """Calls the library with the current stream of tensor device ``device`` (an
+    index) as the last argument, that device made the current one."""
+    torch = _torch()
+    f = getattr(_lib.load(), fn)
+    if torch.cuda.current_device() == device:
+        st = f(*args, torch._C._cuda_getCurrentRawStream(device))
+    else:
+        with torch.cuda.device(device):
+            st = f(*args, torch._C._cuda_getCurrentRawStream(device))
+    if st:
+        _lib.check(fn, st)
 
 
 def _kv8(k_cache, v_cache, k_scale, v_scale, block_table, ctx, cu_q):
-    """The C struct of a cache and a batch, its tensors checked."""
+    """The C struct of a cache and a batch, its tensors checked, and their device's index."""
+    torch = _torch()
+    f8, f32, i32 = torch.float8_e4m3fn, torch.float32, torch.int32
+    try:
+        dev = k_cache.get_device()
+        pages, hkv, page, d = k_cache.shape
+        b, max_pages = block_table.shape
+        good = (dev >= 0 and k_cache.dtype is f8 and v_cache.dtype is f8 and k_scale.dtype is f32
+                and v_scale.dtype is f32 and block_table.dtype is i32 and ctx.dtype is i32
+                and v_cache.get_device() == k_scale.get_device() == v_scale.get_device()
+                == block_table.get_device() == ctx.get_device() == dev
+                and v_cache.shape == (pages, hkv, d, page) and k_scale.shape == (pages, hkv)
+                and v_scale.shape == (pages, hkv) and ctx.shape == (b,)
+                and k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous()
+                and v_scale.is_contiguous() and block_table.is_contiguous() and ctx.is_contiguous()
+                and (cu_q is None or (cu_q.dtype is i32 and cu_q.get_device() == dev and cu_q.shape == (b + 1,)
+                                      and cu_q.is_contiguous())))
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        _kv8_refuse(k_cache, v_cache, k_scale, v_scale, block_table, ctx, cu_q)
+    return _lib.Kv8Cache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                         block_table.data_ptr(), None if cu_q is None else cu_q.data_ptr(), ctx.data_ptr(), pages,
+                         max_pages, b, page, hkv, d), dev
+
+
+def _kv8_refuse(k_cache, v_cache, k_scale, v_scale, block_table, ctx, cu_q):
+    """Raises for the first of the tensors that _kv8 does not take."""
     torch = _torch()
     f8, f32, i32 = torch.float8_e4m3fn, torch.float32, torch.int32
     _dev_tensor(k_cache, f8, "k_cache", 4)
     _dev_tensor(v_cache, f8, "v_cache", 4)
     pages, hkv, page, d = k_cache.shape
-    if v_cache.shape != (pages, hkv, d, page):
-        raise ValueError(f"v_cache must have shape {(pages, hkv, d, page)} (got {tuple(v_cache.shape)})")
+    _out_tensor(v_cache, f8, (pages, hkv, d, page), "v_cache")
     _out_tensor(k_scale, f32, (pages, hkv), "k_scale")
     _out_tensor(v_scale, f32, (pages, hkv), "v_scale")
     _dev_tensor(block_table, i32, "block_table", 2)
-    b, max_pages = block_table.shape
+    b = block_table.shape[0]
     _out_tensor(ctx, i32, (b,), "ctx")
-    dev = k_cache.device
-    for t, name in ((v_cache, "v_cache"), (k_scale, "k_scale"), (v_scale, "v_scale"),
-                    (block_table, "block_table"), (ctx, "ctx")):
-        if t.device != dev:
-            raise ValueError(f"{name} must be on {dev} (got {t.device})")
-    cu = None
     if cu_q is not None:
         _out_tensor(cu_q, i32, (b + 1,), "cu_q")
-        if cu_q.device != dev:
-            raise ValueError(f"cu_q must be on {dev} (got {cu_q.device})")
-        cu = cu_q.data_ptr()
-    return _lib.Kv8Cache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                         block_table.data_ptr(), cu, ctx.data_ptr(), pages, max_pages, b, page, hkv, d)
+    raise ValueError(f"the cache, block_table, ctx and cu_q must be on one device (k_cache is on {k_cache.device})")
 
 
 def _rows(t, dtype, name, heads, d, rows, dev):
-    """A [rows, heads, d] tensor whose heads and channels are packed; its row stride."""
-    if not isinstance(t, _torch().Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev} (got {t.device})")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    if t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads) \
-            or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name} must have shape ({'rows' if rows is None else rows}, "
-                         f"{'heads' if heads is None else heads}, {d}) (got {tuple(t.shape)})")
-    stride, h, c = t.stride()
-    if (c != 1 and d > 1) or (h != d and t.shape[1] > 1):
-        raise ValueError(f"{name} must have packed heads (strides {t.stride()})")
-    return stride if t.shape[0] > 1 else max(stride, t.shape[1] * d)
+    """The row stride of a [rows, heads, d] tensor whose heads and channels are packed."""
+    try:
+        n, h, c = t.shape
+        stride, hs, cs = t.stride()
+        if (t.dtype is dtype and t.get_device() == dev and c == d and (hs == d or h == 1) and cs == 1
+                and (heads is None or h == heads) and (rows is None or n == rows)):
+            return stride if n > 1 else h * d
+    except (AttributeError, TypeError, ValueError):
+        pass
+    _dev_tensor(t if not isinstance(t, _torch().Tensor) else t.reshape(-1)[:0], dtype, name)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the cache's device, cuda:{dev} (got {t.device})")
+    raise ValueError(f"{name} must have shape ({'rows' if rows is None else rows}, {'heads' if heads is None else heads}, "
+                     f"{d}) with packed heads (got {tuple(t.shape)}, strides {t.stride()})")
 
 
 def awq_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, ctx, cu_q=None, q=None, rope=None,
@@ -652,33 +660,30 @@ def awq_kv8_append_bf16(k, v, k_cache, v_cache, k_scale, v_scale, block_table, c
 def _kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, ctx, cu_q, q, rope, interleaved, out, bf):
     torch = _torch()
     dt = torch.bfloat16 if bf else torch.float16
-    c = _kv8(k_cache, v_cache, k_scale, v_scale, block_table, ctx, cu_q)
-    dev = k_cache.device
-    ks = _rows(k, dt, "k", c.hkv, c.d, None, dev)
+    c, dev = _kv8(k_cache, v_cache, k_scale, v_scale, block_table, ctx, cu_q)
+    hkv, d = c.hkv, c.d
+    ks = _rows(k, dt, "k", hkv, d, None, dev)
     rows = k.shape[0]
-    vs = _rows(v, dt, "v", c.hkv, c.d, rows, dev)
+    vs = _rows(v, dt, "v", hkv, d, rows, dev)
     if cu_q is None and rows < c.b:
         raise ValueError("without cu_q there must be a row for every sequence")
     hq = qs = os = 0
     if q is not None:
-        qs = _rows(q, dt, "q", None, c.d, rows, dev)
+        qs = _rows(q, dt, "q", None, d, rows, dev)
         hq = q.shape[1]
         if out is None:
-            out = torch.empty((rows, hq, c.d), dtype=dt, device=dev)
-        os = _rows(out, dt, "out", hq, c.d, rows, dev)
+            out = torch.empty((rows, hq, d), dtype=dt, device=q.device)
+        os = _rows(out, dt, "out", hq, d, rows, dev)
     elif out is not None:
         raise ValueError("out without q")
     positions = rot = 0
     if rope is not None:
         _dev_tensor(rope, torch.float32, "rope", 2)
-        if rope.device != dev:
-            raise ValueError(f"rope must be on {dev} (got {rope.device})")
+        if rope.get_device() != dev:
+            raise ValueError(f"rope must be on the cache's device, cuda:{dev} (got {rope.device})")
         positions, rot = rope.shape
-    fn = "awq_kv8_append_bf16" if bf else "awq_kv8_append"
-    with _on(k_cache):
-        st = getattr(_lib.load(), fn)(_lib.byref(c), rows, _ptr(q), qs, hq, k.data_ptr(), ks, v.data_ptr(), vs,
-                                      _ptr(rope), positions, rot, 1 if interleaved else 0, _ptr(out), os, _stream())
-    _lib.check(fn, st)
+    _call("awq_kv8_append_bf16" if bf else "awq_kv8_append", dev, _lib.byref(c), rows, _ptr(q), qs, hq,
+          k.data_ptr(), ks, v.data_ptr(), vs, _ptr(rope), positions, rot, 1 if interleaved else 0, _ptr(out), os)
     return out
 
 
@@ -712,27 +717,23 @@ def _attn_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx, cu_q, max
               bf):
     torch = _torch()
     dt = torch.bfloat16 if bf else torch.float16
-    c = _kv8(k_cache, v_cache, k_scale, v_scale, block_table, ctx, cu_q)
-    dev = k_cache.device
-    qs = _rows(q, dt, "q", None, c.d, None, dev)
-    rows, hq = q.shape[0], q.shape[1]
-    if cu_q is None and rows < c.b:
+    c, dev = _kv8(k_cache, v_cache, k_scale, v_scale, block_table, ctx, cu_q)
+    b, d = c.b, c.d
+    qs = _rows(q, dt, "q", None, d, None, dev)
+    rows, hq, _ = q.shape
+    if cu_q is None and rows < b:
         raise ValueError("without cu_q there must be a row for every sequence")
     if max_q is None:
         max_q = 1 if cu_q is None else max(rows, 1)
     if out is None:
-        out = torch.empty((rows, hq, c.d), dtype=dt, device=dev)
-    os = _rows(out, dt, "out", hq, c.d, rows, dev)
+        out = torch.empty((rows, hq, d), dtype=dt, device=q.device)
+    os = _rows(out, dt, "out", hq, d, rows, dev)
     if lse is not None:
         _out_tensor(lse, torch.float32, (rows, hq), "lse")
-        if lse.device != dev:
-            raise ValueError(f"lse must be on {dev} (got {lse.device})")
-    fn = "awq_attn_kv8_bf16" if bf else "awq_attn_kv8"
-    with _on(k_cache):
-        wp, wb = _workspace(awq_attn_kv8_workspace_size(c.b, rows, hq, c.hkv, c.d, c.page, c.max_pages, max_q),
-                            dev, workspace)
-        st = getattr(_lib.load(), fn)(_lib.byref(c), rows, max_q, q.data_ptr(), qs, hq,
-                                      c.d ** -0.5 if scale is None else scale, out.data_ptr(), os, _ptr(lse), wp,
-                                      wb, _stream())
-    _lib.check(fn, st)
+        if lse.get_device() != dev:
+            raise ValueError(f"lse must be on the cache's device, cuda:{dev} (got {lse.device})")
+    need = _lib.load().awq_attn_kv8_workspace_size(b, rows, hq, c.hkv, d, c.page, c.max_pages, max_q)
+    wp, wb = _workspace(need, q.device, workspace) if need else (None, 0)
+    _call("awq_attn_kv8_bf16" if bf else "awq_attn_kv8", dev, _lib.byref(c), rows, max_q, q.data_ptr(), qs, hq,
+          d ** -0.5 if scale is None else scale, out.data_ptr(), os, _ptr(lse), wp, wb)
     return out
