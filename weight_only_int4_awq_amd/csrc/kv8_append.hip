@@ -75,44 +75,60 @@ struct AppendP {
   int32_t n_kv;                      // work-groups of the cache's part
 };
 
-// 8 values of a row's head, channels d0 .. d0 + 7, rotated at position pos.
-// The rotation is one product, one product and one sum, each rounded once to
-// fp32 (no fused multiply-add), so that the codes do not hang on contraction.
+// Channels of a head in units of 8 values that one lane holds: two runs of four,
+// from a and from b.  A rotated unit u holds the pairs 4 u .. 4 u + 3 whole (both halves of
+// the split layout, or eight neighbours of the interleaved one), so that a
+// rotation needs nothing from another lane.
+struct Runs {
+  int a, b;
+  bool turn;
+};
+__device__ __forceinline__ Runs runs_of(int u, int rot, bool inter) {
+  Runs r;
+  r.turn = 8 * u < rot;
+  const bool split = r.turn && !inter;
+  r.a = split ? 4 * u : 8 * u;
+  r.b = split ? rot / 2 + 4 * u : 8 * u + 4;
+  return r;
+}
+struct Raw {
+  uint2 a, b;
+};
+__device__ __forceinline__ Raw load_raw(const uint16_t* row, const Runs& r) {
+  return Raw{*(const uint2*)(row + r.a), *(const uint2*)(row + r.b)};
+}
 template <bool BF>
-__device__ __forceinline__ void load_rotated(const uint16_t* row, int d0, const float* cs, int rot,
-                                             bool inter, float* y) {
-  const uint4 raw = *(const uint4*)(row + d0);
-  const uint32_t* r = (const uint32_t*)&raw;
-  float x[8];
+__device__ __forceinline__ void widen(const Raw& w, float* x) {
+  const uint32_t r[4] = {w.a.x, w.a.y, w.b.x, w.b.y};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[2 * i] = act2f<BF>((uint16_t)r[i]);
     x[2 * i + 1] = act2f<BF>((uint16_t)(r[i] >> 16));
   }
-  if (d0 >= rot) {
+}
+// The angles of a unit's four pairs at the table's row cs.
+struct Angles {
+  float c[4], s[4];
+};
+__device__ __forceinline__ Angles load_angles(const float* cs, int u, int rot, const Runs& r) {
+  Angles g;
+  const int j = r.turn ? 4 * u : 0;
+  const float4 c = *(const float4*)(cs + j), s = *(const float4*)(cs + rot / 2 + j);
+  g.c[0] = c.x, g.c[1] = c.y, g.c[2] = c.z, g.c[3] = c.w;
+  g.s[0] = s.x, g.s[1] = s.y, g.s[2] = s.z, g.s[3] = s.w;
+  return g;
+}
+// The rotation is one product, one product and one sum, each rounded once to
+// fp32 (no fused multiply-add), so that the codes do not hang on contraction.
+__device__ __forceinline__ void rotate(float* x, const Angles& g, const Runs& r, bool inter) {
+  if (!r.turn) return;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = x[i];
-    return;
-  }
-  const int half = rot / 2;
-  if (inter) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float c = cs[d0 / 2 + i], s = cs[half + d0 / 2 + i];
-      y[2 * i] = x[2 * i] * c - x[2 * i + 1] * s;
-      y[2 * i + 1] = x[2 * i + 1] * c + x[2 * i] * s;
-    }
-    return;
-  }
-  const bool hi = d0 >= half;
-  const int j = hi ? d0 - half : d0;
-  const uint4 mate = *(const uint4*)(row + (hi ? d0 - half : d0 + half));
-  const uint32_t* mr = (const uint32_t*)&mate;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float z = act2f<BF>((uint16_t)(mr[i / 2] >> (16 * (i & 1))));
-    const float c = cs[j + i], s = cs[half + j + i];
-    y[i] = hi ? x[i] * c + z * s : x[i] * c - z * s;
+  for (int i = 0; i < 4; ++i) {
+    float& p = x[inter ? 2 * i : i];
+    float& q = x[inter ? 2 * i + 1 : 4 + i];
+    const float a = p * g.c[i] - q * g.s[i], b = q * g.c[i] + p * g.s[i];
+    p = a;
+    q = b;
   }
 }
 
@@ -161,17 +177,24 @@ __device__ __forceinline__ int seq_of_unit(const Kv8View& v, int j, int lane) {
   }
   return count - 1;
 }
-__device__ __forceinline__ int seq_of_row(const Kv8View& v, int row, int lane) {
-  if (!v.cu) return row < v.b ? row : -1;
+// Sequences of the rows row0 .. row0 + N - 1 (-1: none); this lane gets that of row
+// row0 + lane / (64 / N).
+template <int N>
+__device__ __forceinline__ int seq_of_rows(const Kv8View& v, int row0, int lane) {
+  const int mine = lane / (64 / N);
+  if (!v.cu) return row0 + mine < v.b && row0 + mine < v.rows ? row0 + mine : -1;
   int count = 0;
   for (int i0 = 0; i0 < v.b; i0 += 64) {
-    const int i = i0 + lane;
-    bool le = false;
-    if (i < v.b) {
-      const SeqRows r = seq_rows(v, i);
-      le = r.r0 + r.n <= row;
+    int end = 0x7FFFFFFF;
+    if (i0 + lane < v.b) {
+      const SeqRows r = seq_rows(v, i0 + lane);
+      end = r.r0 + r.n;
     }
-    count += __popcll(__ballot(le));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int n = __popcll(__ballot(end <= row0 + i));
+      count += mine == i ? n : 0;
+    }
   }
   return count < v.b ? count : -1;
 }
@@ -179,50 +202,53 @@ __device__ __forceinline__ int seq_of_row(const Kv8View& v, int row, int lane) {
 // Cache part: one work-group per (page that a sequence's new rows touch, head).
 // It alone writes that page's codes and scales of the head, so growing a
 // part-filled page's scale and requantizing its older codes needs no atomic
-// and its result does not hang on any order.  Two passes over the new rows
-// (the second from the caches): largest magnitudes and rows that hold inf or
-// NaN, then the codes.  V's codes turn through LDS to lie token by token.
+// and its result does not hang on any order.  Slots are taken 64 at a time: first
+// the largest magnitudes and the rows that hold inf or NaN, then the codes.  The
+// 64 slots' rows are asked for at once and stay in registers between the two;
+// pages of more slots read them again.  V's codes turn through LDS to lie token by
+// token.
 // Query part: rows x groups of heads, the angles kept over the heads.
+// Bound by the bytes: 2 read per value of q, k and v, 2 written for q, 1 for k and v.
 template <int D, bool BF>
 __global__ __launch_bounds__(256) void kv8_append_kernel(AppendP p) {
   constexpr int LPT = D / 8;                 // lanes per token
   constexpr int TPI = 256 / LPT;             // tokens per pass of the work-group
+  constexpr int SL = 64, NI = SL / TPI;      // slots of a chunk, passes for it
   const Kv8View& v = p.v;
   const int lane = threadIdx.x & 63;
-  const int at = threadIdx.x / LPT, d0 = (threadIdx.x % LPT) * 8;
+  const int at = threadIdx.x / LPT, u = threadIdx.x % LPT;
+  const bool inter = p.inter != 0;
+  const Runs ru = runs_of(u, p.rot, inter);
   if ((int)blockIdx.x >= p.n_kv) {
     const int groups = (p.hq + p.hpt - 1) / p.hpt;
-    const int u = blockIdx.x - p.n_kv;
-    const int row0 = (u / groups) * TPI, h0 = (u % groups) * p.hpt;
+    const int w = blockIdx.x - p.n_kv;
+    const int row0 = (w / groups) * TPI, h0 = (w % groups) * p.hpt;
     const int h1 = h0 + p.hpt < p.hq ? h0 + p.hpt : p.hq;
-    // the rows of this wave, one after another: all lanes vote on each
-    constexpr int RPW = 64 / LPT;
-    const int wrow = row0 + (threadIdx.x / 64) * RPW;
-    int seq = -1;
-#pragma unroll
-    for (int i = 0; i < RPW; ++i) {
-      const int s = wrow + i < v.rows ? seq_of_row(v, wrow + i, lane) : -1;
-      if (lane / LPT == i) seq = s;
-    }
+    constexpr int RPW = 64 / LPT;            // rows of a wave
+    const int seq = seq_of_rows<RPW>(v, row0 + (threadIdx.x / 64) * RPW, lane);
     const int row = row0 + at;
     if (seq < 0) return;
     const SeqRows r = seq_rows(v, seq);
     if (row < r.r0 || row >= r.r0 + r.n) return;
     const int64_t pos = (int64_t)r.ctx - r.n + (row - r.r0);
     const bool out_of = p.rope && (pos < 0 || pos >= p.positions);
-    const float* cs = p.rope ? p.rope + (out_of ? 0 : pos) * p.rot : nullptr;
-    for (int h = h0; h < h1; ++h) {
+    Angles g = {};
+    if (p.rope) g = load_angles(p.rope + (out_of ? 0 : pos) * p.rot, u, p.rot, ru);
+    const uint16_t* src = p.q + row * p.q_stride + (int64_t)h0 * D;
+    uint16_t* dst = p.q_out + row * p.o_stride + (int64_t)h0 * D;
+#pragma unroll 8
+    for (int h = h0; h < h1; ++h, src += D, dst += D) {
       float y[8];
-      load_rotated<BF>(p.q + row * p.q_stride + (int64_t)h * D, d0, cs, p.rot, p.inter, y);
-      uint32_t w[4];
+      widen<BF>(load_raw(src, ru), y);
+      rotate(y, g, ru, inter);
+      uint32_t o[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        w[i] = (uint32_t)f2act(out_of ? __builtin_nanf("") : y[2 * i], BF) |
-               (uint32_t)f2act(out_of ? __builtin_nanf("") : y[2 * i + 1], BF) << 16;
-      // the pair's other half is read by other lanes of this wave: with q_out = q
-      // all of them have read it before any writes
-      __builtin_amdgcn_wave_barrier();
-      *(uint4*)(p.q_out + row * p.o_stride + (int64_t)h * D + d0) = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int i = 0; i < 4; ++i) {
+        const float nan = __builtin_nanf("");
+        o[i] = (uint32_t)f2act(out_of ? nan : y[2 * i], BF) | (uint32_t)f2act(out_of ? nan : y[2 * i + 1], BF) << 16;
+      }
+      *(uint2*)(dst + ru.a) = make_uint2(o[0], o[1]);
+      *(uint2*)(dst + ru.b) = make_uint2(o[2], o[3]);
     }
     return;
   }
@@ -244,104 +270,178 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(AppendP p) {
   const int z = (int)(r.ctx - page0 < page ? r.ctx - page0 : page);
   const int64_t ph = (int64_t)pid * v.hkv + h;
   const int64_t row0 = r.r0 + page0 - first;                  // row of the page's slot 0
+  const Runs rv = runs_of(u, 0, false);
+  const uint16_t* ksrc = p.k + row0 * p.k_stride + (int64_t)h * D;
+  const uint16_t* vsrc = p.vv + row0 * p.v_stride + (int64_t)h * D;
 
   __shared__ uint32_t bad[256 / 32];
-  __shared__ float kmax[4], vmax[4];
-  __shared__ uint8_t turn[256][D + 4];                        // V codes [slot][channel]
+  __shared__ uint32_t kmax[4], vmax[4];
+  __shared__ uint32_t turn[SL][D / 4 + 1];                    // V codes [slot][channel]
   if (threadIdx.x < 256 / 32) bad[threadIdx.x] = 0;
-  __syncthreads();
-  float km = 0.0f, vm = 0.0f;
-  for (int s0 = a; s0 < z; s0 += TPI) {
-    const int s = s0 + at;
-    float y[8], x[8], ka = 0.0f, va = 0.0f;
-    bool ok = true;
-    if (s < z) {
-      const int64_t row = row0 + s, pos = page0 + s;
-      const bool out_of = p.rope && pos >= p.positions;
-      const float* cs = p.rope ? p.rope + (out_of ? 0 : pos) * p.rot : nullptr;
-      load_rotated<BF>(p.k + row * p.k_stride + (int64_t)h * D, d0, cs, p.rot, p.inter, y);
-      load_rotated<BF>(p.vv + row * p.v_stride + (int64_t)h * D, d0, nullptr, 0, false, x);
-      ok = !out_of;
+  const float kold = a ? v.ks[ph] : 0.0f, vold = a ? v.vs[ph] : 0.0f;
+  float y[NI][8];                                             // rotated keys
+  Raw x[NI];                                                  // values
+  const int cfirst = a / SL * SL;
+  auto fetch = [&](int c0) {
+    const uint16_t* kp = ksrc + (c0 + at) * p.k_stride;
+    const uint16_t* vp = vsrc + (c0 + at) * p.v_stride;
+    Raw kk[NI];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        ok = ok && finite(y[i]) && finite(x[i]);
-        ka = __builtin_fmaxf(ka, __builtin_fabsf(y[i]));
-        va = __builtin_fmaxf(va, __builtin_fabsf(x[i]));
+    for (int i = 0; i < NI; ++i) {
+      const int s = c0 + i * TPI + at;
+      if (s >= a && s < z) {
+        kk[i] = load_raw(kp + i * TPI * p.k_stride, ru);
+        x[i] = load_raw(vp + i * TPI * p.v_stride, rv);
       }
     }
-    const uint64_t group = ((1ull << LPT) - 1) << (lane & ~(LPT - 1));
-    ok = (__ballot(!ok) & group) == 0;
-    if (!ok && s < z && d0 == 0) atomicOr(&bad[s >> 5], 1u << (s & 31));
-    if (ok) {
-      km = __builtin_fmaxf(km, ka);
-      vm = __builtin_fmaxf(vm, va);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int s = c0 + i * TPI + at;
+      if (s >= a && s < z) {
+        widen<BF>(kk[i], y[i]);
+        if (p.rope) {
+          const int64_t pos = page0 + s;
+          rotate(y[i], load_angles(p.rope + (pos < p.positions ? pos : 0) * p.rot, u, p.rot, ru), ru, inter);
+        }
+      }
+    }
+  };
+  fetch(cfirst);
+  __syncthreads();
+  // Magnitudes are compared as their bits: inf and NaN are above every finite value.
+  constexpr uint32_t kInf16 = BF ? 0x7F80u : 0x7C00u;
+  uint32_t km = 0, vm = 0;
+  for (int c0 = cfirst; c0 < z; c0 += SL) {
+    if (c0 > cfirst) fetch(c0);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int s = c0 + i * TPI + at;
+      const bool here = s >= a && s < z;
+      uint32_t ka = 0, va = 0;
+      if (here) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t m = __builtin_bit_cast(uint32_t, y[i][e]) & 0x7FFFFFFFu;
+          ka = ka > m ? ka : m;
+        }
+        const uint32_t r[4] = {x[i].a.x, x[i].a.y, x[i].b.x, x[i].b.y};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t lo = r[e] & 0x7FFFu, hi = r[e] >> 16 & 0x7FFFu;
+          va = va > lo ? va : lo;
+          va = va > hi ? va : hi;
+        }
+      }
+      bool ok = ka < 0x7F800000u && va < kInf16 && (!p.rope || page0 + s < p.positions || !here);
+      const uint64_t group = ((1ull << LPT) - 1) << (lane & ~(LPT - 1));
+      ok = (__ballot(!ok) & group) == 0;
+      if (!ok && u == 0) atomicOr(&bad[s >> 5], 1u << (s & 31));
+      if (ok) {
+        km = km > ka ? km : ka;
+        vm = vm > va ? vm : va;
+      }
     }
   }
 #pragma unroll
   for (int o = 32; o; o >>= 1) {
-    km = __builtin_fmaxf(km, __shfl_xor(km, o, 64));
-    vm = __builtin_fmaxf(vm, __shfl_xor(vm, o, 64));
+    const uint32_t k2 = __shfl_xor(km, o, 64), v2 = __shfl_xor(vm, o, 64);
+    km = km > k2 ? km : k2;
+    vm = vm > v2 ? vm : v2;
   }
   if (lane == 0) {
     kmax[threadIdx.x >> 6] = km;
     vmax[threadIdx.x >> 6] = vm;
   }
-  const float kold = a ? v.ks[ph] : 0.0f, vold = a ? v.vs[ph] : 0.0f;
   __syncthreads();
-  km = __builtin_fmaxf(__builtin_fmaxf(kmax[0], kmax[1]), __builtin_fmaxf(kmax[2], kmax[3]));
-  vm = __builtin_fmaxf(__builtin_fmaxf(vmax[0], vmax[1]), __builtin_fmaxf(vmax[2], vmax[3]));
-  const float ks = __builtin_fmaxf(scale_of(km), kold), vs = __builtin_fmaxf(scale_of(vm), vold);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    km = km > kmax[i] ? km : kmax[i];
+    vm = vm > vmax[i] ? vm : vmax[i];
+  }
+  const float ks = __builtin_fmaxf(scale_of(__builtin_bit_cast(float, km)), kold);
+  const float vs = __builtin_fmaxf(scale_of(act2f<BF>((uint16_t)vm)), vold);
   const float kr = kold / ks, vr = vold / vs;
   if (threadIdx.x == 0) {
     v.ks[ph] = ks;
     v.vs[ph] = vs;
   }
+  // x / scale is x * (1 / scale) for the powers of two that this kernel writes; a scale
+  // that another writer left in the page need not be one
+  const bool exact = ((__builtin_bit_cast(uint32_t, ks) | __builtin_bit_cast(uint32_t, vs)) & 0x7FFFFFu) == 0;
+  const float ki = 1.0f / ks, vi = 1.0f / vs;
   uint8_t* kp = v.kc + (ph << v.shift) * D;
   uint8_t* vp = v.vc + ((ph * D) << v.shift);
   if (a && kr != 1.0f)
     for (int i = threadIdx.x; i < a * D / 4; i += 256) ((uint32_t*)kp)[i] = rescale4(((uint32_t*)kp)[i], kr);
-  for (int s0 = a; s0 < z; s0 += TPI) {
-    const int s = s0 + at;
-    if (s >= z) continue;
-    const int64_t row = row0 + s, pos = page0 + s;
-    uint2 kw = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu), vw = make_uint2(0, 0);
-    if (!(bad[s >> 5] >> (s & 31) & 1)) {
-      float y[8], x[8];
-      const float* cs = p.rope ? p.rope + pos * p.rot : nullptr;
-      load_rotated<BF>(p.k + row * p.k_stride + (int64_t)h * D, d0, cs, p.rot, p.inter, y);
-      load_rotated<BF>(p.vv + row * p.v_stride + (int64_t)h * D, d0, nullptr, 0, false, x);
-      // true quotients: a scale that another writer left need not be a power of two
-      kw = make_uint2(codes4(y[0] / ks, y[1] / ks, y[2] / ks, y[3] / ks),
-                      codes4(y[4] / ks, y[5] / ks, y[6] / ks, y[7] / ks));
-      vw = make_uint2(codes4(x[0] / vs, x[1] / vs, x[2] / vs, x[3] / vs),
-                      codes4(x[4] / vs, x[5] / vs, x[6] / vs, x[7] / vs));
-    }
-    *(uint2*)(kp + s * D + d0) = kw;
-    uint32_t* t = (uint32_t*)&turn[s][d0];
-    t[0] = vw.x;
-    t[1] = vw.y;
-  }
-  __syncthreads();
-  // V: whole words of four slots; slots that are not new keep what they held
-  const int w0 = vr != 1.0f ? 0 : a >> 2, w1 = (z + 3) >> 2, nw = w1 - w0;
-  for (int i = threadIdx.x; i < nw * D; i += 256) {
-    const int d = i / nw, w = w0 + i % nw;
-    uint32_t* g = (uint32_t*)(vp + (d << v.shift)) + w;
-    uint32_t word = 0, keep = 0, older = 0;
+  for (int c0 = vr != 1.0f ? 0 : cfirst; c0 < z; c0 += SL) {
+    const int c1 = c0 + SL < z ? c0 + SL : z;
+    if (z - cfirst > SL && c1 > a) fetch(c0);
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int s = 4 * w + x;
-      const uint32_t m = 0xFFu << (8 * x);
-      if (s < a) older |= m;
-      else if (s >= z) keep |= m;
-      else word |= (uint32_t)turn[s][d] << (8 * x);
+    for (int i = 0; i < NI; ++i) {
+      const int s = c0 + i * TPI + at;
+      if (s < a || s >= z) continue;
+      uint32_t k0 = 0x7F7F7F7Fu, k1 = 0x7F7F7F7Fu, v0 = 0, v1 = 0;
+      if (!(bad[s >> 5] >> (s & 31) & 1)) {
+        float e[8], f[8];
+        widen<BF>(x[i], f);
+        if (exact) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) e[c] = y[i][c] * ki, f[c] = f[c] * vi;
+        } else {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) e[c] = y[i][c] / ks, f[c] = f[c] / vs;
+        }
+        k0 = codes4(e[0], e[1], e[2], e[3]);
+        k1 = codes4(e[4], e[5], e[6], e[7]);
+        v0 = codes4(f[0], f[1], f[2], f[3]);
+        v1 = codes4(f[4], f[5], f[6], f[7]);
+      }
+      *(uint32_t*)(kp + s * D + ru.a) = k0;
+      *(uint32_t*)(kp + s * D + ru.b) = k1;
+      turn[s % SL][2 * u] = v0;
+      turn[s % SL][2 * u + 1] = v1;
     }
-    if (older | keep) {
-      const uint32_t was = *g;
-      word |= was & keep;
-      word |= (vr != 1.0f ? rescale4(was, vr) : was) & older;
+    __syncthreads();
+    // V: a thread turns 4 channels x 8 slots; eight neighbours write 64 bytes of a
+    // channel.  Slots that are not new keep what they held.
+    const int from = vr != 1.0f || a < c0 ? c0 : a;
+    for (int i = threadIdx.x; i < D / 4 * (SL / 8); i += 256) {
+      const int c = i / (SL / 8), s0 = c0 + i % (SL / 8) * 8;
+      if (s0 + 8 <= from || s0 >= c1) continue;
+      uint32_t t[8], w[4][2];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) t[e] = turn[s0 % SL + e][c];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const uint32_t* r = t + 4 * q;
+        const uint32_t ab0 = __builtin_amdgcn_perm(r[1], r[0], 0x05010400), ab1 = __builtin_amdgcn_perm(r[1], r[0], 0x07030602);
+        const uint32_t cd0 = __builtin_amdgcn_perm(r[3], r[2], 0x05010400), cd1 = __builtin_amdgcn_perm(r[3], r[2], 0x07030602);
+        w[0][q] = __builtin_amdgcn_perm(cd0, ab0, 0x05040100);
+        w[1][q] = __builtin_amdgcn_perm(cd0, ab0, 0x07060302);
+        w[2][q] = __builtin_amdgcn_perm(cd1, ab1, 0x05040100);
+        w[3][q] = __builtin_amdgcn_perm(cd1, ab1, 0x07060302);
+      }
+      const bool all = s0 >= a && s0 + 8 <= z;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t* g = (uint32_t*)(vp + ((4 * c + q) << v.shift) + s0);
+        if (all) {
+          *(uint2*)g = make_uint2(w[q][0], w[q][1]);
+          continue;
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int s = s0 + 4 * half, lo = a - s, hi = z - s;      // slots lo .. hi - 1 of the word are new
+          if (s + 4 <= from || hi <= 0) continue;
+          const uint32_t older = lo <= 0 ? 0u : lo >= 4 ? ~0u : (1u << (8 * lo)) - 1u;
+          const uint32_t keep = hi >= 4 ? 0u : ~((1u << (8 * hi)) - 1u);
+          const uint32_t was = older | keep ? g[half] : 0u;
+          g[half] = (w[q][half] & ~(older | keep)) | (was & keep) |
+                    ((vr != 1.0f && older ? rescale4(was, vr) : was) & older);
+        }
+      }
     }
-    *g = word;
+    __syncthreads();
   }
 }
 
