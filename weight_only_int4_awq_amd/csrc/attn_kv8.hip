@@ -12,12 +12,12 @@
 // c of a sequence is row c / G, query head h * G + c % G.
 //
 // One pass with a running maximum.  The page's value scale goes into the
-// exponent: p' = exp2(s + log2 vs - m) <= 2^kLazy, O = sum p' vcode in units
-// of 1, l = sum p' / vs.  So p' carries exactly the weight of its token's
-// contribution to O whatever the scales are, and fp16 (11 bits) holds it with a
-// relative rounding of 2^-12 to 2^-11; S, O, m and l are fp32.  m moves only when a
-// score exceeds it by 2^kLazy (a wave-wide vote), so most steps neither
-// exchange maxima between lanes nor rescale O.
+// exponent: p' = exp2(s + log2 vs - m), O = sum p' vcode in units of 1,
+// l = sum p' / vs.  So p' carries exactly the weight of its token's contribution
+// to O whatever the scales are, and fp16 (11 bits) holds it with a relative
+// rounding of 2^-12 to 2^-11; S, O, m and l are fp32.  m moves only when a score
+// exceeds it by kLazy (a wave-wide vote), so most steps exchange nothing between
+// lanes and rescale nothing.
 #include "awq_internal.h"
 #include "kv8_common.h"
 
@@ -25,7 +25,7 @@ namespace awq {
 namespace {
 
 constexpr int kStep = 64;            // tokens of one step (a page holds whole steps)
-constexpr float kLazy = 8.0f;        // p' <= 2^8: far inside fp16
+constexpr float kLazy = 8.0f;        // m moves for scores that exceed it by 8: p' <= 2^8, far inside fp16
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kNone = -1e30f;      // running maximum before any visible token
@@ -46,17 +46,14 @@ struct AttnP {
   float* part_ml;
 };
 
-__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
-
 // Results of one column's channels d .. d + 3: O / l, and the lse from channel 0.
 // No visible token: zeros and -inf (a NaN sum is kept).
 template <bool BF>
 __device__ __forceinline__ void store4(const AttnP& p, int row, int head, int D, int d, float4 a, float top,
                                        float sum) {
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  const uint32_t lo = (uint32_t)f2act(a.x * inv, BF) | (uint32_t)f2act(a.y * inv, BF) << 16;
-  const uint32_t hi = (uint32_t)f2act(a.z * inv, BF) | (uint32_t)f2act(a.w * inv, BF) << 16;
-  *(uint2*)(p.out + row * p.out_stride + (int64_t)head * D + d) = make_uint2(lo, hi);
+  *(uint2*)(p.out + row * p.out_stride + (int64_t)head * D + d) =
+      make_uint2(pack2<BF>(a.x * inv, a.y * inv), pack2<BF>(a.z * inv, a.w * inv));
   if (p.lse && d == 0)
     p.lse[(int64_t)row * p.hq + head] = sum == 0.0f ? -__builtin_inff() : (top + __builtin_amdgcn_logf(sum)) * kLn2;
 }
@@ -161,7 +158,7 @@ struct Wave {
     const int c = lane % C, g = lane / C, t0 = st * kStep;
     const int krow = W ? 16 * (c >> 2 & 1) + 4 * (c >> 3) + (c & 3) : 16 * (c >> 2) + (c & 3);
     int pid = uniform(q.bt[t0 >> v.shift]);
-    bad = q.over || (uint32_t)pid >= (uint64_t)v.pages;
+    bad = q.over || (uint32_t)pid >= (uint32_t)v.pages;
     pid = bad ? 0 : pid;
     const int64_t ph = (int64_t)pid * v.hkv + h;
     const int slot0 = t0 & ((1 << v.shift) - 1);
@@ -174,6 +171,62 @@ struct Wave {
 #pragma unroll
       for (int x = 0; x < NX; ++x)
         kr[t][x] = load16<ONCE>(kp + ((W ? 32 : 4) * t + krow) * D + 16 * GR * x + 16 * g);
+  }
+
+  // Scores of one step to softmax weights: the running maximum, l and O brought
+  // up to date, the weights in pf as the value product's operand.
+  __device__ __forceinline__ void weigh(acc_t* s, const Seq& q, int t0, float k1, float v1, bool out_of, int g,
+                                        half8_t* pf) {
+    float a = k1, z = __builtin_amdgcn_logf(v1);
+    const float rv = __builtin_amdgcn_rcpf(v1);
+    if (t0 + kStep - 1 > q.first || out_of) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+          s[t][j] = t0 + token(t, j, g) <= q.pos ? __builtin_fmaf(s[t][j], a, z) : -__builtin_inff();
+      a = 1.0f;
+      z = 0.0f;
+    }
+    float mx = s[0][0];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) mx = __builtin_fmaxf(mx, s[t][j]);
+    mx = __builtin_fmaf(mx, a, z);
+    if (__ballot(mx > m + kLazy)) {
+#pragma unroll
+      for (int x = C; x < 64; x <<= 1) mx = __builtin_fmaxf(mx, __shfl_xor(mx, x, 64));
+      const float mn = __builtin_fmaxf(m, mx);
+      const float f = __builtin_amdgcn_exp2f(m - mn);
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < ND; ++i) o[i] *= f;
+    }
+    z -= m;
+    float sum = 0.0f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][j], a, z));
+        sum += e;
+        pf[(t * NJ + j) / 8][(t * NJ + j) % 8] = (half_t)e;
+      }
+    l = __builtin_fmaf(sum, rv, l);
+  }
+
+  // Codes of 16 tokens, `left` of them before the sequence's end: slots behind it, and
+  // the page read in place of one that is not in the cache, may hold anything,
+  // NaN codes too (0 * NaN).
+  static __device__ __forceinline__ void trim(uint4& x, int left) {
+    uint32_t* w = (uint32_t*)&x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = left - 4 * j;
+      w[j] &= n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
+    }
   }
 
   __device__ __forceinline__ void loop(const Kv8View& v, float scale2, const Seq& q, int h, int st, int st1,
@@ -198,61 +251,16 @@ struct Wave {
           s[t] = mma_q(MQ::from_fp8(kr[t][x].z, kr[t][x].w), qf[x][1], s[t]);
         }
       }
-      float a = ks, z = __builtin_amdgcn_logf(vs);
-      const float rv = 1.0f / vs;
-      const int held = bad ? 0 : q.ctx;
+      const float k1 = ks, v1 = vs;
+      const bool out_of = bad;
       if (st + stride < st1) ask(v, scale2, q, h, st + stride, lane);
-      if (t0 + kStep - 1 > q.first || held == 0) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int j = 0; j < NJ; ++j)
-            s[t][j] = t0 + token(t, j, g) <= q.pos ? __builtin_fmaf(s[t][j], a, z) : -__builtin_inff();
-        a = 1.0f;
-        z = 0.0f;
-      }
-      float mx = s[0][0];
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) mx = __builtin_fmaxf(mx, s[t][j]);
-      mx = __builtin_fmaf(mx, a, z);
-      if (__ballot(mx > m + kLazy)) {
-#pragma unroll
-        for (int x = C; x < 64; x <<= 1) mx = __builtin_fmaxf(mx, __shfl_xor(mx, x, 64));
-        const float mn = __builtin_fmaxf(m, mx);
-        const float f = __builtin_amdgcn_exp2f(m - mn);
-        m = mn;
-        l *= f;
-#pragma unroll
-        for (int i = 0; i < ND; ++i) o[i] *= f;
-      }
-      z -= m;
-      float sum = 0.0f;
       half8_t pf[NT * NJ / 8];
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][j], a, z));
-          sum += e;
-          pf[(t * NJ + j) / 8][(t * NJ + j) % 8] = (half_t)e;
-        }
-      l = __builtin_fmaf(sum, rv, l);
-      // slots behind the sequence's end, and the page read in place of one that is
-      // not in the cache, may hold anything, NaN codes too: 0 * NaN
-      if (t0 + kStep > held) {
+      weigh(s, q, t0, k1, v1, out_of, g, pf);
+      if (t0 + kStep > (out_of ? 0 : q.ctx)) {
 #pragma unroll
         for (int i = 0; i < ND; ++i)
 #pragma unroll
-          for (int t = 0; t < NV; ++t) {
-            uint32_t* x = (uint32_t*)&vr[i][t];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int left = held - (t0 + 32 * t + 16 * g + 4 * j);
-              x[j] &= left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
-            }
-          }
+          for (int t = 0; t < NV; ++t) trim(vr[i][t], (out_of ? 0 : q.ctx) - (t0 + 32 * t + 16 * g));
       }
 #pragma unroll
       for (int i = 0; i < ND; ++i)
@@ -392,13 +400,15 @@ __global__ __launch_bounds__(512, 2) void attn_kv8_line_kernel(AttnP p) {
   int st, st1, cols;
   // the tile's columns and this stretch's steps of it
   auto begin = [&]() {
+    w.b = uniform(w.b), w.steps = uniform(w.steps), w.tile = uniform(w.tile), w.at = uniform(w.at);
+    w.r.n = uniform(w.r.n), w.r.ctx = uniform(w.r.ctx), w.r.r0 = uniform(w.r.r0);
     const int n = w.r.n, ctx = w.r.ctx, col = w.tile * C + c;
     cols = n * G - w.tile * C < C ? n * G - w.tile * C : C;
     q.bt = v.bt + (int64_t)w.b * v.max_pages;
     q.ctx = ctx;
     q.over = ctx > cap;
     q.pos = c < cols ? ctx - n + col / G : -1;
-    q.first = cols < C ? -1 : ctx - n + (w.tile * C) / G;
+    q.first = uniform(cols < C ? -1 : ctx - n + (w.tile * C) / G);
     const int held = ctx / kStep + (ctx % kStep ? 1 : 0), there = held < y.cap ? held : y.cap;
     const uint32_t z = w.at + w.steps < x1 ? w.at + w.steps : x1;
     st = (int)(x - w.at) + wave;
@@ -576,41 +586,166 @@ __device__ __forceinline__ bool find_unit(const AttnP& p, int u, int lane, Unit&
   return false;
 }
 
-// Tiles of 128 columns: each of the four waves has 32 of them and walks all of
-// the unit's steps.  The waves read the same pages within a short time of each
-// other, so all but the first of these reads come from the CU's own cache.
+// Tiles of 128 columns: each of the four waves has 32 of them and walks all of the
+// unit's steps.  A step's codes come to LDS once for the four waves, copied there
+// straight from the cache two stages deep: 16-byte pieces, placed so that the 8
+// lanes of an LDS cycle hit different banks.  (Read by each wave from the CU's
+// vector cache instead, that cache was 92 % busy and the 8 K prompt took 740 us.)
+//   keys    piece j of token r's D / 16 at j ^ key(r): the rows that an 8-lane cycle reads
+//           are 4 neighbours of two blocks of 16;
+//   values  piece j of channel d's four at j ^ (d / 2 % 4).
+template <int D>
+struct Stage {
+  static constexpr int KP = D / 16;              // pieces of a token's keys
+  uint4 k[kStep * KP];
+  uint4 v[D * 4];
+  static __device__ __forceinline__ int key(int r) { return KP == 8 ? (r & 3) | (r >> 2 & 4) : (r >> 1 & 1) | (r >> 3 & 2); }
+  static __device__ __forceinline__ int kat(int r, int j) { return r * KP + (j ^ key(r)); }
+  static __device__ __forceinline__ int vat(int d, int j) { return d * 4 + (j ^ (d >> 1 & 3)); }
+};
+
+// One 16-byte global -> LDS copy per lane: lane i writes LDS bytes base + 16 i .. +15.
+// From inline asm, so that the compiler leaves the waits to the caller: it would
+// drain every outstanding copy before any read of the array.  M0 is the
+// compiler's only to address LDS copies of its own; there are none here.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void lds_copy16(const void* src, uint32_t base) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+               :
+               : "v"(src), "s"(base)
+               : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
 template <int D, bool BF>
 __global__ __launch_bounds__(256, 2) void attn_kv8_tile_kernel(AttnP p) {
-  constexpr int TC = 128, ND = D / 32;
+  constexpr int TC = 128, ND = D / 32, NW = 4;
+  typedef Wave<D, BF, 32, false> E;
+  typedef Stage<D> T;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int h = blockIdx.x % p.v.hkv;
   Unit w;
   if (!find_unit<TC, false>(p, blockIdx.x / p.v.hkv, lane, w)) return;
   const Kv8View& v = p.v;
-  const int b = w.b, S = w.S, sidx = w.s, tile = w.tile, n = w.r.n, r0 = w.r.r0, ctx = w.r.ctx;
+  const int b = uniform(w.b), S = uniform(w.S), sidx = uniform(w.s), tile = uniform(w.tile);
+  const int n = uniform(w.r.n), r0 = uniform(w.r.r0), ctx = uniform(w.r.ctx);
   const int G = p.G, c0 = tile * TC + 32 * wave;
-  const int cols = n * G - c0 < 32 ? n * G - c0 : 32;
-  if (cols <= 0) return;
+  const int cols = n * G - c0 < 32 ? n * G - c0 : 32;           // may be none
   const int c = lane & 31, half = lane >> 5, col = c0 + c;
   const int pos = c < cols ? ctx - n + col / G : -1;
-  const int first = cols < 32 ? -1 : ctx - n + c0 / G;
-  // the unit's share of the tile's steps; this wave stops at what its own rows see
+  const int first = uniform(cols < 32 ? -1 : ctx - n + c0 / G);
+  // the unit's share of the tile's steps; this wave computes what its own rows see
   const int tcols = n * G - tile * TC < TC ? n * G - tile * TC : TC;
-  const int last = ctx - n + (tile * TC + tcols - 1) / G, wlast = ctx - n + (c0 + cols - 1) / G;
+  const int last = ctx - n + (tile * TC + tcols - 1) / G, wlast = cols > 0 ? ctx - n + (c0 + cols - 1) / G : -1;
   const int cap = (int)(((int64_t)v.max_pages << v.shift) / kStep);
-  int steps = last < 0 ? 0 : last / kStep + 1, wsteps = wlast < 0 ? 0 : wlast / kStep + 1;
+  int steps = last < 0 ? 0 : last / kStep + 1;
   steps = steps < cap ? steps : cap;
-  const int st0 = (int)((int64_t)steps * sidx / S);
-  int st1 = (int)((int64_t)steps * (sidx + 1) / S);
-  st1 = st1 < wsteps ? st1 : wsteps;
+  // divisions leave wave-uniform values in vector registers: bring them back, so that
+  // branches on them are scalar
+  const int st0 = uniform((int)((int64_t)steps * sidx / S)), st1 = uniform((int)((int64_t)steps * (sidx + 1) / S));
+  const int wst1 = uniform(wlast < 0 ? 0 : wlast / kStep + 1);
 
-  Wave<D, BF, 32, false> a;
+  __shared__ T stage[2];
+  E a;
   const Seq q = {v.bt + (int64_t)b * v.max_pages, ctx, pos, first, ctx > (int64_t)v.max_pages << v.shift};
-  if (st0 < st1) a.ask(v, p.scale2, q, h, st0, lane);
-  const int cc = c < cols ? col : c0;
-  a.load_q(p.q + (int64_t)(r0 + cc / G) * p.q_stride + (int64_t)(h * G + cc % G) * D, lane);
+  {
+    const int cc = c < cols ? col : tile * TC;
+    a.load_q(p.q + (int64_t)(r0 + cc / G) * p.q_stride + (int64_t)(h * G + cc % G) * D, lane);
+  }
   a.clear();
-  a.loop(v, p.scale2, q, h, st0, st1, 1, lane);
+
+  // this wave's pieces of a step: chunks of 64 pieces, every fourth
+  const int smask = (1 << v.shift) - 1;
+  auto copy = [&](int st, int pid, int to) {
+    const int64_t ph = (int64_t)pid * v.hkv + h;
+    const int slot0 = (st * kStep) & smask;
+    const uint8_t* kp = v.kc + ((ph << v.shift) + slot0) * D;
+    const uint8_t* vp = v.vc + ((ph * D) << v.shift) + slot0;
+    // an LDS address is the low half of its flat one
+    const uint32_t kb = (uint32_t)(uintptr_t)&stage[to].k[0], vb = (uint32_t)(uintptr_t)&stage[to].v[0];
+#pragma unroll
+    for (int i = 0; i < T::KP / NW; ++i) {
+      const int at = (wave + NW * i) * 64 + lane, r = at / T::KP, j = at % T::KP ^ T::key(r);
+      lds_copy16(kp + r * D + 16 * j, uniform(kb + (wave + NW * i) * 1024));
+    }
+#pragma unroll
+    for (int i = 0; i < D / 16 / NW; ++i) {
+      const int at = (wave + NW * i) * 64 + lane, d = at / 4, j = at % 4 ^ (d >> 1 & 3);
+      lds_copy16(vp + (d << v.shift) + 16 * j, uniform(vb + (wave + NW * i) * 1024));
+    }
+  };
+  // where this lane's operands lie in a stage, in bytes: tile t of the keys and tile i of
+  // the values are a constant further on
+  int kat[E::NX], vat[2];
+  {
+    const int r = 16 * (c >> 2 & 1) + 4 * (c >> 3) + (c & 3);
+#pragma unroll
+    for (int x = 0; x < E::NX; ++x) kat[x] = 16 * T::kat(r, 2 * x + half);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) vat[t] = (int)sizeof(stage[0].k) + 16 * T::vat(c, 2 * t + half);
+  }
+  auto page_of = [&](int st) { return uniform(q.bt[(st * kStep) >> v.shift]); };
+  const uint32_t pages = (uint32_t)v.pages;                     // below 2^31
+  auto held = [&](int pid) { return !q.over && (uint32_t)pid < pages; };
+  int pid = 0, next = 0;
+  if (st0 < st1) {
+    pid = page_of(st0);
+    copy(st0, held(pid) ? pid : 0, 0);
+    next = st0 + 1 < st1 ? page_of(st0 + 1) : 0;
+  }
+  for (int st = st0; st < st1; ++st) {
+    const int t0 = st * kStep;
+    const char* sg = (const char*)&stage[(st - st0) & 1];
+    const bool out_of = !held(pid);
+    const int64_t ph = (int64_t)(out_of ? 0 : pid) * v.hkv + h;
+    const float ks = out_of ? __builtin_nanf("") : v.ks[ph] * p.scale2, vs = v.vs[ph];
+    // this wave's copies have landed; behind the barrier everyone's have, and nobody
+    // reads the other stage any more
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    pid = next;
+    if (st + 1 < st1) {
+      copy(st + 1, held(pid) ? pid : 0, (st + 1 - st0) & 1);
+      next = st + 2 < st1 ? page_of(st + 2) : 0;
+    }
+    if (st >= wst1) continue;
+    // two chains of dependent products for the scores, four for the output
+    typename E::acc_t s[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) s[t][j] = 0.0f;
+#pragma unroll
+    for (int x = 0; x < E::NX; ++x) {
+      uint4 kr[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        kr[t] = *(const uint4*)(sg + kat[x] + 32 * t * D);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) s[t] = E::mma_q(E::MQ::from_fp8(kr[t].x, kr[t].y), a.qf[x][0], s[t]);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) s[t] = E::mma_q(E::MQ::from_fp8(kr[t].z, kr[t].w), a.qf[x][1], s[t]);
+    }
+    half8_t pf[4];
+    a.weigh(s, q, t0, ks, vs, out_of, half, pf);
+    const int end = out_of ? 0 : ctx;
+    const bool cut = t0 + kStep > end;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      uint4 vr[ND];
+#pragma unroll
+      for (int i = 0; i < ND; ++i) vr[i] = *(const uint4*)(sg + vat[t] + 32 * i * 64);
+      if (cut) {
+#pragma unroll
+        for (int i = 0; i < ND; ++i) E::trim(vr[i], end - (t0 + 32 * t + 16 * half));
+      }
+#pragma unroll
+      for (int i = 0; i < ND; ++i) a.o[i] = E::mma_v(E::MV::from_fp8(vr[i].x, vr[i].y), pf[2 * t], a.o[i]);
+#pragma unroll
+      for (int i = 0; i < ND; ++i) a.o[i] = E::mma_v(E::MV::from_fp8(vr[i].z, vr[i].w), pf[2 * t + 1], a.o[i]);
+    }
+  }
   a.finish();
   if (c >= cols) return;
   if (S == 1) {
@@ -621,11 +756,8 @@ __global__ __launch_bounds__(256, 2) void attn_kv8_tile_kernel(AttnP p) {
     for (int i = 0; i < ND; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        uint32_t x[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          x[e] = (uint32_t)f2act(a.o[i][4 * j + 2 * e] * inv, BF) |
-                 (uint32_t)f2act(a.o[i][4 * j + 2 * e + 1] * inv, BF) << 16;
+        const uint32_t x[2] = {pack2<BF>(a.o[i][4 * j] * inv, a.o[i][4 * j + 1] * inv),
+                               pack2<BF>(a.o[i][4 * j + 2] * inv, a.o[i][4 * j + 3] * inv)};
         *(uint2*)(op + 32 * i + 8 * j) = make_uint2(x[0], x[1]);
       }
     if (p.lse && half == 0)

@@ -245,7 +245,7 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(AppendP p) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float nan = __builtin_nanf("");
-        o[i] = (uint32_t)f2act(out_of ? nan : y[2 * i], BF) | (uint32_t)f2act(out_of ? nan : y[2 * i + 1], BF) << 16;
+        o[i] = out_of ? pack2<BF>(nan, nan) : pack2<BF>(y[2 * i], y[2 * i + 1]);
       }
       *(uint2*)(dst + ru.a) = make_uint2(o[0], o[1]);
       *(uint2*)(dst + ru.b) = make_uint2(o[2], o[3]);

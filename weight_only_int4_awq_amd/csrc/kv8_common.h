@@ -109,5 +109,12 @@ template <bool BF>
 __device__ __forceinline__ float act2f(uint16_t b) {
   return BF ? bf2f(b) : h2f(b);
 }
+// two values rounded once each (nearest, ties to even) to fp16 or bf16
+template <bool BF>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (BF) return __builtin_bit_cast(uint32_t, (bf16x2_t){(__bf16)a, (__bf16)b});
+  else return __builtin_bit_cast(uint32_t, (half2_t){(half_t)a, (half_t)b});
+}
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
 }  // namespace awq
