@@ -157,15 +157,15 @@ struct Wave {
   __device__ __forceinline__ void ask(const Kv8View& v, float scale2, const Seq& q, int h, int st, int lane) {
     const int c = lane % C, g = lane / C, t0 = st * kStep;
     const int krow = W ? 16 * (c >> 2 & 1) + 4 * (c >> 3) + (c & 3) : 16 * (c >> 2) + (c & 3);
-    int pid = uniform(q.bt[t0 >> v.shift]);
+    int pid = scalar_load(q.bt + (t0 >> v.shift));
     bad = q.over || (uint32_t)pid >= (uint32_t)v.pages;
     pid = bad ? 0 : pid;
     const int64_t ph = (int64_t)pid * v.hkv + h;
     const int slot0 = t0 & ((1 << v.shift) - 1);
     const uint8_t* kp = v.kc + ((ph << v.shift) + slot0) * D;
     vp = v.vc + ((ph * D) << v.shift) + slot0;
-    ks = bad ? __builtin_nanf("") : v.ks[ph] * scale2;
-    vs = v.vs[ph];
+    ks = bad ? __builtin_nanf("") : scalar_load(v.ks + ph) * scale2;
+    vs = scalar_load(v.vs + ph);
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -685,7 +685,7 @@ __global__ __launch_bounds__(256, 2) void attn_kv8_tile_kernel(AttnP p) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) vat[t] = (int)sizeof(stage[0].k) + 16 * T::vat(c, 2 * t + half);
   }
-  auto page_of = [&](int st) { return uniform(q.bt[(st * kStep) >> v.shift]); };
+  auto page_of = [&](int st) { return scalar_load(q.bt + ((st * kStep) >> v.shift)); };
   const uint32_t pages = (uint32_t)v.pages;                     // below 2^31
   auto held = [&](int pid) { return !q.over && (uint32_t)pid < pages; };
   int pid = 0, next = 0;
@@ -699,7 +699,7 @@ __global__ __launch_bounds__(256, 2) void attn_kv8_tile_kernel(AttnP p) {
     const char* sg = (const char*)&stage[(st - st0) & 1];
     const bool out_of = !held(pid);
     const int64_t ph = (int64_t)(out_of ? 0 : pid) * v.hkv + h;
-    const float ks = out_of ? __builtin_nanf("") : v.ks[ph] * p.scale2, vs = v.vs[ph];
+    const float ks = out_of ? __builtin_nanf("") : scalar_load(v.ks + ph) * p.scale2, vs = scalar_load(v.vs + ph);
     // this wave's copies have landed; behind the barrier everyone's have, and nobody
     // reads the other stage any more
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");

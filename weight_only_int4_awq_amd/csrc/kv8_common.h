@@ -116,5 +116,15 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   else return __builtin_bit_cast(uint32_t, (half2_t){(half_t)a, (half_t)b});
 }
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+// A value at an address that is the same in all lanes and that the launch does not
+// write, by a scalar load: it waits for no vector load asked for before it.
+template <class T>
+__device__ __forceinline__ T scalar_load(const T* p) {
+  typedef const T __attribute__((address_space(4))) constant_t;
+  const uint64_t a = (uint64_t)(uintptr_t)p;
+  const uint64_t u = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a) |
+                     (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)) << 32;
+  return *(constant_t*)u;
+}
 
 }  // namespace awq
