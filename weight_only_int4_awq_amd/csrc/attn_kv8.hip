@@ -173,12 +173,13 @@ struct Wave {
         kr[t][x] = load16<ONCE>(kp + ((W ? 32 : 4) * t + krow) * D + 16 * GR * x + 16 * g);
   }
 
-  // Scores of one step to softmax weights: the running maximum, l and O brought
-  // up to date, the weights in pf as the value product's operand.
-  __device__ __forceinline__ void weigh(acc_t* s, const Seq& q, int t0, float k1, float v1, bool out_of, int g,
-                                        half8_t* pf) {
-    float a = k1, z = __builtin_amdgcn_logf(v1);
-    const float rv = __builtin_amdgcn_rcpf(v1);
+  // Scores of one step to softmax weights.  level(): masks, moves m where it has to,
+  // and leaves the scores' factor and addend in a and z; weights(): the weights in pf
+  // as the value product's operand, their sum in l.
+  __device__ __forceinline__ void level(acc_t* s, const Seq& q, int t0, float k1, float v1, bool out_of, int g,
+                                        float& a, float& z) {
+    a = k1;
+    z = __builtin_amdgcn_logf(v1);
     if (t0 + kStep - 1 > q.first || out_of) {
 #pragma unroll
       for (int t = 0; t < NT; ++t)
@@ -205,6 +206,8 @@ struct Wave {
       for (int i = 0; i < ND; ++i) o[i] *= f;
     }
     z -= m;
+  }
+  __device__ __forceinline__ void weights(const acc_t* s, float a, float z, float v1, half8_t* pf) {
     float sum = 0.0f;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -214,7 +217,7 @@ struct Wave {
         sum += e;
         pf[(t * NJ + j) / 8][(t * NJ + j) % 8] = (half_t)e;
       }
-    l = __builtin_fmaf(sum, rv, l);
+    l = __builtin_fmaf(sum, __builtin_amdgcn_rcpf(v1), l);
   }
 
   // Codes of 16 tokens, `left` of them before the sequence's end: slots behind it, and
@@ -255,7 +258,9 @@ struct Wave {
       const bool out_of = bad;
       if (st + stride < st1) ask(v, scale2, q, h, st + stride, lane);
       half8_t pf[NT * NJ / 8];
-      weigh(s, q, t0, k1, v1, out_of, g, pf);
+      float a, z;
+      level(s, q, t0, k1, v1, out_of, g, a, z);
+      weights(s, a, z, v1, pf);
       if (t0 + kStep > (out_of ? 0 : q.ctx)) {
 #pragma unroll
         for (int i = 0; i < ND; ++i)
@@ -604,16 +609,17 @@ struct Stage {
   static __device__ __forceinline__ int vat(int d, int j) { return d * 4 + (j ^ (d >> 1 & 3)); }
 };
 
-// One 16-byte global -> LDS copy per lane: lane i writes LDS bytes base + 16 i .. +15.
+// One 16-byte global -> LDS copy per lane, from src + off: lane i writes LDS bytes
+// base + 16 i .. +15.
 // From inline asm, so that the compiler leaves the waits to the caller: it would
 // drain every outstanding copy before any read of the array.  M0 is the
 // compiler's only to address LDS copies of its own; there are none here.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void lds_copy16(const void* src, uint32_t base) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+__device__ __forceinline__ void lds_copy16(const void* src, uint32_t off, uint32_t base) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                :
-               : "v"(src), "s"(base)
+               : "v"(off), "s"(src), "s"(base)
                : "memory", "m0");
 }
 #pragma clang diagnostic pop
@@ -656,24 +662,36 @@ __global__ __launch_bounds__(256, 2) void attn_kv8_tile_kernel(AttnP p) {
   a.clear();
 
   // this wave's pieces of a step: chunks of 64 pieces, every fourth
+  constexpr int CK = T::KP / NW, CV = D / 16 / NW;
+  uint32_t koff[CK], voff[CV];
+#pragma unroll
+  for (int i = 0; i < CK; ++i) {
+    const int at = (wave + NW * i) * 64 + lane, r = at / T::KP;
+    koff[i] = r * D + 16 * (at % T::KP ^ T::key(r));
+  }
+#pragma unroll
+  for (int i = 0; i < CV; ++i) {
+    const int at = (wave + NW * i) * 64 + lane, d = at / 4;
+    voff[i] = (d << v.shift) + 16 * (at % 4 ^ (d >> 1 & 3));
+  }
   const int smask = (1 << v.shift) - 1;
-  auto copy = [&](int st, int pid, int to) {
-    const int64_t ph = (int64_t)pid * v.hkv + h;
-    const int slot0 = (st * kStep) & smask;
-    const uint8_t* kp = v.kc + ((ph << v.shift) + slot0) * D;
-    const uint8_t* vp = v.vc + ((ph * D) << v.shift) + slot0;
-    // an LDS address is the low half of its flat one
-    const uint32_t kb = (uint32_t)(uintptr_t)&stage[to].k[0], vb = (uint32_t)(uintptr_t)&stage[to].v[0];
+  const uint32_t pages = (uint32_t)v.pages;                     // below 2^31
+  // an LDS address is the low half of its flat one
+  const uint32_t lds0 = uniform((int)(uint32_t)(uintptr_t)&stage[0]) + wave * 1024;
+  auto page_of = [&](int st) { return st < st1 ? scalar_load(q.bt + ((st * kStep) >> v.shift)) : 0; };
+  auto held = [&](int pid) { return !q.over && (uint32_t)pid < pages; };
+  auto head_of = [&](int pid) { return (int64_t)(held(pid) ? pid : 0) * v.hkv + h; };
+  auto copy_k = [&](int st, int pid) {
+    const uint8_t* kp = v.kc + ((head_of(pid) << v.shift) + ((st * kStep) & smask)) * D;
+    const uint32_t base = lds0 + (st & 1) * (uint32_t)sizeof(T);
 #pragma unroll
-    for (int i = 0; i < T::KP / NW; ++i) {
-      const int at = (wave + NW * i) * 64 + lane, r = at / T::KP, j = at % T::KP ^ T::key(r);
-      lds_copy16(kp + r * D + 16 * j, uniform(kb + (wave + NW * i) * 1024));
-    }
+    for (int i = 0; i < CK; ++i) lds_copy16(kp, koff[i], base + NW * 1024 * i);
+  };
+  auto copy_v = [&](int st, int pid) {
+    const uint8_t* vp = v.vc + ((head_of(pid) * D) << v.shift) + ((st * kStep) & smask);
+    const uint32_t base = lds0 + (st & 1) * (uint32_t)sizeof(T) + (uint32_t)sizeof(stage[0].k);
 #pragma unroll
-    for (int i = 0; i < D / 16 / NW; ++i) {
-      const int at = (wave + NW * i) * 64 + lane, d = at / 4, j = at % 4 ^ (d >> 1 & 3);
-      lds_copy16(vp + (d << v.shift) + 16 * j, uniform(vb + (wave + NW * i) * 1024));
-    }
+    for (int i = 0; i < CV; ++i) lds_copy16(vp, voff[i], base + NW * 1024 * i);
   };
   // where this lane's operands lie in a stage, in bytes: tile t of the keys and tile i of
   // the values are a constant further on
@@ -685,33 +703,9 @@ __global__ __launch_bounds__(256, 2) void attn_kv8_tile_kernel(AttnP p) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) vat[t] = (int)sizeof(stage[0].k) + 16 * T::vat(c, 2 * t + half);
   }
-  auto page_of = [&](int st) { return scalar_load(q.bt + ((st * kStep) >> v.shift)); };
-  const uint32_t pages = (uint32_t)v.pages;                     // below 2^31
-  auto held = [&](int pid) { return !q.over && (uint32_t)pid < pages; };
-  int pid = 0, next = 0;
-  if (st0 < st1) {
-    pid = page_of(st0);
-    copy(st0, held(pid) ? pid : 0, 0);
-    next = st0 + 1 < st1 ? page_of(st0 + 1) : 0;
-  }
-  for (int st = st0; st < st1; ++st) {
-    const int t0 = st * kStep;
-    const char* sg = (const char*)&stage[(st - st0) & 1];
-    const bool out_of = !held(pid);
-    const int64_t ph = (int64_t)(out_of ? 0 : pid) * v.hkv + h;
-    const float ks = out_of ? __builtin_nanf("") : scalar_load(v.ks + ph) * p.scale2, vs = scalar_load(v.vs + ph);
-    // this wave's copies have landed; behind the barrier everyone's have, and nobody
-    // reads the other stage any more
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    pid = next;
-    if (st + 1 < st1) {
-      copy(st + 1, held(pid) ? pid : 0, (st + 1 - st0) & 1);
-      next = st + 2 < st1 ? page_of(st + 2) : 0;
-    }
-    if (st >= wst1) continue;
-    // two chains of dependent products for the scores, four for the output
-    typename E::acc_t s[2];
+  // two chains of dependent products
+  auto scores = [&](int st, typename E::acc_t* s) {
+    const char* sg = (const char*)&stage[st & 1];
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -720,31 +714,70 @@ __global__ __launch_bounds__(256, 2) void attn_kv8_tile_kernel(AttnP p) {
     for (int x = 0; x < E::NX; ++x) {
       uint4 kr[2];
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-        kr[t] = *(const uint4*)(sg + kat[x] + 32 * t * D);
+      for (int t = 0; t < 2; ++t) kr[t] = *(const uint4*)(sg + kat[x] + 32 * t * D);
 #pragma unroll
       for (int t = 0; t < 2; ++t) s[t] = E::mma_q(E::MQ::from_fp8(kr[t].x, kr[t].y), a.qf[x][0], s[t]);
 #pragma unroll
       for (int t = 0; t < 2; ++t) s[t] = E::mma_q(E::MQ::from_fp8(kr[t].z, kr[t].w), a.qf[x][1], s[t]);
     }
-    half8_t pf[4];
-    a.weigh(s, q, t0, ks, vs, out_of, half, pf);
+  };
+  // behind it everyone's copies have landed, and nobody reads what was read before
+  auto meet = [&]() {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+  };
+
+  // The scores run a step ahead of the softmax and the value product, so that their
+  // MFMAs have other work to hide behind: step st + 1's keys and step st's values
+  // are in LDS at a time, step st + 2's keys and st + 1's values on their way.
+  int pid = page_of(st0), pid1 = page_of(st0 + 1), pid2 = page_of(st0 + 2);
+  typename E::acc_t s[2];
+  if (st0 < st1) {
+    copy_k(st0, pid);
+    meet();
+    if (st0 + 1 < st1) copy_k(st0 + 1, pid1);
+    copy_v(st0, pid);
+    scores(st0, s);
+  }
+  typename E::acc_t ahead[2];
+  auto step = [&](int st, typename E::acc_t* now, typename E::acc_t* then) {
+    const int t0 = st * kStep;
+    const bool out_of = !held(pid);
+    const float ks = out_of ? __builtin_nanf("") : scalar_load(v.ks + head_of(pid)) * p.scale2;
+    const float vs = scalar_load(v.vs + head_of(pid));
+    meet();
+    if (st + 1 < st1) copy_v(st + 1, pid1);
+    if (st + 2 < st1) copy_k(st + 2, pid2);
+    pid = pid1;
+    pid1 = pid2;
+    pid2 = page_of(st + 3);
     const int end = out_of ? 0 : ctx;
-    const bool cut = t0 + kStep > end;
+    if (t0 + kStep > end) {                    // once in a unit, at its end
+      for (int i = threadIdx.x; i < D * 4; i += 64 * NW)
+        E::trim(stage[st & 1].v[i], end - (t0 + 16 * (i % 4 ^ (i >> 3 & 3))));
+      __syncthreads();
+    }
+    if (st >= wst1) return;
+    half8_t pf[4];
+    float f, z;
+    a.level(now, q, t0, ks, vs, out_of, half, f, z);
+    scores(st + 1, then);                      // of the last step: unused
+    a.weights(now, f, z, vs, pf);
+    const char* sg = (const char*)&stage[st & 1];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       uint4 vr[ND];
 #pragma unroll
       for (int i = 0; i < ND; ++i) vr[i] = *(const uint4*)(sg + vat[t] + 32 * i * 64);
-      if (cut) {
-#pragma unroll
-        for (int i = 0; i < ND; ++i) E::trim(vr[i], end - (t0 + 32 * t + 16 * half));
-      }
 #pragma unroll
       for (int i = 0; i < ND; ++i) a.o[i] = E::mma_v(E::MV::from_fp8(vr[i].x, vr[i].y), pf[2 * t], a.o[i]);
 #pragma unroll
       for (int i = 0; i < ND; ++i) a.o[i] = E::mma_v(E::MV::from_fp8(vr[i].z, vr[i].w), pf[2 * t + 1], a.o[i]);
     }
+  };
+  for (int st = st0; st < st1; st += 2) {
+    step(st, s, ahead);
+    if (st + 1 < st1) step(st + 1, ahead, s);
   }
   a.finish();
   if (c >= cols) return;
