@@ -522,11 +522,14 @@ struct Unit {
 
 // The plan, computed by every wave from the device's own lengths (a captured
 // graph replays with new ones): tiles of TC columns; a sequence's tiles are cut
-// into S = ceil(steps / chunk) units, chunk = total steps over the target.
-// Units of sequences with S > 1 have partial slots, numbered in the same
-// order; there are fewer than 2 * target of them, as S > 1 needs
-// steps > chunk and then ceil(steps / chunk) < 2 steps / chunk.
-// JOIN: u counts the tiles of the split sequences (fewer than target) instead.
+// into S = ceil(steps / chunk) units, chunk = total steps over the target, and the
+// sequences with longer units come first, so that the last work-groups to start
+// are short.  The total counts what causal tiles see, never less than half of
+// their steps, so there are at most 2 * target units and one for each tile.
+// Units of sequences with S > 1 have partial slots, numbered in the same order;
+// fewer than 4 * target, as S > 1 needs steps > chunk and then
+// ceil(steps / chunk) < 2 steps / chunk.
+// JOIN: u counts the tiles of the split sequences (fewer than 2 * target) instead.
 // Everything returned is the same in all lanes.
 template <int TC, bool JOIN>
 __device__ __forceinline__ bool find_unit(const AttnP& p, int u, int lane, Unit& w) {
@@ -547,30 +550,41 @@ __device__ __forceinline__ bool find_unit(const AttnP& p, int u, int lane, Unit&
   uint64_t total = 0;
   for (int i0 = 0; i0 < v.b; i0 += 64) {
     load(i0 + lane, r, tiles, steps);
-    total += (uint64_t)tiles * steps;
+    // a causal tile sees on average what its sequence's middle row sees
+    const int seen = steps - r.n / (2 * kStep), half = (steps + 1) / 2;
+    total += (uint64_t)tiles * (seen > half ? seen : half);
   }
   // below 2^51 for ascending cu: two sums of 32 bits
   const uint32_t lo = __builtin_amdgcn_readlane(wave_scan((int)(total & 0x1FFFFFFu)), 63);
   const uint32_t hi = __builtin_amdgcn_readlane(wave_scan((int)(total >> 25)), 63);
   const double per = __builtin_ceil(((double)hi * 33554432.0 + (double)lo) / (double)p.target);
   const int chunk = per > (double)p.min_steps ? (per < 1e9 ? (int)per : 1000000000) : p.min_steps;
-  auto units_of = [&](int steps) {
-    // a short context is not worth a second launch's work
-    const int S = steps <= p.whole ? 1 : (steps + chunk - 1) / chunk;
-    return S < 1 ? 1 : S;
-  };
   int before = 0, slots = 0;
   for (int i0 = 0; i0 < v.b; i0 += 64) {
     if (v.b > 64) load(i0 + lane, r, tiles, steps);
-    const int S = units_of(steps);
+    // a short context is not worth a second launch's work
+    int S = steps <= p.whole ? 1 : (steps + chunk - 1) / chunk;
+    S = S < 1 ? 1 : S;
     const int held = S > 1 ? tiles * S : 0;
     const int mine = JOIN ? (S > 1 ? tiles : 0) : tiles * S;
-    const int incl = wave_scan(mine), hincl = wave_scan(held);
-    const int all = __builtin_amdgcn_readlane(incl, 63);
+    // this lane's units and slots come behind those of the sequences with longer units
+    const int len = steps / S;
+    int from = 0, sfrom = 0;
+    const int live = v.b - i0 < 64 ? v.b - i0 : 64;
+    for (int j = 0; j < live; ++j) {
+      const int other = __builtin_amdgcn_readlane(len, j);
+      if (other > len || (other == len && j < lane)) {
+        from += __builtin_amdgcn_readlane(mine, j);
+        sfrom += __builtin_amdgcn_readlane(held, j);
+      }
+    }
+    const int all = __builtin_amdgcn_readlane(wave_scan(mine), 63);
     if (u - before < all) {
-      int l = __popcll(__ballot(incl <= u - before));
-      l = l < 63 ? l : 63;
-      const int at = u - before - __builtin_amdgcn_readlane(incl - mine, l);
+      const int x = u - before;
+      const uint64_t hit = __ballot(x >= from && x < from + mine);
+      if (!hit) return false;                // cannot be for ascending cu
+      const int l = __builtin_ctzll(hit);
+      const int at = x - __builtin_amdgcn_readlane(from, l);
       w.b = i0 + l;
       w.S = __builtin_amdgcn_readlane(S, l);
       w.r.r0 = __builtin_amdgcn_readlane(r.r0, l);
@@ -580,13 +594,13 @@ __device__ __forceinline__ bool find_unit(const AttnP& p, int u, int lane, Unit&
       const int order = JOIN ? at : at / w.S;
       w.s = JOIN ? 0 : at % w.S;
       w.tile = nt - 1 - order;               // later rows see more: the longest first
-      w.slot = slots + __builtin_amdgcn_readlane(hincl - held, l) + order * w.S + w.s;
+      w.slot = slots + __builtin_amdgcn_readlane(sfrom, l) + order * w.S + w.s;
       // always so for ascending cu; whatever else the array holds stays in bounds
       const int top = w.S > 1 ? (JOIN ? w.slot + w.S : w.slot + 1) : 0;
       return w.tile >= 0 && w.tile < nt && w.slot >= 0 && top <= p.slots;
     }
     before += all;
-    slots += __builtin_amdgcn_readlane(hincl, 63);
+    slots += __builtin_amdgcn_readlane(wave_scan(held), 63);
   }
   return false;
 }
@@ -732,6 +746,9 @@ __global__ __launch_bounds__(256, 2) void attn_kv8_tile_kernel(AttnP p) {
   // are in LDS at a time, step st + 2's keys and st + 1's values on their way.
   int pid = page_of(st0), pid1 = page_of(st0 + 1), pid2 = page_of(st0 + 2);
   typename E::acc_t s[2];
+  // the queries have come: the compiler, which does not see the copies, would
+  // otherwise wait for them inside the loop, and so for the copies asked for last
+  __builtin_amdgcn_s_waitcnt(0);
   if (st0 < st1) {
     copy_k(st0, pid);
     meet();
@@ -938,13 +955,13 @@ Plan plan_of(int64_t b, int64_t rows, int32_t hq, int32_t hkv, int32_t d, int32_
   } else {
     p.whole = 16;
     p.min_steps = 8;
-    // units of causal tiles differ in length: four per CU even that out (prompt
-    // chunks: 249 us, 304 with two, 250 with eight)
-    p.target = hkv < 1024 ? 1024 / hkv : 1;
+    // two work-groups on each CU
+    const int64_t total = 512;
+    p.target = hkv < total ? (int)(total / hkv) : 1;
     const int64_t most = steps <= p.whole ? 1 : (steps + p.min_steps - 1) / p.min_steps;
-    p.groups = p.target + tiles;
+    p.groups = 2 * p.target + tiles;
     if (most <= p.groups / tiles) p.groups = tiles * most;
-    p.slots = most > 1 ? (2 * (int64_t)p.target < tiles * most ? 2 * (int64_t)p.target : tiles * most) : 0;
+    p.slots = most > 1 ? (4 * (int64_t)p.target < tiles * most ? 4 * (int64_t)p.target : tiles * most) : 0;
     p.joins = (int)(tiles < p.slots / 2 ? tiles : p.slots / 2);
     p.z = 4;
   }
