@@ -44,6 +44,7 @@ struct AttnP {
   int32_t slots;                     // partial slots per head in the workspace
   float* part;                       // partial O [slot][hkv][TC][D], then their (m, l)
   float* part_ml;
+  int4* rec;                         // line: what partial slot [k][first, last] of a head holds
 };
 
 // Results of one column's channels d .. d + 3: O / l, and the lse from channel 0.
@@ -382,7 +383,11 @@ struct Stretch {
 // Tiles of C columns; the NW waves of a work-group take a tile's steps in turn and
 // are joined in LDS at the tile's end, or at the stretch's: a tile that a stretch
 // covers only in part leaves its O, m and l in the workspace, in slot 2 k of work-group k
-// if the part begins the stretch, else in 2 k + 1.
+// if the part begins the stretch, else in 2 k + 1; and a record of the slot (the same for
+// every head, so head 0 writes it): row, rows, tile, and kBegins where the part has the
+// tile's first steps, kEnds where it has the last, kHeld where the slot holds anything.
+constexpr int kHeld = 1, kBegins = 2, kEnds = 4;
+
 template <int D, bool BF, int C, bool ONCE>
 __global__ __launch_bounds__(512, 2) void attn_kv8_line_kernel(AttnP p) {
   constexpr int NW = 8;
@@ -390,6 +395,11 @@ __global__ __launch_bounds__(512, 2) void attn_kv8_line_kernel(AttnP p) {
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const Kv8View& v = p.v;
   const int h = blockIdx.x % v.hkv, k = blockIdx.x / v.hkv, G = p.G;
+  const bool notes = p.rec && h == 0 && threadIdx.x == 0;
+  if (notes) {
+    p.rec[2 * k].w = 0;
+    p.rec[2 * k + 1].w = 0;
+  }
   Stretch<C> y(p, lane);
   const uint32_t x0 = y.start(k), x1 = y.start(k + 1);
   if (x0 >= x1) return;
@@ -452,7 +462,10 @@ __global__ __launch_bounds__(512, 2) void attn_kv8_line_kernel(AttnP p) {
       begin();
     }
     __syncthreads();
-    const bool whole = from == done.at && x <= x1;
+    const bool begins = from == done.at, ends = x <= x1, whole = begins && ends;
+    if (notes && !whole)
+      p.rec[2 * k + (from == x0 ? 0 : 1)] =
+          make_int4(done.r.r0, done.r.n, done.tile, kHeld | (begins ? kBegins : 0) | (ends ? kEnds : 0));
     // a thread: 4 channels of one column
     for (int it = threadIdx.x; it < dcols * (D / 4); it += 64 * NW) {
       const int jc = it / (D / 4), d = it % (D / 4) * 4;
@@ -487,28 +500,34 @@ __global__ __launch_bounds__(512, 2) void attn_kv8_line_kernel(AttnP p) {
   }
 }
 
-// The parts of a tile that stretches share: start(k) lies inside it and start(k - 1)
-// does not.  Its parts are work-group k - 1's last and the first ones of k, k + 1, ...
-// that begin before its end.
-template <int C>
+// The parts of the tile that work-group k - 1 begins and work-group k goes on with:
+// k - 1's last and the first ones of k, k + 1, ... up to the one that ends it.
 __device__ __forceinline__ bool line_parts(const AttnP& p, int k, int lane, Parts& w) {
-  Stretch<C> y(p, lane);
-  const uint32_t x = y.start(k);
-  if (x >= y.line.all) return false;
-  const Place t = y.place(x);
-  if (t.b < 0 || x == t.at) return false;
-  const uint32_t before = y.start(k - 1);
-  if (before > t.at) return false;
-  const uint32_t end = t.at + t.steps;
-  int last = (int)((end - 1) / y.line.per);
-  if (y.start(last) >= end) --last;
-  w.first = 2 * (k - 1) + (before == t.at ? 0 : 1);
+  const int4 a = p.rec[2 * k - 2], b = p.rec[2 * k - 1];
+  // a lane for each of k, k + 1, ...
+  int n = 0;
+  for (int i0 = k; i0 < p.target; i0 += 64) {
+    const int f = i0 + lane < p.target ? p.rec[2 * (i0 + lane)].w : kHeld | kBegins;
+    const uint64_t stop = __ballot((f & kEnds) != 0 || (f & kBegins) != 0 || f == 0);
+    if (stop) {
+      const int l = __builtin_ctzll(stop);
+      const int last = __builtin_amdgcn_readlane(f, l);
+      if (!(last & kEnds) || last & kBegins) return false;      // k does not go on with anything
+      n += l + 1;
+      break;
+    }
+    n += 64;
+  }
+  const bool second = (b.w & (kBegins | kEnds)) == kBegins;
+  if (!second && (a.w & (kBegins | kEnds)) != kBegins) return false;
+  const int4 t = second ? b : a;
+  w.first = 2 * (k - 1) + (second ? 1 : 0);
   w.next = 2 * k;
   w.step = 2;
-  w.count = last - k + 2;
-  w.tile = t.tile;
-  w.r = t.r;
-  return last < p.target;
+  w.count = n + 1;
+  w.tile = t.z;
+  w.r = SeqRows{t.x, t.y, 0};
+  return n > 0;
 }
 
 // ---------------------------------------------------------------- many columns
@@ -848,7 +867,7 @@ __global__ __launch_bounds__(256) void attn_kv8_join_kernel(AttnP p, int Z) {
   const int hkv = p.v.hkv, h = blockIdx.x % hkv, z = blockIdx.x / hkv % Z;
   Parts w;
   if (!(TC == 128 ? unit_parts<TC>(p, blockIdx.x / hkv / Z, lane, w)
-                  : line_parts<TC == 128 ? 16 : TC>(p, blockIdx.x / hkv / Z + 1, lane, w)))
+                  : line_parts(p, blockIdx.x / hkv / Z + 1, lane, w)))
     return;
   const int S = w.count, G = p.G;
   auto slot = [&](int i) { return ((int64_t)(i ? w.next + (i - 1) * w.step : w.first) * hkv + h) * TC; };
@@ -924,7 +943,7 @@ struct Plan {
   int64_t groups;                    // work-groups per head
   int64_t slots;                     // partial slots per head (0: nothing can be split)
   int joins, z;                      // tiles per head to join, at most; work-groups for each
-  size_t off_ml, bytes;
+  size_t off_ml, off_rec, bytes;
 };
 
 Plan plan_of(int64_t b, int64_t rows, int32_t hq, int32_t hkv, int32_t d, int32_t page, int64_t max_pages,
@@ -968,7 +987,8 @@ Plan plan_of(int64_t b, int64_t rows, int32_t hq, int32_t hkv, int32_t d, int32_
   p.once = max_q * G <= p.tc;
   const size_t cols = (size_t)p.slots * hkv * p.tc;
   p.off_ml = cols * d * sizeof(float);
-  p.bytes = (p.off_ml + cols * 2 * sizeof(float) + 255) / 256 * 256;
+  p.off_rec = (p.off_ml + cols * 2 * sizeof(float) + 255) / 256 * 256;
+  p.bytes = p.tc < 128 && p.slots ? p.off_rec + ((size_t)p.slots * sizeof(int4) + 255) / 256 * 256 : p.off_rec;
   return p;
 }
 
@@ -1022,6 +1042,7 @@ hipError_t launch_attn_kv8(const Kv8Args& a, const uint16_t* q, int64_t q_stride
   p.slots = (int32_t)pl.slots;
   p.part = (float*)scratch;
   p.part_ml = (float*)((char*)scratch + pl.off_ml);
+  p.rec = pl.tc < 128 && pl.slots ? (int4*)((char*)scratch + pl.off_rec) : nullptr;
   if (a.d == 64) return bf ? launch<64, true>(p, pl, stream) : launch<64, false>(p, pl, stream);
   return bf ? launch<128, true>(p, pl, stream) : launch<128, false>(p, pl, stream);
 }
