@@ -306,6 +306,21 @@ def test_attention(P, dt, new, ctx, hq, hkv, d, page, pad, known):
     check_attn(c, q, out, lse)
 
 
+@pytest.mark.parametrize("b", [65, 130])
+def test_attention_many_sequences_many_columns(P, b):
+    """More than 64 sequences in tiles of 128 columns, one of them long enough to be split."""
+    rng = np.random.default_rng(b)
+    new = rng.integers(0, 20, b)
+    new[3], new[b - 1] = 40, 33
+    ctx = new + rng.integers(0, 90, b)
+    ctx[b - 1] += 2500
+    c = Case(b + 7, "fp16", new, ctx, 4, 1, 64, 64)
+    c.upload()
+    q = c.act(4)
+    out, lse = run_attn(P, c, q.to(DEV), max_q=40)
+    check_attn(c, q, out, lse)
+
+
 @pytest.mark.parametrize("b", [63, 64, 65, 200])
 def test_attention_many_sequences(P, b):
     rng = np.random.default_rng(b)
@@ -394,6 +409,28 @@ def test_attention_peaked_and_scaled(P):
     q = c.act(4, 25.0)
     out, lse = run_attn(P, c, q.to(DEV), max_q=90, scale=0.2)
     check_attn(c, q, out, lse, scale=0.2)
+
+
+@pytest.mark.parametrize("new", [1, 3, 40])
+@pytest.mark.parametrize("gap", [12.0, 24.3])
+def test_attention_first_token_outweighs_all(P, new, gap):
+    """One token whose score exceeds every other by a factor of 2^gap, its v zero: the result is the
+    others' small share, which must keep its relative precision."""
+    c = Case(96, "fp16", [new], [3000], 4, 1, 128, 64)
+    c.kc[:] = 0
+    c.kc[c.bt[0, 0], 0, 0] = R.encode(np.full(128, 1.0))
+    c.ks[:] = 1.0
+    c.vc[:] = R.encode(np.full(c.vc.shape, 3.0))
+    c.vc[c.bt[0, 0], 0, :, 0] = 0
+    c.vs[:] = 1.0
+    c.upload()
+    q = torch.full((new, 4, 128), gap * np.log(2) / 128 ** 0.5).half()
+    out, lse = run_attn(P, c, q.to(DEV), max_q=new)
+    ref = R.attend(q.double().numpy(), c.kc, c.vc, c.ks, c.vs, c.bt, c.ctx, c.cu, 128 ** -0.5)
+    # scores of a few tens, so weights within 2^-14; fp16 outputs within half a step, or of a subnormal one
+    tol = 2.0 ** -13 * np.abs(ref[0]) + np.maximum(2.0 ** -11 * np.abs(ref[0]), 2.0 ** -25)
+    assert (np.abs(out.double().cpu().numpy() - ref[0]) <= tol).all()
+    check_attn(c, q, out, lse)
 
 
 def test_cache_beyond_32_bit_offsets(P):

@@ -11,13 +11,15 @@
 // group's query heads are further columns of the same key/value head: column
 // c of a sequence is row c / G, query head h * G + c % G.
 //
-// One pass with a running maximum.  The page's value scale goes into the
-// exponent: p' = exp2(s + log2 vs - m), O = sum p' vcode in units of 1,
-// l = sum p' / vs.  So p' carries exactly the weight of its token's contribution
-// to O whatever the scales are, and fp16 (11 bits) holds it with a relative
-// rounding of 2^-12 to 2^-11; S, O, m and l are fp32.  m moves only when a score
-// exceeds it by kLazy (a wave-wide vote), so most steps exchange nothing between
-// lanes and rescale nothing.
+// One pass with a running reference m.  The page's value scale goes into the
+// exponent: p' = exp2(s + log2 vs - m), O = sum p' vcode, l = sum p' / vs.  So p'
+// carries exactly the weight of its token's contribution to O whatever the scales
+// are.  S, O, m and l are fp32; p' enters the value product in fp16, with a relative
+// rounding of at most 2^-11: m lies 2^11 under the largest score it was set by, so
+// weights down to 2^-25 of the largest are normal fp16 numbers (a first token
+// that outweighs every other by 2^20 takes nothing from them).  m moves only when a
+// score would leave fp16 (a wave-wide vote), so most steps exchange nothing
+// between lanes and rescale nothing.
 #include "awq_internal.h"
 #include "kv8_common.h"
 
@@ -25,10 +27,11 @@ namespace awq {
 namespace {
 
 constexpr int kStep = 64;            // tokens of one step (a page holds whole steps)
-constexpr float kLazy = 8.0f;        // m moves for scores that exceed it by 8: p' <= 2^8, far inside fp16
+constexpr float kRoom = 11.0f;       // m is set to the largest score less 11 ...
+constexpr float kMost = 15.0f;       // ... and moves for scores that exceed it by 15: p' <= 2^15, inside fp16
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr float kNone = -1e30f;      // running maximum before any visible token
+constexpr float kNone = -1e30f;      // m before any visible token
 
 struct AttnP {
   Kv8View v;
@@ -196,10 +199,10 @@ struct Wave {
 #pragma unroll
       for (int j = 0; j < NJ; ++j) mx = __builtin_fmaxf(mx, s[t][j]);
     mx = __builtin_fmaf(mx, a, z);
-    if (__ballot(mx > m + kLazy)) {
+    if (__ballot(mx > m + kMost)) {
 #pragma unroll
       for (int x = C; x < 64; x <<= 1) mx = __builtin_fmaxf(mx, __shfl_xor(mx, x, 64));
-      const float mn = __builtin_fmaxf(m, mx);
+      const float mn = __builtin_fmaxf(m, mx - kRoom);
       const float f = __builtin_amdgcn_exp2f(m - mn);
       m = mn;
       l *= f;
@@ -327,6 +330,7 @@ struct Stretch {
       : p(p), lane(lane), cap((int)(((int64_t)p.v.max_pages << p.v.shift) / kStep)) {
     // below 2^31 for ascending cu (the host has seen to it)
     uint32_t sum = 0;
+#pragma unroll 4
     for (int i0 = 0; i0 < p.v.b; i0 += 64) {
       load(i0 + lane);
       sum += (uint32_t)tiles * (uint32_t)steps;
@@ -541,9 +545,9 @@ struct Unit {
 
 // The plan, computed by every wave from the device's own lengths (a captured
 // graph replays with new ones): tiles of TC columns; a sequence's tiles are cut
-// into S = ceil(steps / chunk) units, chunk = total steps over the target, and the
-// sequences with longer units come first, so that the last work-groups to start
-// are short.  The total counts what causal tiles see, never less than half of
+// into S = ceil(steps / chunk) units, chunk = total steps over the target, and (of up
+// to 64 sequences) those with longer units come first, so that the last
+// work-groups to start are short.  The total counts what causal tiles see, never less than half of
 // their steps, so there are at most 2 * target units and one for each tile.
 // Units of sequences with S > 1 have partial slots, numbered in the same order;
 // fewer than 4 * target, as S > 1 needs steps > chunk and then
@@ -586,18 +590,21 @@ __device__ __forceinline__ bool find_unit(const AttnP& p, int u, int lane, Unit&
     S = S < 1 ? 1 : S;
     const int held = S > 1 ? tiles * S : 0;
     const int mine = JOIN ? (S > 1 ? tiles : 0) : tiles * S;
-    // this lane's units and slots come behind those of the sequences with longer units
-    const int len = steps / S;
-    int from = 0, sfrom = 0;
-    const int live = v.b - i0 < 64 ? v.b - i0 : 64;
-    for (int j = 0; j < live; ++j) {
-      const int other = __builtin_amdgcn_readlane(len, j);
-      if (other > len || (other == len && j < lane)) {
-        from += __builtin_amdgcn_readlane(mine, j);
-        sfrom += __builtin_amdgcn_readlane(held, j);
+    const int incl = wave_scan(mine), hincl = wave_scan(held);
+    const int all = __builtin_amdgcn_readlane(incl, 63);
+    int from = incl - mine, sfrom = hincl - held;
+    if (v.b <= 64) {
+      // this lane's units and slots come behind those of the sequences with longer units
+      const int len = steps / S;
+      from = sfrom = 0;
+      for (int j = 0; j < v.b; ++j) {
+        const int other = __builtin_amdgcn_readlane(len, j);
+        const int add = __builtin_amdgcn_readlane(mine, j), sadd = __builtin_amdgcn_readlane(held, j);
+        const bool first = other > len || (other == len && j < lane);
+        from += first ? add : 0;
+        sfrom += first ? sadd : 0;
       }
     }
-    const int all = __builtin_amdgcn_readlane(wave_scan(mine), 63);
     if (u - before < all) {
       const int x = u - before;
       const uint64_t hit = __ballot(x >= from && x < from + mine);
@@ -619,7 +626,7 @@ __device__ __forceinline__ bool find_unit(const AttnP& p, int u, int lane, Unit&
       return w.tile >= 0 && w.tile < nt && w.slot >= 0 && top <= p.slots;
     }
     before += all;
-    slots += __builtin_amdgcn_readlane(wave_scan(held), 63);
+    slots += __builtin_amdgcn_readlane(hincl, 63);
   }
   return false;
 }
