@@ -310,8 +310,10 @@ template <int C>
 struct Stretch {
   const AttnP& p;
   const int lane, cap;
-  SeqRows r;               // of sequence i0 + lane, held for up to 64 sequences
-  int tiles, steps;
+  // the sequences w0 + lane, a window that moves along the line; it begins at wat
+  SeqRows r;
+  int tiles, steps, w0;
+  uint32_t wat;
   Line line;
 
   __device__ __forceinline__ void load(int i) {
@@ -324,6 +326,11 @@ struct Stretch {
       steps = steps < cap ? steps : cap;
       steps = steps < 1 ? 1 : steps;
     }
+  }
+  __device__ __forceinline__ void rewind() {
+    w0 = 0;
+    wat = 0;
+    load(lane);
   }
 
   __device__ __forceinline__ Stretch(const AttnP& p, int lane)
@@ -338,39 +345,43 @@ struct Stretch {
     line.all = __builtin_amdgcn_readlane(wave_scan((int)sum), 63);
     const uint32_t per = (uint32_t)(((uint64_t)line.all + p.target - 1) / (uint32_t)p.target);
     line.per = per > (uint32_t)p.min_steps ? per : p.min_steps;
+    w0 = 0;
+    wat = 0;
+    if (p.v.b > 64) load(lane);
   }
 
   // the tile that holds x < line.all
   __device__ __forceinline__ Place place(uint32_t x) {
-    uint32_t before = 0;
     Place w;
     w.b = -1;
-    for (int i0 = 0; i0 < p.v.b; i0 += 64) {
-      if (p.v.b > 64) load(i0 + lane);
+    if (x < wat) rewind();
+    for (;;) {
       const uint32_t mine = (uint32_t)tiles * (uint32_t)steps;
       const uint32_t incl = wave_scan((int)mine);
       const uint32_t sum = __builtin_amdgcn_readlane((int)incl, 63);
-      if (x - before < sum) {
-        int l = __popcll(__ballot(incl <= x - before));
+      if (x - wat < sum) {
+        int l = __popcll(__ballot(incl <= x - wat));
         l = l < 63 ? l : 63;
-        before += __builtin_amdgcn_readlane((int)(incl - mine), l);
+        const uint32_t in = x - wat - __builtin_amdgcn_readlane((int)(incl - mine), l);
         // always so for ascending cu; whatever else the array holds ends here
-        if (x - before >= (uint32_t)__builtin_amdgcn_readlane((int)mine, l)) return w;
-        w.b = i0 + l;
+        if (in >= (uint32_t)__builtin_amdgcn_readlane((int)mine, l)) return w;
+        w.b = w0 + l;
         w.steps = __builtin_amdgcn_readlane(steps, l);
         w.r.r0 = __builtin_amdgcn_readlane(r.r0, l);
         w.r.n = __builtin_amdgcn_readlane(r.n, l);
         w.r.ctx = __builtin_amdgcn_readlane(r.ctx, l);
-        w.tile = (int)((x - before) / (uint32_t)w.steps);
-        w.at = before + (uint32_t)w.tile * w.steps;
+        w.tile = (int)(in / (uint32_t)w.steps);
+        w.at = x - in + (uint32_t)w.tile * w.steps;
         return w;
       }
-      before += sum;
+      if (w0 + 64 >= p.v.b) return w;
+      w0 += 64;
+      wat += sum;
+      load(w0 + lane);
     }
-    return w;
   }
 
-  // where work-group k begins; with the tile that holds it where it is inside one
+  // where work-group k begins
   __device__ __forceinline__ uint32_t start(int k) {
     const uint64_t x64 = (uint64_t)k * line.per;
     if (k == 0 || x64 >= line.all) return k == 0 ? 0 : line.all;
@@ -392,9 +403,8 @@ struct Stretch {
 // tile's first steps, kEnds where it has the last, kHeld where the slot holds anything.
 constexpr int kHeld = 1, kBegins = 2, kEnds = 4;
 
-template <int D, bool BF, int C, bool ONCE>
-__global__ __launch_bounds__(512, 2) void attn_kv8_line_kernel(AttnP p) {
-  constexpr int NW = 8;
+template <int D, bool BF, int C, int NW, bool ONCE>
+__global__ __launch_bounds__(64 * NW, 2) void attn_kv8_line_kernel(AttnP p) {
   typedef Wave<D, BF, C, ONCE> E;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const Kv8View& v = p.v;
@@ -405,7 +415,9 @@ __global__ __launch_bounds__(512, 2) void attn_kv8_line_kernel(AttnP p) {
     p.rec[2 * k + 1].w = 0;
   }
   Stretch<C> y(p, lane);
-  const uint32_t x0 = y.start(k), x1 = y.start(k + 1);
+  const uint32_t x0 = y.start(k);
+  Stretch<C> ahead = y;                          // leaves y's window where the stretch begins
+  const uint32_t x1 = ahead.start(k + 1);
   if (x0 >= x1) return;
   const int64_t cap = (int64_t)v.max_pages << v.shift;
   const int c = lane % C, g = lane / C;
@@ -946,6 +958,7 @@ __global__ __launch_bounds__(256) void attn_kv8_join_kernel(AttnP p, int Z) {
 struct Plan {
   int tc;                            // columns of a tile: 16 and 32 lie on a line, 128 in units
   int target, min_steps, whole;
+  int waves;                         // of a work-group on the line
   bool once;                         // a sequence has one tile: its cache is read once
   int64_t groups;                    // work-groups per head
   int64_t slots;                     // partial slots per head (0: nothing can be split)
@@ -972,11 +985,14 @@ Plan plan_of(int64_t b, int64_t rows, int32_t hq, int32_t hkv, int32_t d, int32_
     // would need that launch (one sequence of 700 tokens: 8.6 us, 10.5 shared).
     p.whole = tiles * hkv < 64 ? 16 : 8;
     p.min_steps = 4;
-    // one work-group of eight waves on each CU
-    p.target = hkv < 256 ? 256 / hkv : 1;
+    // One work-group of eight waves on each CU; four of two waves where there are so
+    // many tiles that each CU has several whatever their lengths.
+    p.waves = tiles * hkv >= 2048 ? 2 : 8;
+    const int total = p.waves == 8 ? 256 : 1024;
+    p.target = hkv < total ? total / hkv : 1;
     p.groups = p.target;
     p.slots = steps > p.whole && p.target > 1 ? 2 * p.target : 0;
-    p.joins = p.target - 1;
+    p.joins = p.target - 1;                  // may be none
     p.z = (int)(max_q * G < 4 ? max_q * G : 4);
   } else {
     p.whole = 16;
@@ -1006,10 +1022,10 @@ size_t attn_kv8_scratch_bytes(int64_t b, int64_t rows, int32_t hq, int32_t hkv, 
   return plan_of(b, rows, hq, hkv, d, page, max_pages, max_q).bytes;
 }
 
-template <int D, bool BF, int C>
+template <int D, bool BF, int C, int NW>
 static void launch_line(const AttnP& p, const Plan& pl, unsigned grid, unsigned joins, hipStream_t stream) {
-  if (pl.once) attn_kv8_line_kernel<D, BF, C, true><<<grid, 512, 0, stream>>>(p);
-  else attn_kv8_line_kernel<D, BF, C, false><<<grid, 512, 0, stream>>>(p);
+  if (pl.once) attn_kv8_line_kernel<D, BF, C, NW, true><<<grid, 64 * NW, 0, stream>>>(p);
+  else attn_kv8_line_kernel<D, BF, C, NW, false><<<grid, 64 * NW, 0, stream>>>(p);
   if (pl.slots) attn_kv8_join_kernel<D, C, BF><<<joins, 256, 0, stream>>>(p, pl.z);
 }
 
@@ -1017,9 +1033,11 @@ template <int D, bool BF>
 static hipError_t launch(const AttnP& p, const Plan& pl, hipStream_t stream) {
   const unsigned grid = (unsigned)(pl.groups * p.v.hkv), joins = (unsigned)pl.joins * p.v.hkv * pl.z;
   if (pl.tc == 16) {
-    launch_line<D, BF, 16>(p, pl, grid, joins, stream);
+    if (pl.waves == 8) launch_line<D, BF, 16, 8>(p, pl, grid, joins, stream);
+    else launch_line<D, BF, 16, 2>(p, pl, grid, joins, stream);
   } else if (pl.tc == 32) {
-    launch_line<D, BF, 32>(p, pl, grid, joins, stream);
+    if (pl.waves == 8) launch_line<D, BF, 32, 8>(p, pl, grid, joins, stream);
+    else launch_line<D, BF, 32, 2>(p, pl, grid, joins, stream);
   } else {
     attn_kv8_tile_kernel<D, BF><<<grid, 256, 0, stream>>>(p);
     if (pl.slots) attn_kv8_join_kernel<D, 128, BF><<<joins, 256, 0, stream>>>(p, pl.z);
