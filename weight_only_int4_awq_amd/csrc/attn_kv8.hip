@@ -896,42 +896,71 @@ __global__ __launch_bounds__(256) void attn_kv8_join_kernel(AttnP p, int Z) {
   const int s1 = s0 + per < S ? s0 + per : S;
   __shared__ float so[4][D], sml[4][2];
   const int rowl = lane / LPR, d0 = (lane % LPR) * 4;
-  for (int j0 = shared ? z : 4 * z; j0 < cols; j0 += shared ? Z : 4 * Z) {
-    const int jc = shared ? j0 : j0 + wave;
-    const bool mine = jc < cols;
-    float top = kNone, sum = 0.0f;
-    float4 acc = make_float4(0, 0, 0, 0);
-    if (mine) {
-      for (int i = s0 + lane; i < s1; i += 64) top = __builtin_fmaxf(top, p.part_ml[2 * (slot(i) + jc)]);
+  // a column's parts s0 .. s1 - 1: the first rows are asked for with the statistics
+  auto fold = [&](int jc, float& top, float& sum, float4& acc) {
+    auto stats = [&](int i) {
+      return i < s1 ? *(const float2*)(p.part_ml + 2 * (slot(i) + jc)) : make_float2(kNone, 0.0f);
+    };
+    auto row = [&](int i) { return *(const float4*)(p.part + (slot(i) + jc) * D + d0); };
+    float2 ml = stats(s0 + lane);
+    float4 ahead[2];
 #pragma unroll
-      for (int o = 32; o; o >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, o, 64));
+    for (int t = 0; t < 2; ++t)
+      if (s0 + rowl + RPL * t < s1) ahead[t] = row(s0 + rowl + RPL * t);
+    top = ml.x;
+    for (int i0 = s0 + 64; i0 < s1; i0 += 64) top = __builtin_fmaxf(top, stats(i0 + lane).x);
+    top = wave_fold(top, kNone, [](float x, float y) { return __builtin_fmaxf(x, y); });
+    sum = 0.0f;
+    acc = make_float4(0, 0, 0, 0);
+    auto add = [&](float f, float4 x) {
+      acc.x = __builtin_fmaf(f, x.x, acc.x);
+      acc.y = __builtin_fmaf(f, x.y, acc.y);
+      acc.z = __builtin_fmaf(f, x.z, acc.z);
+      acc.w = __builtin_fmaf(f, x.w, acc.w);
+    };
+    for (int i0 = s0; i0 < s1; i0 += 64) {
+      if (i0 > s0) ml = stats(i0 + lane);
+      const float f = __builtin_amdgcn_exp2f(ml.x - top);
+      sum = __builtin_fmaf(f, ml.y, sum);
+      const int n = s1 - i0 < 64 ? s1 - i0 : 64;
 #pragma unroll 4
-      for (int i = s0 + rowl; i < s1; i += RPL) {
-        const int64_t at = slot(i) + jc;
-        const float f = __builtin_amdgcn_exp2f(p.part_ml[2 * at] - top);
-        const float4 x = *(const float4*)(p.part + at * D + d0);
-        sum = __builtin_fmaf(f, p.part_ml[2 * at + 1], sum);
-        acc.x = __builtin_fmaf(f, x.x, acc.x);
-        acc.y = __builtin_fmaf(f, x.y, acc.y);
-        acc.z = __builtin_fmaf(f, x.z, acc.z);
-        acc.w = __builtin_fmaf(f, x.w, acc.w);
-      }
-#pragma unroll
-      for (int o = LPR; o < 64; o <<= 1) {
-        sum += __shfl_xor(sum, o, 64);
-        acc.x += __shfl_xor(acc.x, o, 64);
-        acc.y += __shfl_xor(acc.y, o, 64);
-        acc.z += __shfl_xor(acc.z, o, 64);
-        acc.w += __shfl_xor(acc.w, o, 64);
+      for (int t = 0; t * RPL < n; ++t) {
+        const int i = t * RPL + rowl;
+        const float g = __shfl(f, i, 64);
+        if (i < n) add(g, i0 == s0 && t == 0 ? ahead[0] : i0 == s0 && t == 1 ? ahead[1] : row(i0 + i));
       }
     }
-    if (shared) {
-      if (rowl == 0) *(float4*)&so[wave][d0] = acc;
-      if (lane == 0) {
-        sml[wave][0] = top;
-        sml[wave][1] = sum;
-      }
-      __syncthreads();
+    sum = wave_fold(sum, 0.0f, [](float x, float y) { return x + y; });
+#pragma unroll
+    for (int o = LPR; o < 64; o <<= 1) {
+      acc.x += __shfl_xor(acc.x, o, 64);
+      acc.y += __shfl_xor(acc.y, o, 64);
+      acc.z += __shfl_xor(acc.z, o, 64);
+      acc.w += __shfl_xor(acc.w, o, 64);
+    }
+  };
+  auto store = [&](int jc, float top, float sum, float4 acc) {
+    const int col = w.tile * TC + jc;
+    store4<BF>(p, w.r.r0 + col / G, h * G + col % G, D, d0, acc, top, sum);
+  };
+  float top, sum;
+  float4 acc;
+  if (!shared) {
+    for (int jc = 4 * z + wave; jc < cols; jc += 4 * Z) {
+      fold(jc, top, sum, acc);
+      if (rowl == 0) store(jc, top, sum, acc);
+    }
+    return;
+  }
+  for (int jc = z; jc < cols; jc += Z) {
+    fold(jc, top, sum, acc);
+    if (rowl == 0) *(float4*)&so[wave][d0] = acc;
+    if (lane == 0) {
+      sml[wave][0] = top;
+      sml[wave][1] = sum;
+    }
+    __syncthreads();
+    if (wave == 0 && rowl == 0) {
       top = __builtin_fmaxf(__builtin_fmaxf(sml[0][0], sml[1][0]), __builtin_fmaxf(sml[2][0], sml[3][0]));
       sum = 0.0f;
       acc = make_float4(0, 0, 0, 0);
@@ -945,12 +974,9 @@ __global__ __launch_bounds__(256) void attn_kv8_join_kernel(AttnP p, int Z) {
         acc.z = __builtin_fmaf(f, x.z, acc.z);
         acc.w = __builtin_fmaf(f, x.w, acc.w);
       }
-      __syncthreads();
+      store(jc, top, sum, acc);
     }
-    if (mine && rowl == 0 && (!shared || wave == 0)) {
-      const int col = w.tile * TC + jc, row = w.r.r0 + col / G, head = h * G + col % G;
-      store4<BF>(p, row, head, D, d0, acc, top, sum);
-    }
+    __syncthreads();
   }
 }
 

@@ -66,6 +66,23 @@ __device__ __forceinline__ int wave_scan(int x) {
   return x;
 }
 
+// Largest and sum over the lanes of a wave, the same way; the same in all lanes.
+template <class Op>
+__device__ __forceinline__ float wave_fold(float x, float none, Op op) {
+  const int n = __builtin_bit_cast(int, none);
+  auto from = [&](float v, int moved) { return op(v, __builtin_bit_cast(float, moved)); };
+#define AWQ_FOLD(CTRL, ROWS) \
+  x = from(x, __builtin_amdgcn_update_dpp(n, __builtin_bit_cast(int, x), CTRL, ROWS, 0xf, false))
+  AWQ_FOLD(0x111, 0xf);
+  AWQ_FOLD(0x112, 0xf);
+  AWQ_FOLD(0x114, 0xf);
+  AWQ_FOLD(0x118, 0xf);
+  AWQ_FOLD(0x142, 0xa);
+  AWQ_FOLD(0x143, 0xc);
+#undef AWQ_FOLD
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
+}
+
 // 8 e4m3 codes (two 32-bit words) as the MFMA operand type: exact in fp16 and
 // in bf16 (4 significant bits, |code| <= 448, least 2^-9); NaN codes stay NaN.
 template <bool BF>
