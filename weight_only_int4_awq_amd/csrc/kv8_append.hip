@@ -91,7 +91,7 @@ struct AppendP {
   int64_t positions;
   int32_t rot, inter, hq, hpt;       // hpt: query heads per work-group
   uint16_t* q_out;
-  int32_t n_kv;                      // work-groups of the cache's part
+  int32_t n_kv;                      // work-groups of the cache's part, which come last
 };
 
 // Channels of a head in units of 8 values that one lane holds: two runs of four,
@@ -113,8 +113,11 @@ __device__ __forceinline__ Runs runs_of(int u, int rot, bool inter) {
 struct Raw {
   uint2 a, b;
 };
+// Each value is read once by the launch (but for pages of more than 64 slots).
 __device__ __forceinline__ Raw load_raw(const uint16_t* row, const Runs& r) {
-  return Raw{*(const uint2*)(row + r.a), *(const uint2*)(row + r.b)};
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  return Raw{__builtin_bit_cast(uint2, __builtin_nontemporal_load((const u32x2*)(row + r.a))),
+             __builtin_bit_cast(uint2, __builtin_nontemporal_load((const u32x2*)(row + r.b)))};
 }
 template <bool BF>
 __device__ __forceinline__ void widen(const Raw& w, float* x) {
@@ -238,9 +241,10 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(AppendP p) {
   const int at = threadIdx.x / LPT, u = threadIdx.x % LPT;
   const bool inter = p.inter != 0;
   const Runs ru = runs_of(u, p.rot, inter);
-  if ((int)blockIdx.x >= p.n_kv) {
+  const int n_q = (int)gridDim.x - p.n_kv;
+  if ((int)blockIdx.x < n_q) {
     const int groups = (p.hq + p.hpt - 1) / p.hpt;
-    const int w = blockIdx.x - p.n_kv;
+    const int w = blockIdx.x;
     const int row0 = (w / groups) * TPI, h0 = (w % groups) * p.hpt;
     const int h1 = h0 + p.hpt < p.hq ? h0 + p.hpt : p.hq;
     constexpr int RPW = 64 / LPT;            // rows of a wave
@@ -272,7 +276,7 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(AppendP p) {
     return;
   }
 
-  const int h = blockIdx.x % v.hkv, unit = blockIdx.x / v.hkv;
+  const int h = (blockIdx.x - n_q) % v.hkv, unit = (blockIdx.x - n_q) / v.hkv;
   const int seq = seq_of_unit(v, unit, lane);
   if (seq < 0) return;
   const SeqRows r = seq_rows(v, seq);
