@@ -755,22 +755,25 @@ __global__ __launch_bounds__(256, 2) void attn_kv8_tile_kernel(AttnP p) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) vat[t] = (int)sizeof(stage[0].k) + 16 * T::vat(c, 2 * t + half);
   }
-  // two chains of dependent products
-  auto scores = [&](int st, typename E::acc_t* s) {
+  auto keys = [&](int st, uint4 (*kr)[E::NX]) {
     const char* sg = (const char*)&stage[st & 1];
+#pragma unroll
+    for (int x = 0; x < E::NX; ++x)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) kr[t][x] = *(const uint4*)(sg + kat[x] + 32 * t * D);
+  };
+  // two chains of dependent products
+  auto scores = [&](const uint4 (*kr)[E::NX], typename E::acc_t* s) {
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int j = 0; j < 16; ++j) s[t][j] = 0.0f;
 #pragma unroll
     for (int x = 0; x < E::NX; ++x) {
-      uint4 kr[2];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) kr[t] = *(const uint4*)(sg + kat[x] + 32 * t * D);
+      for (int t = 0; t < 2; ++t) s[t] = E::mma_q(E::MQ::from_fp8(kr[t][x].x, kr[t][x].y), a.qf[x][0], s[t]);
 #pragma unroll
-      for (int t = 0; t < 2; ++t) s[t] = E::mma_q(E::MQ::from_fp8(kr[t].x, kr[t].y), a.qf[x][0], s[t]);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) s[t] = E::mma_q(E::MQ::from_fp8(kr[t].z, kr[t].w), a.qf[x][1], s[t]);
+      for (int t = 0; t < 2; ++t) s[t] = E::mma_q(E::MQ::from_fp8(kr[t][x].z, kr[t][x].w), a.qf[x][1], s[t]);
     }
   };
   // behind it everyone's copies have landed, and nobody reads what was read before
@@ -792,7 +795,9 @@ __global__ __launch_bounds__(256, 2) void attn_kv8_tile_kernel(AttnP p) {
     meet();
     if (st0 + 1 < st1) copy_k(st0 + 1, pid1);
     copy_v(st0, pid);
-    scores(st0, s);
+    uint4 kr[2][E::NX];
+    keys(st0, kr);
+    scores(kr, s);
   }
   typename E::acc_t ahead[2];
   auto step = [&](int st, typename E::acc_t* now, typename E::acc_t* then) {
@@ -815,19 +820,25 @@ __global__ __launch_bounds__(256, 2) void attn_kv8_tile_kernel(AttnP p) {
     if (st >= wst1) return;
     half8_t pf[4];
     float f, z;
+    // LDS reads are asked for well before their use: left to itself the compiler puts
+    // them right in front of it
+    uint4 kr[2][E::NX], vr[2][ND];
+    keys(st + 1, kr);                          // of the last step: unused
+    __builtin_amdgcn_sched_barrier(0);
     a.level(now, q, t0, ks, vs, out_of, half, f, z);
-    scores(st + 1, then);                      // of the last step: unused
-    a.weights(now, f, z, vs, pf);
     const char* sg = (const char*)&stage[st & 1];
 #pragma unroll
+    for (int i = 0; i < ND; ++i) vr[0][i] = *(const uint4*)(sg + vat[0] + 32 * i * 64);
+    scores(kr, then);
+    a.weights(now, f, z, vs, pf);
+#pragma unroll
+    for (int i = 0; i < ND; ++i) vr[1][i] = *(const uint4*)(sg + vat[1] + 32 * i * 64);
+#pragma unroll
     for (int t = 0; t < 2; ++t) {
-      uint4 vr[ND];
 #pragma unroll
-      for (int i = 0; i < ND; ++i) vr[i] = *(const uint4*)(sg + vat[t] + 32 * i * 64);
+      for (int i = 0; i < ND; ++i) a.o[i] = E::mma_v(E::MV::from_fp8(vr[t][i].x, vr[t][i].y), pf[2 * t], a.o[i]);
 #pragma unroll
-      for (int i = 0; i < ND; ++i) a.o[i] = E::mma_v(E::MV::from_fp8(vr[i].x, vr[i].y), pf[2 * t], a.o[i]);
-#pragma unroll
-      for (int i = 0; i < ND; ++i) a.o[i] = E::mma_v(E::MV::from_fp8(vr[i].z, vr[i].w), pf[2 * t + 1], a.o[i]);
+      for (int i = 0; i < ND; ++i) a.o[i] = E::mma_v(E::MV::from_fp8(vr[t][i].z, vr[t][i].w), pf[2 * t + 1], a.o[i]);
     }
   };
   for (int st = st0; st < st1; st += 2) {
