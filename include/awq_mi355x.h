@@ -535,9 +535,10 @@ awq_status awq_rope_table(int64_t positions, int32_t rot, double base, int32_t s
  *   magnitude appended to the page by this call is at most 448 * 2^e.  Where
  *   the page holds older tokens of the sequence the scale never falls: it is
  *   the larger of the old one and that, and older codes are requantized to
- *   e4m3_rn(code * old / new), exact but for results below 2^-6.  New codes are
- *   e4m3_rn(x / scale) (ties to even).  Slots behind the sequence's end keep
- *   what they held.
+ *   e4m3_rn(code * (old / new)), exact but for results below 2^-6.  New codes
+ *   are e4m3_rn(x / scale) (ties to even).  Quotients and products are fp32 (exact
+ *   unless another writer left a scale that is no power of two).  Slots behind
+ *   the sequence's end keep what they held.
  *   A token whose rotated k or v holds inf or NaN, or whose position is not in
  *   the table, is stored as a k of NaN codes and a v of zeros and does not
  *   count for the scales: who may see it gets NaN, and nobody else does.  Its

@@ -2,8 +2,8 @@
 infrastructure: imports nothing of the product package).
 
 append() follows the documented arithmetic bit for bit: the rotation is float32 with
-every product and sum rounded once, everything behind it is exact in float64 up to
-the one rounding to an e4m3 code.  attend() is float64 throughout and returns
+every product and sum rounded once, the quotient by the scale is float32 (exact for a
+power of two), and then there is the one rounding to an e4m3 code.  attend() is float64 throughout and returns
 what the error bound of the kernels needs."""
 from __future__ import annotations
 
@@ -90,13 +90,13 @@ def append(kc, vc, ks, vs, bt, ctx, cu, k, v, table=None, inter=False):
                     if old:
                         s = max(s, scale[at, h])
                         if s != scale[at, h]:
-                            cache[:old] = encode(CODE[cache[:old]] * (float(scale[at, h]) / float(s)))
+                            cache[:old] = encode((CODE[cache[:old]].astype(np.float32) * (scale[at, h] / s)).astype(np.float64))
                     scale[at, h] = s
                     for i in np.nonzero(here)[0]:
                         if bad[i, h]:
                             cache[pos[i] - j * page] = 0x7F if scale is ks else 0
                         else:
-                            cache[pos[i] - j * page] = encode(x[i, h].astype(np.float64) / float(s))
+                            cache[pos[i] - j * page] = encode((x[i, h] / np.float32(s)).astype(np.float64))
 
 
 def attend(q, kc, vc, ks, vs, bt, ctx, cu, scale):

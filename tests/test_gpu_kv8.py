@@ -231,6 +231,24 @@ def test_append_odd_tokens(P):
         assert nan[68:70].all() and not nan[:68].any()          # positions 88 and 89 of a table of 88
 
 
+@pytest.mark.parametrize("loud", [0.02, 40.0])
+def test_append_keeps_scales_of_other_writers(P, loud):
+    """Older tokens under scales that are no powers of two: kept (new codes by true quotients) or
+    grown to a power of two."""
+    for dt, page in (("bf16", 64), ("fp16", 128)):
+        c = Case(25, dt, [3, 30, 1], [20, 90, 64], 4, 2, 128, page)
+        c.ks *= c.rng.uniform(1.0, 1.999, c.ks.shape).astype(np.float32)
+        c.vs *= c.rng.uniform(1.0, 1.999, c.vs.shape).astype(np.float32)
+        x = c.act(8, loud)
+        c.upload()
+        dx = x.to(DEV)
+        append_fn(P, dt)(dx[:, 4:6], dx[:, 6:], c.dk, c.dv, c.dks, c.dvs, c.dbt, c.dctx, cu_q=c.dcu)
+        f = x.float().numpy()
+        want = [a.copy() for a in (c.kc, c.vc, c.ks, c.vs)]
+        R.append(*want, c.bt, c.ctx, c.cu, f[:, 4:6], f[:, 6:])
+        same_cache(c, want)
+
+
 def test_append_bad_pages_and_lengths(P):
     """Pages outside the cache and tokens past the table of pages are dropped, as are
     rows before position 0; nothing else changes."""
@@ -400,6 +418,66 @@ def test_poisoned_token_is_seen_by_later_rows_only(P):
     assert nan[70:, :2].all() and not nan[:70].any() and not nan[:, 2:].any()
     # the scale of its page is another, as the token does not count for it: compare the page before it
     assert np.array_equal(outs[0][:64], outs[1][:64])
+
+
+@pytest.mark.parametrize("new", [3, 5, 50])
+def test_odd_queries_stay_alone(P, new):
+    """NaN and inf in one row's query change that row and head only."""
+    c = Case(98, "bf16", [new, 2], [400, 66], 4, 1, 128, 64)
+    c.upload()
+    q = c.act(4)
+    want = run_attn(P, c, q.to(DEV), max_q=new)
+    bad = q.clone()
+    bad[1, 2, 7] = float("nan")
+    bad[new, 0, 0] = float("inf")
+    out, lse = run_attn(P, c, bad.to(DEV), max_q=new)
+    odd = torch.zeros(c.rows, 4, dtype=torch.bool, device=DEV)
+    odd[1, 2] = odd[new, 0] = True
+    assert torch.isnan(out[odd]).all() and torch.isnan(lse[odd]).all()
+    assert torch.equal(out[~odd], want[0][~odd]) and torch.equal(lse[~odd], want[1][~odd])
+
+
+def test_no_rows_and_no_sequences(P):
+    """Empty calls write nothing: no rows, no sequences, an empty block table."""
+    c = Case(100, "fp16", [0, 0], [70, 3], 4, 2, 64, 64)
+    c.upload()
+    none = torch.empty(0, 4, 64, dtype=torch.float16, device=DEV)
+    kv = torch.empty(0, 2, 64, dtype=torch.float16, device=DEV)
+    assert P.awq_kv8_append(kv, kv, c.dk, c.dv, c.dks, c.dvs, c.dbt, c.dctx, cu_q=c.dcu, q=none).shape == (0, 4, 64)
+    assert P.awq_attn_kv8(none, c.dk, c.dv, c.dks, c.dvs, c.dbt, c.dctx, cu_q=c.dcu).shape == (0, 4, 64)
+    same_cache(c, (c.kc, c.vc, c.ks, c.vs))
+    # rows, but every sequence idle: the rows are nobody's
+    q = torch.randn(5, 4, 64, device=DEV).half()
+    out, lse = torch.full_like(q, 7.0), torch.full((5, 4), 7.0, device=DEV)
+    P.awq_attn_kv8(q, c.dk, c.dv, c.dks, c.dvs, c.dbt, c.dctx, cu_q=c.dcu, out=out, lse=lse)
+    P.awq_kv8_append(q[:, :2], q[:, 2:], c.dk, c.dv, c.dks, c.dvs, c.dbt, c.dctx, cu_q=c.dcu)
+    assert (out == 7).all() and (lse == 7).all()
+    same_cache(c, (c.kc, c.vc, c.ks, c.vs))
+    # no pages at all: every row sees nothing (ctx 0) or NaN (ctx 1)
+    ctx = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    bt = torch.empty(2, 0, dtype=torch.int32, device=DEV)
+    out, lse = torch.full_like(q[:2], 7.0), torch.full((2, 4), 7.0, device=DEV)
+    P.awq_attn_kv8(q[:2], c.dk, c.dv, c.dks, c.dvs, bt, ctx, out=out, lse=lse)
+    assert (out[0] == 0).all() and torch.isneginf(lse[0]).all()
+    assert torch.isnan(out[1]).all() and torch.isnan(lse[1]).all()
+
+
+@pytest.mark.parametrize("extra", [1, 40])
+def test_rows_within_the_block_table_are_kept(P, extra):
+    """A sequence longer than its row of the block table: NaN for the rows that stand behind it only."""
+    c = Case(102, "fp16", [30 + extra, 3], [640 + extra, 100], 4, 1, 128, 64)
+    assert c.bt.shape[1] == 11
+    q = c.act(4)
+    c.upload()
+    want = run_attn(P, c, q.to(DEV), max_q=30 + extra)
+    c.dbt = c.dbt[:, :10].contiguous()
+    for max_q in (30 + extra, 1):
+        out, lse = run_attn(P, c, q.to(DEV), max_q=max_q)
+        lost = torch.zeros(c.rows, dtype=torch.bool, device=DEV)
+        lost[30:30 + extra] = True
+        assert torch.isnan(out[lost]).all() and torch.isnan(lse[lost]).all()
+        assert torch.isfinite(out[~lost]).all()
+        assert (out[~lost].double() - want[0][~lost].double()).abs().max() <= 2.0 ** -9 * want[0].double().abs().max()
 
 
 def test_attention_peaked_and_scaled(P):

@@ -734,6 +734,8 @@ def _attn_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx, cu_q, max
             raise ValueError(f"lse must be on the cache's device, cuda:{dev} (got {lse.device})")
     need = _lib.load().awq_attn_kv8_workspace_size(b, rows, hq, c.hkv, d, c.page, c.max_pages, max_q)
     wp, wb = _workspace(need, q.device, workspace) if need else (None, 0)
+    if need and workspace is not None and workspace.get_device() != dev:
+        raise ValueError(f"workspace must be on the cache's device, cuda:{dev} (got {workspace.device})")
     _call("awq_attn_kv8_bf16" if bf else "awq_attn_kv8", dev, _lib.byref(c), rows, max_q, q.data_ptr(), qs, hq,
           d ** -0.5 if scale is None else scale, out.data_ptr(), os, _ptr(lse), wp, wb)
     return out

@@ -82,7 +82,6 @@ struct Seq {
   const int32_t* bt;       // its row of the block table
   int ctx, pos, first;     // pos: the last position that this lane's column sees (-1: none);
                            // first: the least pos of the wave's columns
-  bool over;               // longer than its row of the block table: NaN
 };
 
 // One wave's columns of one key/value head, a step at a time: keys and values go
@@ -162,7 +161,7 @@ struct Wave {
     const int c = lane % C, g = lane / C, t0 = st * kStep;
     const int krow = W ? 16 * (c >> 2 & 1) + 4 * (c >> 3) + (c & 3) : 16 * (c >> 2) + (c & 3);
     int pid = scalar_load(q.bt + (t0 >> v.shift));
-    bad = q.over || (uint32_t)pid >= (uint32_t)v.pages;
+    bad = (uint32_t)pid >= (uint32_t)v.pages;
     pid = bad ? 0 : pid;
     const int64_t ph = (int64_t)pid * v.hkv + h;
     const int slot0 = t0 & ((1 << v.shift) - 1);
@@ -281,10 +280,12 @@ struct Wave {
     }
   }
 
-  // l over the lane groups
-  __device__ __forceinline__ void finish() {
+  // l over the lane groups; NaN where the column sees positions behind the sequence's
+  // row of the block table
+  __device__ __forceinline__ void finish(const Kv8View& v, int pos) {
 #pragma unroll
     for (int x = C; x < 64; x <<= 1) l += __shfl_xor(l, x, 64);
+    if (pos >= (int64_t)v.max_pages << v.shift) l = __builtin_nanf("");
   }
 };
 
@@ -419,7 +420,6 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_kv8_line_kernel(AttnP p) {
   Stretch<C> ahead = y;                          // leaves y's window where the stretch begins
   const uint32_t x1 = ahead.start(k + 1);
   if (x0 >= x1) return;
-  const int64_t cap = (int64_t)v.max_pages << v.shift;
   const int c = lane % C, g = lane / C;
   __shared__ __attribute__((aligned(16))) float so[NW * C * (D + 4)];     // O [wave][column][channel]
   __shared__ float sm[NW * C], sl[NW * C];
@@ -437,7 +437,6 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_kv8_line_kernel(AttnP p) {
     cols = n * G - w.tile * C < C ? n * G - w.tile * C : C;
     q.bt = v.bt + (int64_t)w.b * v.max_pages;
     q.ctx = ctx;
-    q.over = ctx > cap;
     q.pos = c < cols ? ctx - n + col / G : -1;
     q.first = uniform(cols < C ? -1 : ctx - n + (w.tile * C) / G);
     const int held = ctx / kStep + (ctx % kStep ? 1 : 0), there = held < y.cap ? held : y.cap;
@@ -453,7 +452,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_kv8_line_kernel(AttnP p) {
   for (;;) {
     e.clear();
     e.loop(v, p.scale2, q, h, st, st1, NW, lane);
-    e.finish();
+    e.finish(v, q.pos);
     const Place done = w;
     const int dcols = cols;
     const uint32_t from = x;
@@ -706,7 +705,7 @@ __global__ __launch_bounds__(256, 2) void attn_kv8_tile_kernel(AttnP p) {
 
   __shared__ T stage[2];
   E a;
-  const Seq q = {v.bt + (int64_t)b * v.max_pages, ctx, pos, first, ctx > (int64_t)v.max_pages << v.shift};
+  const Seq q = {v.bt + (int64_t)b * v.max_pages, ctx, pos, first};
   {
     const int cc = c < cols ? col : tile * TC;
     a.load_q(p.q + (int64_t)(r0 + cc / G) * p.q_stride + (int64_t)(h * G + cc % G) * D, lane);
@@ -731,7 +730,7 @@ __global__ __launch_bounds__(256, 2) void attn_kv8_tile_kernel(AttnP p) {
   // an LDS address is the low half of its flat one
   const uint32_t lds0 = uniform((int)(uint32_t)(uintptr_t)&stage[0]) + wave * 1024;
   auto page_of = [&](int st) { return st < st1 ? scalar_load(q.bt + ((st * kStep) >> v.shift)) : 0; };
-  auto held = [&](int pid) { return !q.over && (uint32_t)pid < pages; };
+  auto held = [&](int pid) { return (uint32_t)pid < pages; };
   auto head_of = [&](int pid) { return (int64_t)(held(pid) ? pid : 0) * v.hkv + h; };
   auto copy_k = [&](int st, int pid) {
     const uint8_t* kp = v.kc + ((head_of(pid) << v.shift) + ((st * kStep) & smask)) * D;
@@ -845,7 +844,7 @@ __global__ __launch_bounds__(256, 2) void attn_kv8_tile_kernel(AttnP p) {
     step(st, s, ahead);
     if (st + 1 < st1) step(st + 1, ahead, s);
   }
-  a.finish();
+  a.finish(v, pos);
   if (c >= cols) return;
   if (S == 1) {
     const int row = r0 + col / G, head = h * G + col % G;
