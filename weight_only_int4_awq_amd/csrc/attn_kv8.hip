@@ -596,7 +596,7 @@ __device__ __forceinline__ bool find_unit(const AttnP& p, int u, int lane, Unit&
   int before = 0, slots = 0;
   for (int i0 = 0; i0 < v.b; i0 += 64) {
     if (v.b > 64) load(i0 + lane, r, tiles, steps);
-    // a short context is not worth a second launch's work
+    // a short context is not worth partial results and a second launch's work
     int S = steps <= p.whole ? 1 : (steps + chunk - 1) / chunk;
     S = S < 1 ? 1 : S;
     const int held = S > 1 ? tiles * S : 0;
@@ -1031,7 +1031,10 @@ Plan plan_of(int64_t b, int64_t rows, int32_t hq, int32_t hkv, int32_t d, int32_
     p.joins = p.target - 1;                  // may be none
     p.z = (int)(max_q * G < 4 ? max_q * G : 4);
   } else {
-    p.whole = 16;
+    // a tile in parts writes and reads 64 KB for each, some 8 steps' time (a prompt of
+    // 2048, 32 steps: 60 us whole, 74 in halves; chunks of prompts of up to 106
+    // steps: 166 us in halves, 180 whole)
+    p.whole = 32;
     p.min_steps = 8;
     // two work-groups on each CU
     const int64_t total = 512;
