@@ -357,6 +357,30 @@ def test_attention_many_sequences(P, b):
     check_attn(c, q, out, lse)
 
 
+def test_attention_so_many_sequences_that_two_waves_take_a_tile(P):
+    rng = np.random.default_rng(300)
+    ctx = rng.integers(0, 40, 300)
+    ctx[17], ctx[299] = 2000, 700
+    for hq, once in ((8, True), (16, False)):
+        new = np.ones(300, np.int64) if once else rng.integers(0, 3, 300)
+        c = Case(301 + hq, "bf16" if once else "fp16", new, np.maximum(ctx, new), hq, 8, 64, 64)
+        c.upload()
+        q = c.act(hq)
+        out, lse = run_attn(P, c, q.to(DEV), max_q=int(new.max()), cu=not once)
+        check_attn(c, q, out, lse)
+
+
+def test_attention_joins_hundreds_of_parts(P):
+    """One context so much longer than thousands of others that its column comes in some 300 parts."""
+    ctx = np.ones(2050, np.int64)
+    ctx[2000] = 80000
+    c = Case(2050, "bf16", [1] * 2050, ctx, 1, 1, 64, 64)
+    c.upload()
+    q = c.act(1)
+    out, lse = run_attn(P, c, q.to(DEV), cu=False)
+    check_attn(c, q, out, lse)
+
+
 @pytest.mark.parametrize("new", [1, 6, 40])
 def test_attention_long_context_is_split(P, new):
     c = Case(77, "fp16", [new, new], [9000, 700], 4, 1, 128, 64)
@@ -365,6 +389,51 @@ def test_attention_long_context_is_split(P, new):
     assert P.awq_attn_kv8_workspace_size(2, c.rows, 4, 1, 128, 64, c.bt.shape[1], new) > 0
     out, lse = run_attn(P, c, q.to(DEV), max_q=new)
     check_attn(c, q, out, lse)
+
+
+@pytest.mark.parametrize("d,page", [(64, 64), (128, 256)])
+def test_attention_split_in_wide_tiles(P, d, page):
+    """Enough rows and heads for tiles of 128 columns, contexts long enough to be split between them."""
+    c = Case(78, "bf16", [200, 150, 3], [3000, 2300, 70], 32, 32, d, page, pad=1)
+    c.upload()
+    q = c.act(32)
+    out, lse = run_attn(P, c, q.to(DEV), max_q=200)
+    check_attn(c, q, out, lse)
+    again = run_attn(P, c, q.to(DEV), max_q=200)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("b", [64, 100])
+def test_attention_many_sequences_in_wide_tiles(P, b):
+    rng = np.random.default_rng(b)
+    new = rng.integers(0, 20, b)
+    new[3], new[b - 1] = 40, 33
+    ctx = new + rng.integers(0, 90, b)
+    ctx[b - 1] += 2500
+    c = Case(b + 9, "bf16", new, ctx, 8, 2, 64, 64)
+    c.upload()
+    q = c.act(8)
+    out, lse = run_attn(P, c, q.to(DEV), max_q=40)
+    check_attn(c, q, out, lse)
+
+
+def test_attention_bad_page_and_odd_query_in_wide_tiles(P):
+    """The same isolation in tiles of 128 columns: a page outside the cache is seen by later rows only."""
+    c = Case(79, "fp16", [140, 60], [2400, 2200], 16, 16, 128, 64)
+    q = c.act(16)
+    c.upload()
+    want = run_attn(P, c, q.to(DEV), max_q=140)
+    bt = c.bt.copy()
+    bt[0, 36] = -7                                      # positions 2304 ..: rows 44 on of sequence 0
+    c.dbt.copy_(torch.from_numpy(bt))
+    bad = q.clone()
+    bad[150, 3, 2] = float("nan")
+    out, lse = run_attn(P, c, bad.to(DEV), max_q=140)
+    odd = torch.zeros(c.rows, 16, dtype=torch.bool, device=DEV)
+    odd[44:140] = True
+    odd[150, 3] = True
+    assert torch.isnan(out[odd]).all() and torch.isnan(lse[odd]).all()
+    assert torch.equal(out[~odd], want[0][~odd]) and torch.equal(lse[~odd], want[1][~odd])
 
 
 def test_attention_scales_far_apart(P):

@@ -1007,14 +1007,21 @@ struct Plan {
 Plan plan_of(int64_t b, int64_t rows, int32_t hq, int32_t hkv, int32_t d, int32_t page, int64_t max_pages,
              int64_t max_q) {
   Plan p;
+  max_q = max_q < (1 << 24) ? max_q : 1 << 24;
   const int64_t G = hq / hkv, steps = max_pages * (page / kStep) > 1 ? max_pages * (page / kStep) : 1;
-  // 128-column tiles share what they read among four waves, and need 128 columns
-  // for it: up to 64 the eight waves of a work-group share the steps instead
-  p.tc = max_q > 64 || max_q * G > 64 ? 128 : max_q * G > 16 ? 32 : 16;
   auto tiles_of = [&](int tc) {
     const int64_t by_rows = rows * ((G + tc - 1) / tc), by_cols = rows * G / tc + b;
     return by_rows < by_cols ? by_rows : by_cols;
   };
+  // Up to 64 columns of a sequence: 16 (8 sequences of 16 rows of 4 heads behind 4000
+  // tokens: 27 us, 29 with 32, 33 with 128; of 5 rows: 18, 23, 44).  More: 128 columns,
+  // which share what they read among four waves, but for long contexts in too few
+  // such tiles to fill the card, which 32 columns on the line share out evenly (24 rows
+  // behind 4000: 28 us, 53 with 128; one sequence of 200 rows: 37, 44; 96 rows, 160
+  // tiles: 83, 61; 40 sequences of 48 rows behind 2000, 560 tiles: 68, 54; of 20 rows
+  // behind 100: 21, 10).
+  const int64_t cols = max_q * G, t128 = tiles_of(128) * hkv;
+  p.tc = cols <= 64 ? 16 : steps <= 32 ? 128 : t128 < 144 || (cols <= 128 && t128 < 400) ? 32 : 128;
   if (p.tc < 128 && tiles_of(p.tc) * steps >= (1ll << 31)) p.tc = 128;    // the line is 32 bits long
   const int64_t tiles = tiles_of(p.tc);
   if (p.tc < 128) {
@@ -1024,8 +1031,10 @@ Plan plan_of(int64_t b, int64_t rows, int32_t hq, int32_t hkv, int32_t d, int32_
     p.whole = tiles * hkv < 64 ? 16 : 8;
     p.min_steps = 4;
     // One work-group of eight waves on each CU; four of two waves where there are so
-    // many tiles that each CU has several whatever their lengths.
-    p.waves = tiles * hkv >= 2048 ? 2 : 8;
+    // many tiles that each CU has eight whatever their lengths (1024 sequences of 50
+    // tokens: 48 us, 98 with eight waves; of 500: 124, 152; 512 tiles of up to 2000
+    // tokens: 38, 34).  Tiles of 32 columns are never that many.
+    p.waves = p.tc == 16 && tiles * hkv >= 2048 ? 2 : 8;
     const int total = p.waves == 8 ? 256 : 1024;
     p.target = hkv < total ? total / hkv : 1;
     p.groups = p.target;
@@ -1034,7 +1043,7 @@ Plan plan_of(int64_t b, int64_t rows, int32_t hq, int32_t hkv, int32_t d, int32_
     p.z = (int)(max_q * G < 4 ? max_q * G : 4);
   } else {
     // a tile in parts writes and reads 64 KB for each, some 8 steps' time (a prompt of
-    // 2048, 32 steps: 60 us whole, 74 in halves; chunks of prompts of up to 106
+    // 2048, 32 steps: 55 us whole, 74 in halves; chunks of prompts of up to 106
     // steps: 166 us in halves, 180 whole)
     p.whole = 32;
     p.min_steps = 8;
@@ -1049,9 +1058,9 @@ Plan plan_of(int64_t b, int64_t rows, int32_t hq, int32_t hkv, int32_t d, int32_
     p.z = 4;
   }
   p.once = max_q * G <= p.tc;
-  const size_t cols = (size_t)p.slots * hkv * p.tc;
-  p.off_ml = cols * d * sizeof(float);
-  p.off_rec = (p.off_ml + cols * 2 * sizeof(float) + 255) / 256 * 256;
+  const size_t kept = (size_t)p.slots * hkv * p.tc;
+  p.off_ml = kept * d * sizeof(float);
+  p.off_rec = (p.off_ml + kept * 2 * sizeof(float) + 255) / 256 * 256;
   p.bytes = p.tc < 128 && p.slots ? p.off_rec + ((size_t)p.slots * sizeof(int4) + 255) / 256 * 256 : p.off_rec;
   return p;
 }
@@ -1077,8 +1086,7 @@ static hipError_t launch(const AttnP& p, const Plan& pl, hipStream_t stream) {
     if (pl.waves == 8) launch_line<D, BF, 16, 8>(p, pl, grid, joins, stream);
     else launch_line<D, BF, 16, 2>(p, pl, grid, joins, stream);
   } else if (pl.tc == 32) {
-    if (pl.waves == 8) launch_line<D, BF, 32, 8>(p, pl, grid, joins, stream);
-    else launch_line<D, BF, 32, 2>(p, pl, grid, joins, stream);
+    launch_line<D, BF, 32, 8>(p, pl, grid, joins, stream);
   } else {
     attn_kv8_tile_kernel<D, BF><<<grid, 256, 0, stream>>>(p);
     if (pl.slots) attn_kv8_join_kernel<D, 128, BF><<<joins, 256, 0, stream>>>(p, pl.z);
