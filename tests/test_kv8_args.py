@@ -158,3 +158,13 @@ def test_reference_codes_are_e4m3():
         want = torch.from_numpy(a).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
         assert np.array_equal(R.encode(a.astype(np.float64)), want)
     assert R.scale_of(448.0) == 1.0 and R.scale_of(448.5) == 2.0 and R.scale_of(0.0) == np.float32(2.0 ** -64)
+
+
+@pytest.mark.parametrize("rows", [1, 40, 5000, 2 ** 31 - 1])
+@pytest.mark.parametrize("most", [2 ** 24, 2 ** 40, 2 ** 59 + 1, 2 ** 63 - 1])
+def test_workspace_size_for_any_most_rows(lib, rows, most):
+    """max_q times the heads of a key/value head need not fit in 64 bits."""
+    f = lib.awq_attn_kv8_workspace_size
+    size = f(3, rows, 32, 8, 128, 64, 2048, most)
+    assert size == f(3, rows, 32, 8, 128, 64, 2048, 2 ** 20)
+    assert (size > 0) == (rows <= 2 ** 24)                          # beyond the limit of rows there is none
