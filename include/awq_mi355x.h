@@ -477,7 +477,8 @@ awq_status awq_linear_w4a16_group_bf16(const awq_linear_item* items, int32_t cou
  *   page number outside 0 .. pages - 1, or a position past max_pages pages,
  *   is dropped by the append and gives NaN where the attention would see it.
  *   Limits: page in {64, 128, 256}; d in {64, 128}; 1 <= hkv <= 1024; hq a
- *   multiple of hkv; 0 <= b <= 65536; 0 <= rows <= 2^24 and rows * hq <= 2^30.
+ *   multiple of hkv; 0 <= b <= 65536; 0 <= rows <= 2^24 and rows * hq <= 2^30;
+ *   b * hkv <= 2^21 and rows * hkv <= 2^27 (what one launch holds).
  *   q, k, v and the outputs are [rows][heads][d] with rows `stride` elements
  *   apart (a multiple of 8, 16-byte aligned, so slices of the stacked q, k, v
  *   projection do).

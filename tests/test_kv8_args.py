@@ -168,3 +168,15 @@ def test_workspace_size_for_any_most_rows(lib, rows, most):
     size = f(3, rows, 32, 8, 128, 64, 2048, most)
     assert size == f(3, rows, 32, 8, 128, 64, 2048, 2 ** 20)
     assert (size > 0) == (rows <= 2 ** 24)                          # beyond the limit of rows there is none
+
+
+@pytest.mark.parametrize("fn", ["awq_kv8_append", "awq_kv8_append_bf16", "awq_attn_kv8", "awq_attn_kv8_bf16"])
+@pytest.mark.parametrize("b,rows,hkv", [(65536, 5, 64), (2049, 2049, 1024), (2, 1 << 24, 16), (2, (1 << 17) + 1, 1024)])
+def test_more_than_one_launch_holds_is_refused(lib, fn, b, rows, hkv):
+    c = cache(b=b, hkv=hkv)
+    if "append" in fn:
+        args = [rows, None, 0, hkv, FAKE, hkv * 128, FAKE, hkv * 128, None, 0, 0, 0, None, 0, None]
+    else:
+        args = [rows, rows, FAKE, hkv * 128, hkv, 1.0, FAKE, hkv * 128, None, FAKE, 1 << 40, None]
+        assert lib.awq_attn_kv8_workspace_size(b, rows, hkv, hkv, 128, 64, 4000, rows) == 0
+    assert status(lib, fn, C.byref(c), *args) == 2

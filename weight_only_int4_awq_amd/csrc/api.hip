@@ -556,6 +556,13 @@ awq_status awq_rope_table(int64_t positions, int32_t rot, double base, int32_t s
   return AWQ_OK;
 }
 
+// A launch holds fewer than 2^24 work-groups of 256 threads.  The append's: rows / 64 + 2 b
+// for each key/value head and some rows * hq / 128 for the queries, at most
+// 2^21 + 2^22 + 2^23; the attention's: rows * hq / 128 + b * hkv, at most 2^23 + 2^21.
+static bool kv8_fits(int64_t b, int64_t rows, int32_t hkv) {
+  return b * hkv <= (1 << 21) && rows * hkv <= (1 << 27);
+}
+
 // Checks shared by the append and the attention; fills `a`.
 static awq_status kv8_args(const char* fn, const awq_kv8_cache* c, int64_t rows, awq::Kv8Args* a) {
   char msg[128];
@@ -573,6 +580,8 @@ static awq_status kv8_args(const char* fn, const awq_kv8_cache* c, int64_t rows,
     return err(AWQ_ERR_SHAPE, "max_pages=%lld out of range", c->max_pages);
   if (c->b < 0 || c->b > 65536) return err(AWQ_ERR_SHAPE, "b=%lld outside 0..65536", c->b);
   if (rows < 0 || rows > (1 << 24)) return err(AWQ_ERR_SHAPE, "rows=%lld outside 0..2^24", rows);
+  if (!kv8_fits(c->b, rows, c->hkv))
+    return err(AWQ_ERR_SHAPE, "b * hkv above 2^21 or rows * hkv above 2^27");
   if (!c->k || !c->v || !c->k_scale || !c->v_scale) return err(AWQ_ERR_NULL, "null pointer");
   if (c->b > 0 && (!c->ctx || (c->max_pages > 0 && !c->block_table))) return err(AWQ_ERR_NULL, "null pointer");
   if (!aligned(c->k, 16) || !aligned(c->v, 16)) return err(AWQ_ERR_ALIGN, "k and v must be 16-byte aligned");
@@ -665,7 +674,7 @@ size_t awq_attn_kv8_workspace_size(int64_t b, int64_t rows, int32_t hq, int32_t 
                                    int64_t max_pages, int64_t max_q) {
   if (b < 1 || b > 65536 || rows < 1 || rows > (1 << 24) || hkv < 1 || hkv > 1024 || hq < 1 || hq > 65536 ||
       hq % hkv || rows * hq > (1ll << 30) || (d != 64 && d != 128) || (page != 64 && page != 128 && page != 256) ||
-      max_pages < 0 || max_pages > 0x7FFFFFFF / page || max_q < 1)
+      max_pages < 0 || max_pages > 0x7FFFFFFF / page || max_q < 1 || !kv8_fits(b, rows, hkv))
     return 0;
   return awq::attn_kv8_scratch_bytes(b, rows, hq, hkv, d, page, max_pages, max_q);
 }
