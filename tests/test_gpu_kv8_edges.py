@@ -1,0 +1,63 @@
+"""Edges of the 8-bit paged KV cache on the GPU: what a page outside the cache stands on, the
+numerics of far-apart scales and weights in the widest tiles, callers in several threads, far
+rotary positions."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+from tests import kv8_ref as R
+from tests.test_gpu_kv8 import DEV, P, Case, attn_fn, check_attn, run_attn  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+# ---------------------------------------------------------------- pages outside the cache
+
+def leave_page_0(c):
+    """Moves what a sequence holds in page 0 of the cache to a page that none holds."""
+    used = {int(p) for i, n in enumerate(c.ctx) for p in c.bt[i, :max(1, -(-int(n) // c.page))]}
+    if 0 not in used:
+        return
+    free = max(p for p in range(c.pages) if p not in used)
+    at = np.argwhere(c.bt == 0)
+    for i, j in at:
+        if j < max(1, -(-int(c.ctx[i]) // c.page)):
+            c.bt[i, j] = free
+    for a in (c.kc, c.vc, c.ks, c.vs):
+        a[[0, free]] = a[[free, 0]]
+
+
+FORMS = [
+    # dt, new, ctx, hq, hkv, d, the entry of sequence 0 that names no page, its first row that sees it
+    ("fp16", [6, 2], [130, 70], 4, 2, 128, 2, 4),                 # one tile of 16 columns
+    ("bf16", [6, 2], [8964, 70], 4, 2, 128, 140, 2),              # the same in parts
+    ("bf16", [6, 0], [130, 9], 16, 2, 64, 2, 4),                  # tiles of 16 columns of one sequence
+    ("fp16", [40, 3], [2970, 100], 4, 1, 64, 46, 14),             # tiles of 32 columns
+    ("fp16", [70, 1], [130, 200], 4, 2, 128, 1, 4),               # tiles of 128 columns
+    ("bf16", [140, 60], [2400, 2200], 64, 64, 64, 36, 44)]        # the same in parts
+
+
+@pytest.mark.parametrize("dt,new,ctx,hq,hkv,d,entry,sees", FORMS)
+@pytest.mark.parametrize("scale0", [0.0, float("nan"), float("inf"), 1e-40])
+def test_bad_page_whatever_page_0_holds(P, dt, new, ctx, hq, hkv, d, entry, sees, scale0):  # noqa: F811
+    """Page 0 belongs to nobody and its scales were never set: rows that do not see the page outside the
+    cache keep their results, those that see it are NaN."""
+    c = Case(200 + d + len(ctx), dt, new, ctx, hq, hkv, d, 64)
+    leave_page_0(c)
+    c.ks[0] = c.vs[0] = scale0
+    c.upload()
+    q = c.act(hq).to(DEV)
+    want = run_attn(P, c, q, max_q=max(new))
+    assert torch.isfinite(want[0]).all() and torch.isfinite(want[1]).all()
+    for outside in (-1, c.pages):
+        bt = c.bt.copy()
+        bt[0, entry] = outside
+        c.dbt.copy_(torch.from_numpy(bt))
+        out, lse = run_attn(P, c, q, max_q=max(new))
+        odd = torch.zeros(c.rows, dtype=torch.bool, device=DEV)
+        odd[sees:new[0]] = True
+        assert torch.isnan(out[odd]).all() and torch.isnan(lse[odd]).all()
+        assert torch.equal(out[~odd], want[0][~odd]) and torch.equal(lse[~odd], want[1][~odd])

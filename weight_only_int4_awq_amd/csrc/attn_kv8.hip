@@ -167,8 +167,11 @@ struct Wave {
     const int slot0 = t0 & ((1 << v.shift) - 1);
     const uint8_t* kp = v.kc + ((ph << v.shift) + slot0) * D;
     vp = v.vc + ((ph * D) << v.shift) + slot0;
+    // not in the cache: the key scale makes NaN of what is seen; the value scale must be
+    // one that leaves the sums of the columns that see none of it alone (0 / vs = 0)
+    const float v1 = scalar_load(v.vs + ph);
     ks = bad ? __builtin_nanf("") : scalar_load(v.ks + ph) * scale2;
-    vs = scalar_load(v.vs + ph);
+    vs = bad ? 1.0f : v1;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -805,7 +808,7 @@ __global__ __launch_bounds__(256, 2) void attn_kv8_tile_kernel(AttnP p) {
     const int t0 = st * kStep;
     const bool out_of = !held(pid);
     const float ks = out_of ? __builtin_nanf("") : scalar_load(v.ks + head_of(pid)) * p.scale2;
-    const float vs = scalar_load(v.vs + head_of(pid));
+    const float v1 = scalar_load(v.vs + head_of(pid)), vs = out_of ? 1.0f : v1;   // as in Wave::ask
     meet();
     if (st + 1 < st1) copy_v(st + 1, pid1);
     if (st + 2 < st1) copy_k(st + 2, pid2);
