@@ -568,9 +568,11 @@ awq_status awq_kv8_append_bf16(const awq_kv8_cache* cache, int64_t rows, const u
  *   for such a row (results of parts of a context can be joined with it).
  *   Codes enter the products exactly; scores, statistics and sums are fp32,
  *   the softmax weights of the value product fp16 (relative rounding 2^-11).
- *   Scales: positive, finite, the value scales of one context within 2^90 of
- *   each other; values |scale * code| within fp32, scores within +-1e29.  v codes
- *   of visible tokens must not be NaN (awq_kv8_append writes none).
+ *   Scales of the pages of a context: from 2^-64 to 2^120 (what awq_kv8_append
+ *   writes; the sums of p / scale leave fp32 below some 2^-100 and at 2^127), the
+ *   value scales of one context within 2^90 of each other; values |scale * code|
+ *   within fp32, scores within +-1e29.  v codes of visible tokens must not be NaN
+ *   (awq_kv8_append writes none).
  *   max_q >= 1: the most new tokens that one sequence has, as far as the host
  *   knows.  It chooses between kernels; results are right for any value.
  *   workspace: awq_attn_kv8_workspace_size(b, rows, hq, hkv, d, page,

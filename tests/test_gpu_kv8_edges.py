@@ -61,3 +61,28 @@ def test_bad_page_whatever_page_0_holds(P, dt, new, ctx, hq, hkv, d, entry, sees
         odd[sees:new[0]] = True
         assert torch.isnan(out[odd]).all() and torch.isnan(lse[odd]).all()
         assert torch.equal(out[~odd], want[0][~odd]) and torch.equal(lse[~odd], want[1][~odd])
+
+
+# ---------------------------------------------------------------- scales at the ends of their range
+
+@pytest.mark.parametrize("new,ctx,hq,hkv", [([3], [200], 4, 2), ([3], [9000], 4, 2), ([40], [2500], 4, 1),
+                                            ([70], [200], 4, 2), ([130], [2500], 72, 72)])
+@pytest.mark.parametrize("exponent", [-64, 120])
+def test_value_scales_at_their_ends(P, new, ctx, hq, hkv, exponent):  # noqa: F811
+    """Every value scale 2^-64 (a page of zeros as the append writes it) or 2^120 (of bf16's largest values), in each
+    tile form, whole and in parts."""
+    c = Case(240, "bf16", new, ctx, hq, hkv, 64, 64)
+    c.vs[:] = 2.0 ** exponent
+    small = np.abs(R.CODE[c.vc]) < 8                    # values within bf16: 448 * 2^120 is not
+    c.vc = np.where(small, c.vc, R.encode(np.full(c.vc.shape, 2.0))).astype(np.uint8)
+    c.upload()
+    q = c.act(hq, 1.3)
+    out, lse = run_attn(P, c, q.to(DEV), max_q=new[0])
+    ref = R.attend(q.double().numpy(), c.kc, c.vc, c.ks, c.vs, c.bt, c.ctx, c.cu, 64 ** -0.5)
+    # attend()'s bounds take the argument of exp2 for one of at most 2 smag + 128; with a scale of 2^120 it is at
+    # most 2 smag + 240, and the rounding 2^-23 * 112 more, which counts twice in a weight
+    more = 2.0 ** -23 * 112
+    to, tl = R.bounds(*ref, 64, torch.finfo(torch.bfloat16).eps)
+    to, tl = to + 2 * more * 1.01 * ref[2], tl + more
+    assert (np.abs(out.double().cpu().numpy() - ref[0]) <= to).all()
+    assert (np.abs(lse.double().cpu().numpy() - ref[1]) <= tl).all()
