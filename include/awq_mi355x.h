@@ -513,7 +513,7 @@ typedef struct {
  *     AWQ_ROPE_YARN    (1 - w) f + w f / factor, w linear in j from
  *                      max(floor(n(high)), 0) to min(ceil(n(low)), rot - 1),
  *                      n(t) = rot ln(trained / (2 pi t)) / (2 ln base);
- *                      m = 0.1 ln(factor) + 1.
+ *                      m = 0.1 ln(factor) + 1, of factors up to 1 m = 1.
  *   Limits: rot even in 2..256; positions <= 2^31 - 1; base > 1; factor > 0;
  *   0 < low < high and trained > 0 where they are read.
  * ------------------------------------------------------------------------- */

@@ -86,3 +86,17 @@ def test_value_scales_at_their_ends(P, new, ctx, hq, hkv, exponent):  # noqa: F8
     to, tl = to + 2 * more * 1.01 * ref[2], tl + more
     assert (np.abs(out.double().cpu().numpy() - ref[0]) <= to).all()
     assert (np.abs(lse.double().cpu().numpy() - ref[1]) <= tl).all()
+
+
+# ---------------------------------------------------------------- rotary tables
+
+@pytest.mark.parametrize("factor", [0.25, 1.0, 1.5])
+def test_yarn_magnitude_starts_at_one(P, factor):  # noqa: F811
+    """The magnitude 0.1 ln(factor) + 1 is for contexts that grow; up to factor 1 it is 1."""
+    table = P.awq_rope_table(100, 64, scaling="yarn", factor=factor, low=1.0, high=32.0, trained=4096)
+    m = 0.1 * np.log(factor) + 1 if factor > 1 else 1.0
+    # position 0: cos 0 = 1 and sin 0 = 0 exactly, so m rounded to fp32 (half a step is 2^-24 of it)
+    assert (table[0, 32:] == 0).all() and (table[0, :32].double() - m).abs().max().item() <= 2.0 ** -24 * m
+    # cos^2 + sin^2 = m^2: each within 2^-22 m, so their squares' sum within 2 * 2^-22 * 1.5 m^2
+    t = table.double().cpu()
+    assert ((t[:, :32] ** 2 + t[:, 32:] ** 2) - m * m).abs().max().item() <= 3 * 2.0 ** -22 * m * m

@@ -476,7 +476,7 @@ hipError_t launch_rope_table(int64_t positions, int32_t rot, double base, const 
   // about eight work-groups per CU, each at least one round of its threads
   int64_t per = (positions + 2047) / 2048;
   per = (per + step - 1) / step * step;
-  const float mag = sc.kind == 3 ? (float)(0.1 * log(sc.factor) + 1.0) : 1.0f;
+  const float mag = sc.kind == 3 && sc.factor > 1 ? (float)(0.1 * log(sc.factor) + 1.0) : 1.0f;
   rope_table_kernel<<<(unsigned)((positions + per - 1) / per), 256, 0, stream>>>(positions, rot, base, sc, mag,
                                                                                 (int32_t)per, table);
   return hipGetLastError();
