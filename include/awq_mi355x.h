@@ -502,8 +502,9 @@ typedef struct {
 /* ---------------------------------------------------------------------------
  * awq_rope_table -- cosines and sines of rotary positions.
  *   table [positions][rot] fp32 out: table[p][j] = m cos(p f_j) and
- *   table[p][rot/2 + j] = m sin(p f_j), j < rot/2, within 2 ulp of m; angles
- *   are reduced in float64.  f_j = base^(-2j/rot), changed for long contexts by
+ *   table[p][rot/2 + j] = m sin(p f_j), j < rot/2.  f_j and p f_j are float64:
+ *   entries are within 2 ulp of m up to angles p f_j of 2^24, and the angle is off by
+ *   up to 2^-49 p f_j beyond.  f_j = base^(-2j/rot), changed for long contexts by
  *     AWQ_ROPE_NONE    nothing (the other parameters are not read), m = 1;
  *     AWQ_ROPE_LINEAR  f / factor, m = 1;
  *     AWQ_ROPE_BANDS   w f + (1 - w) f / factor, m = 1, with

@@ -100,3 +100,19 @@ def test_yarn_magnitude_starts_at_one(P, factor):  # noqa: F811
     # cos^2 + sin^2 = m^2: each within 2^-22 m, so their squares' sum within 2 * 2^-22 * 1.5 m^2
     t = table.double().cpu()
     assert ((t[:, :32] ** 2 + t[:, 32:] ** 2) - m * m).abs().max().item() <= 3 * 2.0 ** -22 * m * m
+
+
+@pytest.mark.parametrize("positions,rot,base", [(1 << 24, 16, 10000.0), (1 << 27, 16, 500000.0), ((1 << 31) - 1, 2, 10000.0)])
+def test_rope_table_far_positions(P, positions, rot, base):  # noqa: F811
+    """The last rows of long tables, against 80-bit floats: 2 ulp of 1 (2^-22) and the angle's own 2^-49 p f beyond
+    p f = 2^24."""
+    table = P.awq_rope_table(positions, rot, base=base)
+    n = 20000
+    got = table[-n:].cpu().numpy().astype(np.float64)
+    del table
+    p = np.arange(positions - n, positions).astype(np.longdouble)
+    f = np.longdouble(base) ** (np.arange(rot // 2).astype(np.longdouble) * -2 / rot)
+    a = p[:, None] * f
+    tol = 2.0 ** -22 + np.where(a > 2.0 ** 24, 2.0 ** -49 * a.astype(np.float64), 0)
+    assert (np.abs(got[:, :rot // 2] - np.cos(a)) <= tol).all()
+    assert (np.abs(got[:, rot // 2:] - np.sin(a)) <= tol).all()
