@@ -1077,8 +1077,11 @@ size_t attn_kv8_scratch_bytes(int64_t b, int64_t rows, int32_t hq, int32_t hkv, 
 
 template <int D, bool BF, int C, int NW>
 static void launch_line(const AttnP& p, const Plan& pl, unsigned grid, unsigned joins, hipStream_t stream) {
-  if (pl.once) attn_kv8_line_kernel<D, BF, C, NW, true><<<grid, 64 * NW, 0, stream>>>(p);
-  else attn_kv8_line_kernel<D, BF, C, NW, false><<<grid, 64 * NW, 0, stream>>>(p);
+  auto kernel = attn_kv8_line_kernel<D, BF, C, NW, false>;
+  if constexpr (C == 16) {       // a sequence in tiles of 32 has more than 64 columns: never one tile
+    if (pl.once) kernel = attn_kv8_line_kernel<D, BF, C, NW, true>;
+  }
+  kernel<<<grid, 64 * NW, 0, stream>>>(p);
   if (pl.slots) attn_kv8_join_kernel<D, C, BF><<<joins, 256, 0, stream>>>(p, pl.z);
 }
 

@@ -179,10 +179,6 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float r) {
                 __builtin_amdgcn_cvt_f32_fp8(w, 2) * r, __builtin_amdgcn_cvt_f32_fp8(w, 3) * r);
 }
 
-__device__ __forceinline__ bool finite(float x) {
-  return (__builtin_bit_cast(uint32_t, x) & 0x7F800000u) != 0x7F800000u;
-}
-
 // Sequence of unit j of the cache's part.  Sequence i owns the numbers from
 // cu[i] / page + 2 i on, of which it uses one for each page that its rows
 // touch: n rows touch at most (n - 2) / page + 2 pages (n >= 2; one for n = 1),
