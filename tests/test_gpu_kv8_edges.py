@@ -116,3 +116,43 @@ def test_rope_table_far_positions(P, positions, rot, base):  # noqa: F811
     tol = 2.0 ** -22 + np.where(a > 2.0 ** 24, 2.0 ** -49 * a.astype(np.float64), 0)
     assert (np.abs(got[:, :rot // 2] - np.cos(a)) <= tol).all()
     assert (np.abs(got[:, rot // 2:] - np.sin(a)) <= tol).all()
+
+
+# ---------------------------------------------------------------- numerics of the 128-column tiles
+
+WIDE = [
+    # new, ctx, hq, hkv, d: over 64 columns on contexts of at most 32 steps; then at least 144 tiles
+    # over all heads on longer ones, in parts
+    ([40, 1], [300, 640], 8, 2, 128),
+    ([130, 3], [3000, 70], 72, 72, 64)]
+
+
+@pytest.mark.parametrize("new,ctx,hq,hkv,d", WIDE)
+def test_wide_tiles_scales_far_apart(P, new, ctx, hq, hkv, d):  # noqa: F811
+    """Value scales from 2^-40 to 2^40 in one context, key scales likewise, peaked scores."""
+    c = Case(211 + d, "bf16", new, ctx, hq, hkv, d, 64)
+    rng = np.random.default_rng(2)
+    c.vs[:] = 2.0 ** rng.choice([-40, -20, -3, 10, 40], c.vs.shape)
+    c.ks[:] = 2.0 ** rng.choice([-64, -9, -5], c.ks.shape)
+    c.upload()
+    q = c.act(hq, 2.0)
+    out, lse = run_attn(P, c, q.to(DEV), max_q=max(new))
+    check_attn(c, q, out, lse)
+
+
+@pytest.mark.parametrize("new,ctx,hq,hkv,d", [([40], [2000], 4, 1, 128), ([130], [3000], 72, 72, 64)])
+@pytest.mark.parametrize("gap", [12.0, 24.3])
+def test_wide_tiles_first_token_outweighs_all(P, new, ctx, hq, hkv, d, gap):  # noqa: F811
+    """One token whose score exceeds every other by a factor of 2^gap, its v zero and the others' v all
+    alike: the bound is relative to the small share that is left of them."""
+    c = Case(215, "fp16", new, ctx, hq, hkv, d, 64)
+    c.kc[:] = 0
+    c.kc[c.bt[0, 0], :, 0] = R.encode(np.full(d, 1.0))
+    c.ks[:] = 1.0
+    c.vc[:] = R.encode(np.full(c.vc.shape, 3.0))
+    c.vc[c.bt[0, 0], :, :, 0] = 0
+    c.vs[:] = 1.0
+    c.upload()
+    q = torch.full((new[0], hq, d), gap * np.log(2) / d ** 0.5).half()
+    out, lse = run_attn(P, c, q.to(DEV), max_q=new[0])
+    check_attn(c, q, out, lse)
