@@ -156,3 +156,46 @@ def test_wide_tiles_first_token_outweighs_all(P, new, ctx, hq, hkv, d, gap):  # 
     q = torch.full((new[0], hq, d), gap * np.log(2) / d ** 0.5).half()
     out, lse = run_attn(P, c, q.to(DEV), max_q=new[0])
     check_attn(c, q, out, lse)
+
+
+# ---------------------------------------------------------------- callers
+
+def test_two_threads(P):  # noqa: F811
+    """Append and attention from two threads at once, a stream each, with the binding's own workspaces."""
+    import threading
+    cases, xs, want = [], [], []
+    for i in range(2):
+        c = Case(230 + i, "fp16", [2, 1], [6000, 900], 8, 2, 128, 64)
+        c.upload()
+        cases.append(c)
+        xs.append(c.act(12).to(DEV))
+
+    def step(c, x):
+        P.awq_kv8_append(x[:, 8:10], x[:, 10:], c.dk, c.dv, c.dks, c.dvs, c.dbt, c.dctx, cu_q=c.dcu)
+        return run_attn(P, c, x[:, :8], max_q=2)
+
+    for c, x in zip(cases, xs):
+        want.append(step(c, x))                       # the same tokens again change nothing
+    torch.cuda.synchronize()
+    got, failed = [[], []], []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(20):
+                    got[i].append(step(cases[i], xs[i]))
+            s.synchronize()
+        except BaseException as e:                    # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    for g, w in zip(got, want):
+        assert len(g) == 20
+        for o, l in g:
+            assert torch.equal(o, w[0]) and torch.equal(l, w[1])
