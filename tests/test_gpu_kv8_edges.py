@@ -158,7 +158,7 @@ def test_wide_tiles_first_token_outweighs_all(P, new, ctx, hq, hkv, d, gap):  # 
     check_attn(c, q, out, lse)
 
 
-# ---------------------------------------------------------------- callers
+# ---------------------------------------------------------------- callers, padded batches, graphs
 
 def test_two_threads(P):  # noqa: F811
     """Append and attention from two threads at once, a stream each, with the binding's own workspaces."""
@@ -199,3 +199,101 @@ def test_two_threads(P):  # noqa: F811
         assert len(g) == 20
         for o, l in g:
             assert torch.equal(o, w[0]) and torch.equal(l, w[1])
+
+
+@pytest.mark.parametrize("ctx", [[70, 3, 400], [70, 3, 9000]])
+def test_padded_batch_of_single_tokens(P, ctx):  # noqa: F811
+    """Without cu_q, more rows than sequences: those behind the last one are neither read nor written."""
+    hq, hkv, d = 8, 2, 128
+    c = Case(250, "fp16", [1, 1, 1], ctx, hq, hkv, d, 64, pad=3)
+    x = c.act(hq + 2 * hkv)
+    x[3:] = float("nan")
+    c.upload()
+    dx = x.to(DEV)
+    q_out = torch.full((6, hq, d), 7.0, dtype=torch.float16, device=DEV)
+    P.awq_kv8_append(dx[:, hq:hq + hkv], dx[:, hq + hkv:], c.dk, c.dv, c.dks, c.dvs, c.dbt, c.dctx, q=dx[:, :hq],
+                     out=q_out)
+    f = x.float().numpy()
+    R.append(c.kc, c.vc, c.ks, c.vs, c.bt, c.ctx, c.cu, f[:, hq:hq + hkv], f[:, hq + hkv:])
+    for got, want in zip(c.cache(), (c.kc, c.vc, c.ks, c.vs)):
+        assert np.array_equal(got, want)
+    assert torch.equal(q_out[:3], dx[:3, :hq]) and (q_out[3:] == 7).all()
+    out, lse = run_attn(P, c, q_out, cu=False)
+    check_attn(c, q_out.cpu(), out, lse)
+
+
+def test_captured_prompts_follow_the_lengths(P):  # noqa: F811
+    """Append and attention over 128-column tiles and their joins, captured once and replayed with other rows per
+    sequence and other contexts, eager calls with the same workspace between the replays."""
+    hq, hkv, d = 32, 32, 64
+    steps = [([200, 150, 3], [2900, 2300, 70]), ([3, 310, 40], [3, 3000, 2800]), ([0, 0, 353], [9, 0, 3000]),
+             ([353, 0, 0], [353, 64, 0])]
+    base = Case(260, "bf16", [200, 150, 3], [3000, 3000, 3000], hq, hkv, d, 64)
+    base.upload()
+    table = P.awq_rope_table(3000, d)
+    x = base.act(hq + 2 * hkv).to(DEV)
+    rows = x.shape[0]
+    need = P.awq_attn_kv8_workspace_size(3, rows, hq, hkv, d, 64, base.bt.shape[1], rows)
+    assert need > 0
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    q_out = torch.zeros(rows, hq, d, dtype=torch.bfloat16, device=DEV)
+    out, lse = torch.zeros_like(q_out), torch.zeros(rows, hq, device=DEV)
+
+    def step():
+        P.awq_kv8_append_bf16(x[:, hq:hq + hkv], x[:, hq + hkv:], base.dk, base.dv, base.dks, base.dvs, base.dbt,
+                              base.dctx, cu_q=base.dcu, q=x[:, :hq], rope=table, out=q_out)
+        P.awq_attn_kv8_bf16(q_out, base.dk, base.dv, base.dks, base.dvs, base.dbt, base.dctx, cu_q=base.dcu, max_q=rows,
+                            out=out, lse=lse, workspace=ws)
+
+    cache = (base.dk.view(torch.uint8), base.dv.view(torch.uint8), base.dks, base.dvs)
+    start = [t.clone() for t in cache]
+
+    def place(new, ctx):
+        for t, s in zip(cache, start):
+            t.copy_(s)
+        base.dcu.copy_(torch.tensor([0, new[0], new[0] + new[1], sum(new)], dtype=torch.int32))
+        base.dctx.copy_(torch.tensor(ctx, dtype=torch.int32))
+        out.fill_(7.0)
+        lse.fill_(7.0)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for new, ctx in steps + steps[::-1]:
+        place(new, ctx)
+        step()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in (out, lse, *cache)]
+        place(new, ctx)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(t, w) for t, w in zip((out, lse, *cache), want))
+
+
+def test_two_graphs_share_a_workspace(P):  # noqa: F811
+    """Two captured calls with one workspace, replayed in turn on a stream."""
+    cases = [Case(270 + i, "fp16", new, ctx, 8, 2, 128, 64)
+             for i, (new, ctx) in enumerate((([1, 2], [6000, 900]), ([5, 1, 9], [3000, 8000, 100])))]
+    qs, need = [], 0
+    for c in cases:
+        c.upload()
+        qs.append(c.act(8).to(DEV))
+        need = max(need, P.awq_attn_kv8_workspace_size(len(c.new), c.rows, 8, 2, 128, 64, c.bt.shape[1], max(c.new)))
+    assert need > 0
+    want = [run_attn(P, c, q, max_q=max(c.new)) for c, q in zip(cases, qs)]
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    outs, graphs = [torch.zeros_like(q) for q in qs], []
+    for c, q, o in zip(cases, qs, outs):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            P.awq_attn_kv8(q, c.dk, c.dv, c.dks, c.dvs, c.dbt, c.dctx, cu_q=c.dcu, max_q=max(c.new), out=o, workspace=ws)
+        graphs.append(graph)
+    for _ in range(4):
+        for o in outs:
+            o.fill_(7.0)
+        for graph in graphs:
+            graph.replay()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w[0])
