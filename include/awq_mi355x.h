@@ -477,8 +477,10 @@ awq_status awq_linear_w4a16_group_bf16(const awq_linear_item* items, int32_t cou
  *   page number outside 0 .. pages - 1, or a position past max_pages pages,
  *   is dropped by the append and gives NaN where the attention would see it.
  *   Limits: page in {64, 128, 256}; d in {64, 128}; 1 <= hkv <= 1024; hq a
- *   multiple of hkv; 0 <= b <= 65536; 0 <= rows <= 2^24 and rows * hq <= 2^30;
- *   b * hkv <= 2^21 and rows * hkv <= 2^27 (what one launch holds).
+ *   multiple of hkv up to 65536; 1 <= pages <= 2^31 - 1; max_pages * page <=
+ *   2^31 - 1; 0 <= b <= 65536; 0 <= rows <= 2^24 and rows * hq <= 2^30;
+ *   b * hkv <= 2^21 and rows * hkv <= 2^27 (what one launch holds); strides up to
+ *   2^31.
  *   q, k, v and the outputs are [rows][heads][d] with rows `stride` elements
  *   apart (a multiple of 8, 16-byte aligned, so slices of the stacked q, k, v
  *   projection do).
@@ -575,7 +577,10 @@ awq_status awq_kv8_append_bf16(const awq_kv8_cache* cache, int64_t rows, const u
  *   within fp32, scores within +-1e29.  v codes of visible tokens must not be NaN
  *   (awq_kv8_append writes none).
  *   max_q >= 1: the most new tokens that one sequence has, as far as the host
- *   knows.  It chooses between kernels; results are right for any value.
+ *   knows.  It chooses between kernels; results are right for any value.  The
+ *   other thing the choice goes by is max_pages * page, the tokens that the block
+ *   table holds: one far wider than its contexts is planned for as long contexts are
+ *   (a launch more, and other tiles).
  *   workspace: awq_attn_kv8_workspace_size(b, rows, hq, hkv, d, page,
  *            max_pages, max_q) bytes, 256-byte aligned (NULL if that is 0):
  *            partial results where a long context is split over work-groups.

@@ -60,8 +60,7 @@ def positions(cu, ctx, b):
 
 
 def append(kc, vc, ks, vs, bt, ctx, cu, k, v, table=None, inter=False):
-    """Updates kc, vc (uint8) and ks, vs (float32) in place; k, v float32 [rows, hkv, d].
-    Returns float32 rotated rows' positions for the caller's own rotation of q."""
+    """Updates kc, vc (uint8) and ks, vs (float32) in place; k, v float32 [rows, hkv, d]."""
     pages, hkv, page, d = kc.shape
     for b in range(len(ctx)):
         rows, first = positions(cu, ctx, b)

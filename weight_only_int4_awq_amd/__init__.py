@@ -699,7 +699,9 @@ def awq_attn_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx, cu_q=N
 
     block_table, ctx and cu_q as in awq_kv8_append.  max_q: the most rows of one
     sequence as far as the caller knows (default: 1 without cu_q, else all
-    rows); it chooses between kernels and never changes what is computed.
+    rows); it chooses between kernels and never changes what is computed.  Pass it
+    with cu_q where sequences have few rows each: the default takes the tiles of a
+    prompt.
     scale: softmax scale (default d ** -0.5).  lse: fp32 [rows, hq] to fill with
     the logarithms of the softmax denominators, or None."""
     return _attn_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx, cu_q, max_q, scale, out, lse,

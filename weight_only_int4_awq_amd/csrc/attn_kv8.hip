@@ -69,7 +69,8 @@ struct Parts {
 };
 
 // 16 bytes of the cache.  ONCE: nothing else of the launch reads them, so they
-// are not kept in the caches (one sequence of 128 K tokens: 53.5 us against 58).
+// are not kept in the caches (one sequence of 128 K tokens: 50.3 us against 56.1; 64 ragged
+// of up to 8 K: 95.8 against 106.1).
 template <bool ONCE>
 __device__ __forceinline__ uint4 load16(const uint8_t* p) {
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -300,8 +301,8 @@ struct Wave {
 // start(k + 1): equal stretches whatever the lengths are, so all work-groups,
 // one on each CU, end together.  A stretch's ends move off a tile that is too
 // short to be worth sharing, and off a tile's last few steps.  (64 ragged sequences of
-// up to 8 K tokens, 541 MB: 92 us, 5.9 TB/s; 101 to 128 us with one unit for each
-// share of a context, by their number.)
+// up to 8 K tokens, 541 MB: 92 us, 5.9 TB/s.  When stretches came in the place of one unit
+// for each share of a context: 101 us against 108 to 128, by the number of units.)
 struct Line {
   uint32_t per;            // length of a stretch
   uint32_t all;            // length of the line
@@ -651,7 +652,8 @@ __device__ __forceinline__ bool find_unit(const AttnP& p, int u, int lane, Unit&
 // unit's steps.  A step's codes come to LDS once for the four waves, copied there
 // straight from the cache two stages deep: 16-byte pieces, placed so that the 8
 // lanes of an LDS cycle hit different banks.  (Read by each wave from the CU's
-// vector cache instead, that cache was 92 % busy and the 8 K prompt took 740 us.)
+// vector cache instead, that cache was 92 % busy and the 8 K prompt took 740 us, against 607 at
+// that step.)
 //   keys    piece j of token r's D / 16 at j ^ key(r): the rows that an 8-lane cycle reads
 //           are 4 neighbours of two blocks of 16;
 //   values  piece j of channel d's four at j ^ (d / 2 % 4).
@@ -1016,13 +1018,16 @@ Plan plan_of(int64_t b, int64_t rows, int32_t hq, int32_t hkv, int32_t d, int32_
     const int64_t by_rows = rows * ((G + tc - 1) / tc), by_cols = rows * G / tc + b;
     return by_rows < by_cols ? by_rows : by_cols;
   };
-  // Up to 64 columns of a sequence: 16 (8 sequences of 16 rows of 4 heads behind 4000
-  // tokens: 27 us, 29 with 32, 33 with 128; of 5 rows: 18, 23, 44).  More: 128 columns,
-  // which share what they read among four waves, but for long contexts in too few
-  // such tiles to fill the card, which 32 columns on the line share out evenly (24 rows
-  // behind 4000: 28 us, 53 with 128; one sequence of 200 rows: 37, 44; 96 rows, 160
-  // tiles: 83, 61; 40 sequences of 48 rows behind 2000, 560 tiles: 68, 54; of 20 rows
-  // behind 100: 21, 10).
+  // `steps` is what the block table holds: the host does not know the lengths, so a table
+  // far wider than its contexts is planned for as long ones are.  Microseconds of tables as
+  // wide as their contexts, sequences x rows of 4 heads behind so many tokens:
+  //   up to 64 columns of a sequence: 16 (8 x 16 behind 4000: 27, 29 with 32, 33 with 128;
+  //   8 x 5: 18, 23, 44);
+  //   more: 128, which share what they read among four waves (8 x 96 behind 4000, 160 tiles:
+  //   61, 83 with 32; 40 x 48 behind 2000, 560 tiles: 54, 68; 20 x 20 behind 100: 10, 21);
+  //   but 32 on the line, which shares its steps out evenly, where few such tiles stand
+  //   under a table of more than 32 steps (8 x 24 behind 4000: 28, 53 with 128; 1 x 200
+  //   behind 4000: 37, 44).
   const int64_t cols = max_q * G, t128 = tiles_of(128) * hkv;
   p.tc = cols <= 64 ? 16 : steps <= 32 ? 128 : t128 < 144 || (cols <= 128 && t128 < 400) ? 32 : 128;
   if (p.tc < 128 && tiles_of(p.tc) * steps >= (1ll << 31)) p.tc = 128;    // the line is 32 bits long
@@ -1030,7 +1035,8 @@ Plan plan_of(int64_t b, int64_t rows, int32_t hq, int32_t hkv, int32_t d, int32_
   if (p.tc < 128) {
     // Work-groups of eight waves: up to 8 steps a tile is one round of them, and
     // sharing it pays only for the launch that joins; up to 16 where nothing else
-    // would need that launch (one sequence of 700 tokens: 8.6 us, 10.5 shared).
+    // would need that launch (one sequence of 700 tokens: 8.5 us under a table of its own
+    // width; 10.3 under one wider than 16 steps, whose launch finds nothing to join).
     p.whole = tiles * hkv < 64 ? 16 : 8;
     p.min_steps = 4;
     // One work-group of eight waves on each CU; four of two waves where there are so
