@@ -599,6 +599,128 @@ awq_status awq_attn_kv8_bf16(const awq_kv8_cache* cache, int64_t rows, int64_t m
                              uint16_t* out, int64_t out_stride, float* lse,
                              void* workspace, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * awq_linear_w4a16_act, awq_linear_w4a16_act_bf16 -- the 4-bit linear with what
+ * follows it in its epilogue: bias, activation (of its output, or of a gate that
+ * multiplies a second projection of the same input) and the residual's addition.
+ * Passage: as awq_linear_w4a16; bjdmk.com.cn page, section "融合模块优化" (merging
+ * computation steps into one operation).
+ *
+ *   v[t][j] = sum_k x_tilde_tk (q_jk - z_j) D_j,  j = 0 .. n - 1
+ *   not gated: y[t][o] = act(v[t][o] + bias[o]) + residual[t][o]
+ *   gated:     y[t][o] = act(v[t][o] + bias[o]) (v[t][n + o] + bias[n + o]) + residual[t][o]
+ *              of 2 n weight rows: the gate's n, then the n it multiplies (packed
+ *              from the two weights stacked, as awq_search_scale takes them).
+ *   act: AWQ_ACT_NONE; AWQ_ACT_SILU v / (1 + e^-v); AWQ_ACT_GELU v Phi(v), Phi the
+ *   normal distribution; AWQ_ACT_GELU_TANH v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2.
+ *   Sums, bias, activation, product and residual are fp32, rounded once to the
+ *   type of y.  x_tilde = fp16_rn(x inv_s16) or x; bf16 x is rounded once to fp16
+ *   first (see awq_linear_w4a16_bf16 for its range); weights enter the products
+ *   exactly or as fp16_rn((q - z) D), by the number of rows and g.
+ *   Before the activation the sum is within 5e-3 * max(|v_ref|, rms of the row of
+ *   v_ref) of the float64 value.
+ *   x [m][k], residual, y [m][n], bias [n] ([2 n] gated): fp16 (bf16); bias and
+ *   residual may be NULL; residual may be y.  x, inv_s16 and qweight 16-byte aligned,
+ *   scales and qzeros 4-byte aligned.  workspace:
+ *   awq_linear_act_workspace_size(m, n, k, g, gated, inv_s16 != NULL, bf16) bytes,
+ *   256-byte aligned (NULL if that is 0).
+ *   Limits: g in {32, 64, 128}; k % g == 0; k % 64 == 0; 0 <= m <= 2^27; packed weights
+ *   below 4 GiB; m * n/4, m * k/8 <= 2^31.
+ * ------------------------------------------------------------------------- */
+enum { AWQ_ACT_NONE = 0, AWQ_ACT_SILU = 1, AWQ_ACT_GELU = 2, AWQ_ACT_GELU_TANH = 3 };
+size_t awq_linear_act_workspace_size(int64_t m, int64_t n, int64_t k, int32_t g, int32_t gated,
+                                     int32_t has_inv_s16, int32_t bf16);
+awq_status awq_linear_w4a16_act(const uint16_t* x, const uint32_t* qweight, const uint16_t* scales,
+                                const uint32_t* qzeros, const uint16_t* inv_s16, const uint16_t* bias,
+                                const uint16_t* residual, int32_t act, int32_t gated, int64_t m, int64_t n,
+                                int64_t k, int32_t g, uint16_t* y, void* workspace, size_t ws_bytes,
+                                void* stream);
+awq_status awq_linear_w4a16_act_bf16(const uint16_t* x, const uint32_t* qweight, const uint16_t* scales,
+                                     const uint32_t* qzeros, const uint16_t* inv_s16,
+                                     const uint16_t* bias, const uint16_t* residual, int32_t act,
+                                     int32_t gated, int64_t m, int64_t n, int64_t k, int32_t g,
+                                     uint16_t* y, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Mixture of experts: awq_moe_route, awq_moe_linear_w4a16, awq_moe_combine.
+ * A block whose linears are e experts' sends each of t tokens through topk of them:
+ *   awq_moe_route (from the router's logits) -> awq_moe_linear_w4a16 (gate and up,
+ *   gated, rows gathered from the tokens) -> awq_moe_linear_w4a16 (down) ->
+ *   awq_moe_combine (weights and residual).
+ * Row counts of the experts stay on the device: a captured block replays with
+ * whatever routing it computes.
+ *
+ * awq_moe_route:
+ *   logits [t][e] fp32, fp16 or bf16 (AWQ_LOGITS_*).  Token i's experts are those of
+ *   its topk largest logits, ties to the lower expert, best first.  An expert whose
+ *   logit is -inf or NaN is closed to the token.
+ *   ids [t][topk] int32: the experts; -1 where fewer are open.
+ *   weights [t][topk] fp32: scale * p of the expert, p in fp32:
+ *     AWQ_ROUTE_SOFTMAX  exp(x_j - max) / sum of exp(x - max) over all experts, or
+ *                        renormalize: over the chosen ones;
+ *     AWQ_ROUTE_SIGMOID  1 / (1 + exp(-x_j)); renormalize: divided by the sum of the
+ *                        chosen ones' (0 where that is 0).
+ *   0 where the id is -1.  All weights of a token with a NaN logit are NaN, and with
+ *   softmax those of a token with a logit of +inf.
+ *   offsets [e + 1] int32: rows offsets[j] .. offsets[j + 1] - 1 are expert j's.
+ *   row_slot [t * topk] int32: row r stands for slot row_slot[r] = token * topk + choice;
+ *     rows by expert, then by slot.  Rows from offsets[e] on are not written.
+ *   slot_row [t][topk] int32: the row of a slot, -1 where its id is.
+ *   workspace: awq_moe_route_workspace_size(t, e) bytes, 256-byte aligned (NULL if 0).
+ *   Limits: 0 <= t <= 2^24; 1 <= e <= 1024; 1 <= topk <= min(e, 32); t * topk <= 2^27;
+ *   scale > 0.
+ *
+ * awq_moe_linear_w4a16, _bf16: awq_linear_w4a16_act of every expert on its rows.
+ *   qweight [e][nw][k/8], scales [e][nw][k/g], qzeros [e][nw][ceil(k/(8g))] in layout v1
+ *   (nw = n, gated 2 n), bias [e][nw] or NULL, inv_s16 [k] (one for all experts, as
+ *   projections of one input share it) or NULL (folded: awq_fold_inv_scale and
+ *   awq_fold_inv_scale_rows).  Row r of y [rows][n] reads x[row_slot[r] / topk] of
+ *   x [x_rows][k], or with row_slot NULL x[r] of x [rows][k] (x_rows is not read).
+ *   offsets and row_slot are device data and not checked on the host: whatever they
+ *   hold, nothing outside the tensors is read or written.  Rows of y that no expert
+ *   has are not written.  rows: what row_slot and y hold, at least offsets[e].  The
+ *   number of rows and experts chooses between kernels; results are right for any
+ *   split of the rows.
+ *   workspace: awq_moe_linear_workspace_size(rows, x_rows, e, n, k, g, gated,
+ *     inv_s16 != NULL, bf16) bytes (x_rows = rows without row_slot), 256-byte aligned.
+ *   Limits: those of awq_linear_w4a16_act with rows for m, packed weights of one expert
+ *   below 4 GiB; 1 <= e <= 1024; 1 <= topk <= 32; with row_slot x below 4 GiB.
+ *
+ * awq_moe_combine, _bf16:
+ *   y[i] = residual[i] + sum_j weights[i][j] rows[slot_row[i][j]], fp32 in the order of j,
+ *   rounded once.  A slot_row outside 0 .. row_count - 1 adds its weight times zero.
+ *   rows [row_count][n], residual [t][n] or NULL (may be y), y [t][n]: fp16 (bf16).
+ *   Limits: t <= 2^24; 1 <= n <= 2^24; topk <= 32; row_count <= 2^27; t * n/8 (t * n where
+ *   n % 8) <= 2^31.
+ * ------------------------------------------------------------------------- */
+enum { AWQ_LOGITS_F32 = 0, AWQ_LOGITS_F16 = 1, AWQ_LOGITS_BF16 = 2 };
+enum { AWQ_ROUTE_SOFTMAX = 0, AWQ_ROUTE_SIGMOID = 1 };
+size_t awq_moe_route_workspace_size(int64_t t, int32_t e);
+awq_status awq_moe_route(const void* logits, int32_t logits_type, int64_t t, int32_t e, int32_t topk,
+                         int32_t scoring, int32_t renormalize, float scale, int32_t* ids, float* weights,
+                         int32_t* offsets, int32_t* row_slot, int32_t* slot_row, void* workspace,
+                         size_t ws_bytes, void* stream);
+size_t awq_moe_linear_workspace_size(int64_t rows, int64_t x_rows, int32_t e, int64_t n, int64_t k,
+                                     int32_t g, int32_t gated, int32_t has_inv_s16, int32_t bf16);
+awq_status awq_moe_linear_w4a16(const uint16_t* x, int64_t x_rows, const uint32_t* qweight,
+                                const uint16_t* scales, const uint32_t* qzeros, const uint16_t* inv_s16,
+                                const uint16_t* bias, int32_t act, int32_t gated, int32_t e,
+                                const int32_t* offsets, const int32_t* row_slot, int32_t topk, int64_t rows,
+                                int64_t n, int64_t k, int32_t g, uint16_t* y, void* workspace,
+                                size_t ws_bytes, void* stream);
+awq_status awq_moe_linear_w4a16_bf16(const uint16_t* x, int64_t x_rows, const uint32_t* qweight,
+                                     const uint16_t* scales, const uint32_t* qzeros, const uint16_t* inv_s16,
+                                     const uint16_t* bias, int32_t act, int32_t gated, int32_t e,
+                                     const int32_t* offsets, const int32_t* row_slot, int32_t topk,
+                                     int64_t rows, int64_t n, int64_t k, int32_t g, uint16_t* y,
+                                     void* workspace, size_t ws_bytes, void* stream);
+awq_status awq_moe_combine(const uint16_t* rows, int64_t row_count, const float* weights,
+                           const int32_t* slot_row, const uint16_t* residual, int64_t t, int64_t n,
+                           int32_t topk, uint16_t* y, void* stream);
+awq_status awq_moe_combine_bf16(const uint16_t* rows, int64_t row_count, const float* weights,
+                                const int32_t* slot_row, const uint16_t* residual, int64_t t, int64_t n,
+                                int32_t topk, uint16_t* y, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

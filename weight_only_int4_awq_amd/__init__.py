@@ -14,6 +14,10 @@ the library's HIP kernels; there is no fallback.
     awq_rope_table(positions, rot)              -> table fp32 [positions, rot]
     awq_kv8_append(k, v, *cache, block_table, ctx, q=q, rope=table) -> rotated q
     awq_attn_kv8(q, *cache, block_table, ctx)   -> out [rows, hq, d]
+    awq_linear_w4a16_act(x, qweight, scales, qzeros, bias=, act=, gated=, residual=) -> y [m, n]
+    awq_moe_route(logits, topk)                 -> (ids, weights, offsets, row_slot, slot_row)
+    awq_moe_linear_w4a16(x, qweight, scales, qzeros, offsets, row_slot, topk) -> y [rows, n]
+    awq_moe_combine(rows, weights, slot_row, residual) -> y [t, n]
 
 The linear calls take an optional ``workspace`` (a uint8 device tensor of at
 least the size the library's query returns); without one the binding
@@ -32,7 +36,10 @@ __all__ = ["awq_calib_stats", "awq_search_workspace_size", "awq_search_scale", "
            "awq_salient_channels", "awq_channel_mask", "awq_gather_channels", "awq_mixed_loss",
            "awq_linear_mixed", "awq_fold_inv_scale_rows", "awq_linear_w4a16_group_noalloc",
            "awq_rope_table", "awq_kv8_append", "awq_kv8_append_bf16", "awq_attn_kv8", "awq_attn_kv8_bf16",
-           "awq_attn_kv8_workspace_size", "kv8_cache", "AWQError", "load"]
+           "awq_attn_kv8_workspace_size", "kv8_cache", "awq_linear_w4a16_act", "awq_linear_w4a16_act_bf16",
+           "awq_linear_act_workspace_size", "awq_moe_route", "awq_moe_route_workspace_size", "awq_moe_linear_w4a16",
+           "awq_moe_linear_w4a16_bf16", "awq_moe_linear_workspace_size", "awq_moe_combine", "awq_moe_combine_bf16",
+           "AWQError", "load"]
 
 
 def load():
@@ -740,4 +747,249 @@ def _attn_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx, cu_q, max
         raise ValueError(f"workspace must be on the cache's device, cuda:{dev} (got {workspace.device})")
     _call("awq_attn_kv8_bf16" if bf else "awq_attn_kv8", dev, _lib.byref(c), rows, max_q, q.data_ptr(), qs, hq,
           d ** -0.5 if scale is None else scale, out.data_ptr(), os, _ptr(lse), wp, wb)
+    return out
+
+
+# ---------------------------------------------------------------- linears with an epilogue, mixture of experts
+
+_ACT = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3}
+_SCORING = {"softmax": 0, "sigmoid": 1}
+
+
+def _same(t, dtype, shape, dev):
+    """Whether t is a packed tensor of this type, shape and device (index); None is."""
+    return t is None or (t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous())
+
+
+def _refuse(dev, *checks):
+    """Raises for the first (tensor, dtype, shape, name) that is not as it should be."""
+    for t, dtype, shape, name in checks:
+        if t is not None:
+            _out_tensor(t, dtype, shape, name)
+            if t.get_device() != dev:
+                raise ValueError(f"{name} must be on cuda:{dev} (got {t.device})")
+    raise ValueError("tensors do not fit together")
+
+
+def _scratch(need, dev, workspace):
+    """(pointer, bytes) of a call's workspace on device ``dev`` (an index)."""
+    if not need:
+        return None, 0
+    torch = _torch()
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _dev_tensor(workspace, torch.uint8, "workspace")
+        if workspace.get_device() != dev:
+            raise ValueError(f"workspace must be on cuda:{dev} (got {workspace.device})")
+    return workspace.data_ptr(), workspace.numel()
+
+
+def _act_code(act, gated):
+    if act not in _ACT:
+        raise ValueError(f"act must be one of {sorted(_ACT)} (got {act!r})")
+    return _ACT[act], 1 if gated else 0
+
+
+def awq_linear_act_workspace_size(m, n, k, g=128, gated=False, has_inv_s16=True, bf16=False):
+    """Device scratch bytes of awq_linear_w4a16_act (n: output columns)."""
+    return int(_lib.load().awq_linear_act_workspace_size(m, n, k, g, 1 if gated else 0, 1 if has_inv_s16 else 0,
+                                                         1 if bf16 else 0))
+
+
+def awq_linear_w4a16_act(x, qweight, scales, qzeros, inv_s16=None, bias=None, act="none", gated=False, residual=None,
+                         g=128, out=None, workspace=None):
+    """awq_linear_w4a16 with bias, activation and residual in its epilogue: x fp16 [m, k]
+    -> fp16 [m, n].
+
+    act: "none", "silu", "gelu" or "gelu_tanh".  gated: the packed rows are the gate's n,
+    then the n it multiplies (y = act(gate) * up).  bias: fp16, one per packed row.
+    residual: fp16 [m, n], added last (may be ``out``)."""
+    return _linear_act(x, qweight, scales, qzeros, inv_s16, bias, act, gated, residual, g, out, workspace, False)
+
+
+def awq_linear_w4a16_act_bf16(x, qweight, scales, qzeros, inv_s16=None, bias=None, act="none", gated=False,
+                              residual=None, g=128, out=None, workspace=None):
+    """awq_linear_w4a16_act with bf16 x, bias, residual and out."""
+    return _linear_act(x, qweight, scales, qzeros, inv_s16, bias, act, gated, residual, g, out, workspace, True)
+
+
+def _linear_act(x, qweight, scales, qzeros, inv_s16, bias, act, gated, residual, g, out, workspace, bf):
+    torch = _torch()
+    f16, i32 = torch.float16, torch.int32
+    dt = torch.bfloat16 if bf else f16
+    act, gated = _act_code(act, gated)
+    try:
+        dev = x.get_device()
+        m, k = x.shape
+        nw = qweight.shape[0]
+        n = nw // 2 if gated else nw
+        checks = ((x, dt, (m, k), "x"), (qweight, i32, (nw, k // 8), "qweight"), (scales, f16, (nw, k // g), "scales"),
+                  (qzeros, i32, (nw, -(-k // (8 * g))), "qzeros"), (inv_s16, f16, (k,), "inv_s16"),
+                  (bias, dt, (nw,), "bias"), (residual, dt, (m, n), "residual"), (out, dt, (m, n), "out"))
+        good = dev >= 0 and not (gated and nw % 2) and all(_same(*c[:3], dev) for c in checks)
+    except (AttributeError, TypeError, ValueError):
+        _dev_tensor(x, dt, "x", 2)
+        _dev_tensor(qweight, i32, "qweight", 2)
+        raise
+    if not good:
+        _dev_tensor(x, dt, "x", 2)
+        if gated and nw % 2:
+            raise ValueError("gated: qweight must have an even number of rows")
+        _refuse(dev, *checks)
+    if out is None:
+        out = torch.empty((m, n), dtype=dt, device=x.device)
+    need = _lib.load().awq_linear_act_workspace_size(m, n, k, g, gated, inv_s16 is not None, bf)
+    wp, wb = _scratch(need, dev, workspace)
+    _call("awq_linear_w4a16_act_bf16" if bf else "awq_linear_w4a16_act", dev, x.data_ptr(), qweight.data_ptr(),
+          scales.data_ptr(), qzeros.data_ptr(), _ptr(inv_s16), _ptr(bias), _ptr(residual), act, gated, m, n, k, g,
+          out.data_ptr(), wp, wb)
+    return out
+
+
+def awq_moe_route_workspace_size(t, e):
+    """Device scratch bytes of awq_moe_route (0 for few tokens)."""
+    return int(_lib.load().awq_moe_route_workspace_size(t, e))
+
+
+def awq_moe_route(logits, topk, scoring="softmax", renormalize=True, scale=1.0, out=None, workspace=None):
+    """Routes tokens to experts: logits fp32, fp16 or bf16 [t, e] -> (ids int32 [t, topk],
+    weights fp32 [t, topk], offsets int32 [e + 1], row_slot int32 [t * topk], slot_row
+    int32 [t, topk]), written into ``out`` when given.
+
+    The topk largest logits, ties to the lower expert; -inf and NaN are closed (id -1,
+    weight 0, no row).  scoring: "softmax" (over all experts; renormalize: over the chosen
+    ones) or "sigmoid" (renormalize: divided by the chosen ones' sum); weights are times
+    ``scale``.  Rows offsets[j] .. offsets[j + 1] - 1 are expert j's; row r stands for slot
+    row_slot[r] = token * topk + choice; rows from offsets[e] on are left as they were."""
+    torch = _torch()
+    i32 = torch.int32
+    if scoring not in _SCORING:
+        raise ValueError(f"scoring must be one of {sorted(_SCORING)} (got {scoring!r})")
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    kind = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}.get(logits.dtype)
+    if kind is None:
+        raise TypeError(f"logits must be float32, float16 or bfloat16 (got {logits.dtype})")
+    _dev_tensor(logits, logits.dtype, "logits", 2)
+    dev = logits.get_device()
+    t, e = logits.shape
+    if out is None:
+        if not 1 <= topk <= e:
+            raise ValueError(f"topk must be between 1 and the {e} experts (got {topk})")
+        at = logits.device
+        out = (torch.empty((t, topk), dtype=i32, device=at), torch.empty((t, topk), dtype=torch.float32, device=at),
+               torch.empty(e + 1, dtype=i32, device=at), torch.empty(t * topk, dtype=i32, device=at),
+               torch.empty((t, topk), dtype=i32, device=at))
+    ids, weights, offsets, row_slot, slot_row = out
+    checks = ((ids, i32, (t, topk), "ids"), (weights, torch.float32, (t, topk), "weights"),
+              (offsets, i32, (e + 1,), "offsets"), (row_slot, i32, (t * topk,), "row_slot"),
+              (slot_row, i32, (t, topk), "slot_row"))
+    try:
+        good = all(o is not None for o in out) and all(_same(*c[:3], dev) for c in checks)
+    except (AttributeError, TypeError):
+        good = False
+    if not good:
+        _refuse(dev, *checks)
+    wp, wb = _scratch(_lib.load().awq_moe_route_workspace_size(t, e), dev, workspace)
+    _call("awq_moe_route", dev, logits.data_ptr(), kind, t, e, topk, _SCORING[scoring], 1 if renormalize else 0, scale,
+          ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), row_slot.data_ptr(), slot_row.data_ptr(), wp, wb)
+    return ids, weights, offsets, row_slot, slot_row
+
+
+def awq_moe_linear_workspace_size(rows, x_rows, e, n, k, g=128, gated=False, has_inv_s16=False, bf16=False):
+    """Device scratch bytes of awq_moe_linear_w4a16 (x_rows = rows without row_slot)."""
+    return int(_lib.load().awq_moe_linear_workspace_size(rows, x_rows, e, n, k, g, 1 if gated else 0,
+                                                         1 if has_inv_s16 else 0, 1 if bf16 else 0))
+
+
+def awq_moe_linear_w4a16(x, qweight, scales, qzeros, offsets, row_slot=None, topk=1, inv_s16=None, bias=None,
+                         act="none", gated=False, g=128, out=None, workspace=None):
+    """awq_linear_w4a16_act of every expert on its rows -> fp16 [rows, n].
+
+    qweight int32 [e, nw, k/8], scales fp16 [e, nw, k/g], qzeros int32 [e, nw, ceil(k/(8g))]
+    (nw = n, gated 2 n: the gate's rows first); offsets int32 [e + 1]: rows offsets[j] ..
+    offsets[j + 1] - 1 are expert j's.  row_slot int32 [rows] (awq_moe_route): row r reads
+    x[row_slot[r] // topk] of x fp16 [t, k]; without it row r reads x[r].  inv_s16 fp16 [k]
+    for all experts, bias fp16 [e, nw].  Rows of no expert are left as they were."""
+    return _moe_linear(x, qweight, scales, qzeros, offsets, row_slot, topk, inv_s16, bias, act, gated, g, out,
+                       workspace, False)
+
+
+def awq_moe_linear_w4a16_bf16(x, qweight, scales, qzeros, offsets, row_slot=None, topk=1, inv_s16=None, bias=None,
+                              act="none", gated=False, g=128, out=None, workspace=None):
+    """awq_moe_linear_w4a16 with bf16 x, bias and out."""
+    return _moe_linear(x, qweight, scales, qzeros, offsets, row_slot, topk, inv_s16, bias, act, gated, g, out,
+                       workspace, True)
+
+
+def _moe_linear(x, qweight, scales, qzeros, offsets, row_slot, topk, inv_s16, bias, act, gated, g, out, workspace, bf):
+    torch = _torch()
+    f16, i32 = torch.float16, torch.int32
+    dt = torch.bfloat16 if bf else f16
+    act, gated = _act_code(act, gated)
+    try:
+        dev = x.get_device()
+        t, k = x.shape
+        e, nw, _ = qweight.shape
+        n = nw // 2 if gated else nw
+        rows = t if row_slot is None else row_slot.shape[0]
+        checks = ((x, dt, (t, k), "x"), (qweight, i32, (e, nw, k // 8), "qweight"),
+                  (scales, f16, (e, nw, k // g), "scales"), (qzeros, i32, (e, nw, -(-k // (8 * g))), "qzeros"),
+                  (offsets, i32, (e + 1,), "offsets"), (row_slot, i32, (rows,), "row_slot"),
+                  (inv_s16, f16, (k,), "inv_s16"), (bias, dt, (e, nw), "bias"), (out, dt, (rows, n), "out"))
+        good = dev >= 0 and offsets is not None and not (gated and nw % 2) and all(_same(*c[:3], dev) for c in checks)
+    except (AttributeError, TypeError, ValueError):
+        _dev_tensor(x, dt, "x", 2)
+        _dev_tensor(qweight, i32, "qweight", 3)
+        raise
+    if not good:
+        _dev_tensor(x, dt, "x", 2)
+        if gated and nw % 2:
+            raise ValueError("gated: qweight must have an even number of rows")
+        _refuse(dev, *checks)
+    if out is None:
+        out = torch.empty((rows, n), dtype=dt, device=x.device)
+    need = _lib.load().awq_moe_linear_workspace_size(rows, t, e, n, k, g, gated, inv_s16 is not None, bf)
+    wp, wb = _scratch(need, dev, workspace)
+    _call("awq_moe_linear_w4a16_bf16" if bf else "awq_moe_linear_w4a16", dev, x.data_ptr(), t, qweight.data_ptr(),
+          scales.data_ptr(), qzeros.data_ptr(), _ptr(inv_s16), _ptr(bias), act, gated, e, offsets.data_ptr(),
+          _ptr(row_slot), topk, rows, n, k, g, out.data_ptr(), wp, wb)
+    return out
+
+
+def awq_moe_combine(rows, weights, slot_row, residual=None, out=None):
+    """y[i] = residual[i] + sum_j weights[i, j] rows[slot_row[i, j]]: rows fp16 [r, n], weights
+    fp32 and slot_row int32 [t, topk] (awq_moe_route), residual fp16 [t, n] or None (may be
+    ``out``) -> fp16 [t, n], summed in fp32.  Slots without a row (-1) add nothing."""
+    return _moe_combine(rows, weights, slot_row, residual, out, False)
+
+
+def awq_moe_combine_bf16(rows, weights, slot_row, residual=None, out=None):
+    """awq_moe_combine with bf16 rows, residual and out."""
+    return _moe_combine(rows, weights, slot_row, residual, out, True)
+
+
+def _moe_combine(rows, weights, slot_row, residual, out, bf):
+    torch = _torch()
+    dt = torch.bfloat16 if bf else torch.float16
+    try:
+        dev = rows.get_device()
+        r, n = rows.shape
+        t, topk = weights.shape
+        checks = ((rows, dt, (r, n), "rows"), (weights, torch.float32, (t, topk), "weights"),
+                  (slot_row, torch.int32, (t, topk), "slot_row"), (residual, dt, (t, n), "residual"),
+                  (out, dt, (t, n), "out"))
+        good = dev >= 0 and slot_row is not None and all(_same(*c[:3], dev) for c in checks)
+    except (AttributeError, TypeError, ValueError):
+        _dev_tensor(rows, dt, "rows", 2)
+        _dev_tensor(weights, torch.float32, "weights", 2)
+        raise
+    if not good:
+        _dev_tensor(rows, dt, "rows", 2)
+        _refuse(dev, *checks)
+    if out is None:
+        out = torch.empty((t, n), dtype=dt, device=rows.device)
+    _call("awq_moe_combine_bf16" if bf else "awq_moe_combine", dev, rows.data_ptr(), r, weights.data_ptr(),
+          slot_row.data_ptr(), _ptr(residual), t, n, topk, out.data_ptr())
     return out

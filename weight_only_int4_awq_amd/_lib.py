@@ -97,6 +97,26 @@ SIGNATURES["awq_attn_kv8"] = (C.c_int, [C.c_void_p, C.c_int64, C.c_int64, C.c_vo
                                         C.c_float, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_size_t,
                                         C.c_void_p])
 SIGNATURES["awq_attn_kv8_bf16"] = SIGNATURES["awq_attn_kv8"]
+SIGNATURES["awq_linear_act_workspace_size"] = (C.c_size_t, [C.c_int64, C.c_int64, C.c_int64, C.c_int32, C.c_int32,
+                                                            C.c_int32, C.c_int32])
+SIGNATURES["awq_linear_w4a16_act"] = (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                                C.c_void_p, C.c_int32, C.c_int32, C.c_int64, C.c_int64, C.c_int64,
+                                                C.c_int32, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p])
+SIGNATURES["awq_linear_w4a16_act_bf16"] = SIGNATURES["awq_linear_w4a16_act"]
+SIGNATURES["awq_moe_route_workspace_size"] = (C.c_size_t, [C.c_int64, C.c_int32])
+SIGNATURES["awq_moe_route"] = (C.c_int, [C.c_void_p, C.c_int32, C.c_int64, C.c_int32, C.c_int32, C.c_int32, C.c_int32,
+                                         C.c_float, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                         C.c_void_p, C.c_size_t, C.c_void_p])
+SIGNATURES["awq_moe_linear_workspace_size"] = (C.c_size_t, [C.c_int64, C.c_int64, C.c_int32, C.c_int64, C.c_int64,
+                                                            C.c_int32, C.c_int32, C.c_int32, C.c_int32])
+SIGNATURES["awq_moe_linear_w4a16"] = (C.c_int, [C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                                C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p,
+                                                C.c_int32, C.c_int64, C.c_int64, C.c_int64, C.c_int32, C.c_void_p,
+                                                C.c_void_p, C.c_size_t, C.c_void_p])
+SIGNATURES["awq_moe_linear_w4a16_bf16"] = SIGNATURES["awq_moe_linear_w4a16"]
+SIGNATURES["awq_moe_combine"] = (C.c_int, [C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64,
+                                           C.c_int64, C.c_int32, C.c_void_p, C.c_void_p])
+SIGNATURES["awq_moe_combine_bf16"] = SIGNATURES["awq_moe_combine"]
 
 _lib = None
 

@@ -725,4 +725,231 @@ awq_status awq_attn_kv8_bf16(const awq_kv8_cache* cache, int64_t rows, int64_t m
                        workspace, ws_bytes, true, stream);
 }
 
+// ---------------------------------------------------------------- experts, and linears with an epilogue
+
+size_t awq_moe_route_workspace_size(int64_t t, int32_t e) {
+  if (t < 0 || t > (1 << 24) || e < 1 || e > 1024) return 0;
+  return awq::moe_route_scratch_bytes(t, e);
+}
+
+awq_status awq_moe_route(const void* logits, int32_t logits_type, int64_t t, int32_t e, int32_t topk,
+                         int32_t scoring, int32_t renormalize, float scale, int32_t* ids, float* weights,
+                         int32_t* offsets, int32_t* row_slot, int32_t* slot_row, void* workspace, size_t ws_bytes,
+                         void* stream) {
+  g_err[0] = 0;
+  if (logits_type < AWQ_LOGITS_F32 || logits_type > AWQ_LOGITS_BF16)
+    return fail(AWQ_ERR_SHAPE, "awq_moe_route: logits_type=%lld unknown", logits_type);
+  if (scoring != AWQ_ROUTE_SOFTMAX && scoring != AWQ_ROUTE_SIGMOID)
+    return fail(AWQ_ERR_SHAPE, "awq_moe_route: scoring=%lld unknown", scoring);
+  if (e < 1 || e > 1024) return fail(AWQ_ERR_SHAPE, "awq_moe_route: e=%lld outside 1..1024", e);
+  if (topk < 1 || topk > 32 || topk > e)
+    return fail(AWQ_ERR_SHAPE, "awq_moe_route: topk=%lld outside 1..32 or above e=%lld", topk, e);
+  if (t < 0 || t > (1 << 24) || t * topk > (1 << 27))
+    return fail(AWQ_ERR_SHAPE, "awq_moe_route: t=%lld outside 0..2^24, or t * topk above 2^27", t);
+  if (!(scale > 0.0f) || !(scale < 1e30f))
+    return fail(AWQ_ERR_SHAPE, "awq_moe_route: scale must be positive and finite");
+  if (!offsets || (t > 0 && (!logits || !ids || !weights || !row_slot || !slot_row)))
+    return fail(AWQ_ERR_NULL, "awq_moe_route: null pointer");
+  if (!aligned(logits, logits_type == AWQ_LOGITS_F32 ? 4 : 2) || !aligned(ids, 4) || !aligned(weights, 4) ||
+      !aligned(offsets, 4) || !aligned(row_slot, 4) || !aligned(slot_row, 4))
+    return fail(AWQ_ERR_ALIGN, "awq_moe_route: misaligned pointer");
+  const size_t need = awq::moe_route_scratch_bytes(t, e);
+  if (need > 0) {
+    if (!workspace || ws_bytes < need)
+      return fail(AWQ_ERR_WORKSPACE, "awq_moe_route: workspace of %lld bytes < %lld needed", (long long)ws_bytes,
+                  (long long)need);
+    if (!aligned(workspace, 256)) return fail(AWQ_ERR_ALIGN, "awq_moe_route: workspace must be 256-byte aligned");
+  }
+  hipError_t err = awq::launch_moe_route(logits, logits_type, t, e, topk, scoring, renormalize != 0, scale, ids, weights,
+                                         offsets, row_slot, slot_row, workspace, (hipStream_t)stream);
+  if (err != hipSuccess) return hip_fail(err, "awq_moe_route");
+  return AWQ_OK;
+}
+
+static awq_status moe_combine_impl(const char* fn, const uint16_t* rows, int64_t row_count, const float* weights,
+                                   const int32_t* slot_row, const uint16_t* residual, int64_t t, int64_t n,
+                                   int32_t topk, bool bf, uint16_t* y, void* stream) {
+  g_err[0] = 0;
+  char msg[128];
+  auto err = [&](awq_status s, const char* what, long long x = 0, long long z = 0) {
+    snprintf(msg, sizeof(msg), "%s: %s", fn, what);
+    return fail(s, msg, x, z);
+  };
+  if (topk < 1 || topk > 32) return err(AWQ_ERR_SHAPE, "topk=%lld outside 1..32", topk);
+  if (n < 1 || n > (1 << 24)) return err(AWQ_ERR_SHAPE, "n=%lld outside 1..2^24", n);
+  if (t < 0 || t > (1 << 24)) return err(AWQ_ERR_SHAPE, "t=%lld outside 0..2^24", t);
+  if (row_count < 0 || row_count > (1 << 27)) return err(AWQ_ERR_SHAPE, "rows=%lld outside 0..2^27", row_count);
+  if (t * (n % 8 ? n : n / 8) > (1ll << 31)) return err(AWQ_ERR_SHAPE, "t=%lld tokens of n=%lld are more than one launch holds", t, n);
+  if (t == 0) return AWQ_OK;
+  if (!weights || !slot_row || !y || (row_count > 0 && !rows)) return err(AWQ_ERR_NULL, "null pointer");
+  if (!aligned(rows, 2) || !aligned(residual, 2) || !aligned(y, 2) || !aligned(weights, 4) || !aligned(slot_row, 4))
+    return err(AWQ_ERR_ALIGN, "misaligned pointer");
+  hipError_t e = awq::launch_moe_combine(rows, row_count, weights, slot_row, residual, t, n, topk, bf, y,
+                                         (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return AWQ_OK;
+}
+
+awq_status awq_moe_combine(const uint16_t* rows, int64_t row_count, const float* weights, const int32_t* slot_row,
+                           const uint16_t* residual, int64_t t, int64_t n, int32_t topk, uint16_t* y, void* stream) {
+  return moe_combine_impl("awq_moe_combine", rows, row_count, weights, slot_row, residual, t, n, topk, false, y, stream);
+}
+
+awq_status awq_moe_combine_bf16(const uint16_t* rows, int64_t row_count, const float* weights,
+                                const int32_t* slot_row, const uint16_t* residual, int64_t t, int64_t n, int32_t topk,
+                                uint16_t* y, void* stream) {
+  return moe_combine_impl("awq_moe_combine_bf16", rows, row_count, weights, slot_row, residual, t, n, topk, true, y,
+                          stream);
+}
+
+// Sizes of a linear with an epilogue: AWQ_OK, or what is wrong with them.
+static awq_status act_sizes(const char* fn, awq::ActArgs& a) {
+  char msg[160];
+  auto err = [&](awq_status s, const char* what, long long x = 0, long long z = 0) {
+    snprintf(msg, sizeof(msg), "%s: %s", fn, what);
+    return fail(s, msg, x, z);
+  };
+  if (!group_ok(a.g)) return err(AWQ_ERR_SHAPE, "g=%lld not in {32,64,128}", a.g);
+  if (a.k < 64 || a.k > 0x7FFFFFFF || a.k % a.g || a.k % 64)
+    return err(AWQ_ERR_SHAPE, "k=%lld not a positive multiple of 64 and g=%lld", a.k, a.g);
+  if (a.n < 1 || a.n > 0x7FFFFFFF) return err(AWQ_ERR_SHAPE, "n=%lld out of range", a.n);
+  a.nw = a.gated ? 2 * a.n : a.n;
+  if (a.nw * (a.k / 2) >= (1ll << 32)) return err(AWQ_ERR_SHAPE, "packed weights of n=%lld, k=%lld reach 4 GiB", a.n, a.k);
+  if (a.act < AWQ_ACT_NONE || a.act > AWQ_ACT_GELU_TANH) return err(AWQ_ERR_SHAPE, "act=%lld unknown", a.act);
+  if (a.e < 1 || a.e > 1024) return err(AWQ_ERR_SHAPE, "e=%lld outside 1..1024", a.e);
+  if (a.topk < 1 || a.topk > 32) return err(AWQ_ERR_SHAPE, "topk=%lld outside 1..32", a.topk);
+  if (a.rows < 0 || a.rows > (1 << 27) || a.x_rows < 0 || a.x_rows > (1 << 27))
+    return err(AWQ_ERR_SHAPE, "rows=%lld or x_rows=%lld outside 0..2^27", a.rows, a.x_rows);
+  if (a.rows > 0 && a.x_rows > 0 && !awq::linear_act_fits(a))
+    return err(AWQ_ERR_SHAPE, "rows=%lld of n=%lld are more than one launch holds", a.rows, a.n);
+  return AWQ_OK;
+}
+
+static awq_status linear_act_impl(const char* fn, awq::ActArgs& a, void* workspace, size_t ws_bytes, void* stream) {
+  char msg[128];
+  auto err = [&](awq_status s, const char* what, long long x = 0, long long z = 0) {
+    snprintf(msg, sizeof(msg), "%s: %s", fn, what);
+    return fail(s, msg, x, z);
+  };
+  if (a.rows == 0) return AWQ_OK;
+  if (!a.x || !a.qw || !a.sc || !a.qz || !a.y) return err(AWQ_ERR_NULL, "null pointer");
+  if (!aligned(a.x, 16) || !aligned(a.qw, 16) || !aligned(a.inv, 16))
+    return err(AWQ_ERR_ALIGN, "x, inv_s16 and qweight must be 16-byte aligned");
+  if (!aligned(a.sc, 4) || !aligned(a.qz, 4)) return err(AWQ_ERR_ALIGN, "scales and qzeros must be 4-byte aligned");
+  if (!aligned(a.bias, 2) || !aligned(a.res, 2) || !aligned(a.y, 2) || !aligned(a.offsets, 4) || !aligned(a.row_slot, 4))
+    return err(AWQ_ERR_ALIGN, "misaligned pointer");
+  const size_t need = awq::linear_act_scratch_bytes(a);
+  if (need > 0) {
+    if (!workspace || ws_bytes < need)
+      return err(AWQ_ERR_WORKSPACE, "workspace of %lld bytes < %lld needed", (long long)ws_bytes, (long long)need);
+    if (!aligned(workspace, 256)) return err(AWQ_ERR_ALIGN, "workspace must be 256-byte aligned");
+  }
+  hipError_t e = awq::launch_linear_act(a, workspace, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return AWQ_OK;
+}
+
+static const int32_t kSomeOffsets = 0;       // a plan looks only at whether there are any
+static const uint16_t kSomeScale = 0;
+
+size_t awq_linear_act_workspace_size(int64_t m, int64_t n, int64_t k, int32_t g, int32_t gated, int32_t has_inv_s16,
+                                     int32_t bf16) {
+  awq::ActArgs a{};
+  a.inv = has_inv_s16 ? &kSomeScale : nullptr;
+  a.rows = a.x_rows = m;
+  a.n = n; a.k = k; a.g = g; a.e = 1; a.topk = 1;
+  a.gated = gated != 0; a.bf = bf16 != 0;
+  if (act_sizes("awq_linear_act_workspace_size", a) != AWQ_OK || m < 1) return 0;
+  return awq::linear_act_scratch_bytes(a);
+}
+
+size_t awq_moe_linear_workspace_size(int64_t rows, int64_t x_rows, int32_t e, int64_t n, int64_t k, int32_t g,
+                                     int32_t gated, int32_t has_inv_s16, int32_t bf16) {
+  awq::ActArgs a{};
+  a.inv = has_inv_s16 ? &kSomeScale : nullptr;
+  a.offsets = &kSomeOffsets;
+  a.rows = rows; a.x_rows = x_rows;
+  a.n = n; a.k = k; a.g = g; a.e = e; a.topk = 1;
+  a.gated = gated != 0; a.bf = bf16 != 0;
+  if (act_sizes("awq_moe_linear_workspace_size", a) != AWQ_OK || rows < 1 || x_rows < 1) return 0;
+  return awq::linear_act_scratch_bytes(a);
+}
+
+static awq_status dense_act(const char* fn, const uint16_t* x, const uint32_t* qweight, const uint16_t* scales,
+                            const uint32_t* qzeros, const uint16_t* inv_s16, const uint16_t* bias,
+                            const uint16_t* residual, int32_t act, int32_t gated, int64_t m, int64_t n, int64_t k,
+                            int32_t g, uint16_t* y, bool bf, void* workspace, size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  awq::ActArgs a{};
+  a.x = x; a.qw = qweight; a.sc = scales; a.qz = qzeros; a.inv = inv_s16; a.bias = bias; a.res = residual; a.y = y;
+  a.rows = a.x_rows = m;
+  a.n = n; a.k = k; a.g = g; a.e = 1; a.topk = 1;
+  a.act = act; a.gated = gated != 0; a.bf = bf;
+  const awq_status st = act_sizes(fn, a);
+  return st != AWQ_OK ? st : linear_act_impl(fn, a, workspace, ws_bytes, stream);
+}
+
+awq_status awq_linear_w4a16_act(const uint16_t* x, const uint32_t* qweight, const uint16_t* scales,
+                                const uint32_t* qzeros, const uint16_t* inv_s16, const uint16_t* bias,
+                                const uint16_t* residual, int32_t act, int32_t gated, int64_t m, int64_t n,
+                                int64_t k, int32_t g, uint16_t* y, void* workspace, size_t ws_bytes, void* stream) {
+  return dense_act("awq_linear_w4a16_act", x, qweight, scales, qzeros, inv_s16, bias, residual, act, gated, m, n, k,
+                   g, y, false, workspace, ws_bytes, stream);
+}
+
+awq_status awq_linear_w4a16_act_bf16(const uint16_t* x, const uint32_t* qweight, const uint16_t* scales,
+                                     const uint32_t* qzeros, const uint16_t* inv_s16, const uint16_t* bias,
+                                     const uint16_t* residual, int32_t act, int32_t gated, int64_t m, int64_t n,
+                                     int64_t k, int32_t g, uint16_t* y, void* workspace, size_t ws_bytes,
+                                     void* stream) {
+  return dense_act("awq_linear_w4a16_act_bf16", x, qweight, scales, qzeros, inv_s16, bias, residual, act, gated, m, n,
+                   k, g, y, true, workspace, ws_bytes, stream);
+}
+
+static awq_status moe_linear(const char* fn, const uint16_t* x, int64_t x_rows, const uint32_t* qweight,
+                             const uint16_t* scales, const uint32_t* qzeros, const uint16_t* inv_s16,
+                             const uint16_t* bias, int32_t act, int32_t gated, int32_t e, const int32_t* offsets,
+                             const int32_t* row_slot, int32_t topk, int64_t rows, int64_t n, int64_t k, int32_t g,
+                             uint16_t* y, bool bf, void* workspace, size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  awq::ActArgs a{};
+  a.x = x; a.qw = qweight; a.sc = scales; a.qz = qzeros; a.inv = inv_s16; a.bias = bias; a.y = y;
+  a.offsets = offsets ? offsets : &kSomeOffsets;
+  a.row_slot = row_slot;
+  a.rows = rows; a.x_rows = row_slot ? x_rows : rows;
+  a.n = n; a.k = k; a.g = g; a.e = e; a.topk = topk;
+  a.act = act; a.gated = gated != 0; a.bf = bf;
+  const awq_status st = act_sizes(fn, a);
+  if (st != AWQ_OK) return st;
+  char msg[128];
+  auto err = [&](awq_status s, const char* what, long long v = 0, long long z = 0) {
+    snprintf(msg, sizeof(msg), "%s: %s", fn, what);
+    return fail(s, msg, v, z);
+  };
+  if (rows > 0 && !offsets) return err(AWQ_ERR_NULL, "null pointer");
+  if (rows > 0 && row_slot && x_rows < 1) return err(AWQ_ERR_SHAPE, "x_rows=%lld < 1", x_rows);
+  if (row_slot && x_rows * k >= (1ll << 31))
+    return err(AWQ_ERR_SHAPE, "x of x_rows=%lld rows of k=%lld, gathered, reaches 4 GiB", x_rows, k);
+  return linear_act_impl(fn, a, workspace, ws_bytes, stream);
+}
+
+awq_status awq_moe_linear_w4a16(const uint16_t* x, int64_t x_rows, const uint32_t* qweight, const uint16_t* scales,
+                                const uint32_t* qzeros, const uint16_t* inv_s16, const uint16_t* bias, int32_t act,
+                                int32_t gated, int32_t e, const int32_t* offsets, const int32_t* row_slot,
+                                int32_t topk, int64_t rows, int64_t n, int64_t k, int32_t g, uint16_t* y,
+                                void* workspace, size_t ws_bytes, void* stream) {
+  return moe_linear("awq_moe_linear_w4a16", x, x_rows, qweight, scales, qzeros, inv_s16, bias, act, gated, e, offsets,
+                    row_slot, topk, rows, n, k, g, y, false, workspace, ws_bytes, stream);
+}
+
+awq_status awq_moe_linear_w4a16_bf16(const uint16_t* x, int64_t x_rows, const uint32_t* qweight,
+                                     const uint16_t* scales, const uint32_t* qzeros, const uint16_t* inv_s16,
+                                     const uint16_t* bias, int32_t act, int32_t gated, int32_t e,
+                                     const int32_t* offsets, const int32_t* row_slot, int32_t topk, int64_t rows,
+                                     int64_t n, int64_t k, int32_t g, uint16_t* y, void* workspace, size_t ws_bytes,
+                                     void* stream) {
+  return moe_linear("awq_moe_linear_w4a16_bf16", x, x_rows, qweight, scales, qzeros, inv_s16, bias, act, gated, e,
+                    offsets, row_slot, topk, rows, n, k, g, y, true, workspace, ws_bytes, stream);
+}
+
 }  // extern "C"

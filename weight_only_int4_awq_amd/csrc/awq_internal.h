@@ -138,4 +138,37 @@ hipError_t launch_attn_kv8(const Kv8Args& a, const uint16_t* q, int64_t q_stride
                            int64_t max_q, float scale, bool bf, uint16_t* out, int64_t out_stride,
                            float* lse, void* scratch, hipStream_t stream);
 
+// Linears with an epilogue and products grouped by expert (linear_act.hip), the routing
+// and the sum of the experts' results (moe_route.hip).
+struct ActArgs {
+  const uint16_t* x;           // [x_rows][k]
+  const uint32_t* qw;          // [e][nw][k / 8], layout v1
+  const uint16_t* sc;
+  const uint32_t* qz;
+  const uint16_t* inv;         // [k] or null
+  const uint16_t* bias;        // [e][nw] or null
+  const uint16_t* res;         // [rows][n] or null
+  uint16_t* y;                 // [rows][n]
+  const int32_t* offsets;      // [e + 1] rows of the experts; null: one matrix, all rows
+  const int32_t* row_slot;     // [rows]: row r reads x[row_slot[r] / topk]; null: x[r]
+  float* part;                 // partial sums of the K slices (set by the launch)
+  int64_t rows, x_rows, n, nw, k;   // nw weight rows: n, or 2 n gated (gate rows first)
+  int32_t e, topk, g, act, gated, bf;
+  // the plan
+  int32_t ng, nzw, ncol, ks, per;
+};
+// Scratch bytes, and whether one launch holds the call's work-groups (rows, x_rows, n, k, e, g,
+// gated, bf, inv and offsets are looked at, the pointers only for being null).
+size_t linear_act_scratch_bytes(const ActArgs& a);
+bool linear_act_fits(const ActArgs& a);
+hipError_t launch_linear_act(const ActArgs& a, void* scratch, hipStream_t stream);
+
+size_t moe_route_scratch_bytes(int64_t t, int32_t e);
+hipError_t launch_moe_route(const void* logits, int32_t type, int64_t t, int32_t e, int32_t topk, int32_t scoring,
+                            bool renorm, float scale, int32_t* ids, float* weights, int32_t* offsets,
+                            int32_t* row_slot, int32_t* slot_row, void* scratch, hipStream_t stream);
+hipError_t launch_moe_combine(const uint16_t* rows, int64_t cap, const float* weights, const int32_t* slot_row,
+                              const uint16_t* residual, int64_t t, int64_t n, int32_t topk, bool bf, uint16_t* y,
+                              hipStream_t stream);
+
 }  // namespace awq

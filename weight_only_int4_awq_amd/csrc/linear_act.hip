@@ -1,0 +1,867 @@
+// The 4-bit linear with an epilogue, alone or grouped by expert:
+//
+//   acc[r][c] = sum_k x~[r][k] (q[c][k] - z[c][k / g]) D[c][k / g]        x~ = fp16(x inv_s) or x
+//   y[r][o]   = act(acc[r][o] + bias[o]) (+ res[r][o])
+//   y[r][o]   = act(acc[r][o] + bias[o]) (acc[r][n + o] + bias[n + o]) (+ res[r][o])    gated
+//
+// Rows of expert i are offsets[i] .. offsets[i + 1] - 1 and use its weights; the row counts
+// are device data, so work-groups find their expert and rows themselves and the grid is an
+// upper bound.  bf16 activations are rounded once to fp16.  Sums, bias, activation and
+// residual are fp32 with one rounding at the end.
+#include "decode_common.h"
+#include "moe_common.h"
+
+namespace awq {
+
+// ---------------------------------------------------------------- which rows a work-group has
+
+struct Place {
+  int expert, row0, rows;      // rows of the tile: row0 .. row0 + rows - 1, at least one
+  int col, sl;                 // column block, slice of K
+  int tile;                    // row tile within the expert
+};
+
+// Rows of expert i, held within the rows there are whatever the array says.
+__device__ __forceinline__ void expert_rows(const ActArgs& a, int i, int& r0, int& n) {
+  const int cap = (int)a.rows;
+  int s = a.offsets[i], t = a.offsets[i + 1];
+  s = s < 0 ? 0 : (s > cap ? cap : s);
+  t = t < s ? s : (t > cap ? cap : t);
+  r0 = s;
+  n = t - s;
+}
+
+// Unit blockIdx.x of the tiles of TM rows x column blocks x K slices: every XCD takes a
+// contiguous run of the order, in which the tiles of an expert follow one another (bands of
+// four row tiles, column by column), so work-groups that share weights or rows share an L2.
+// False: nothing to do.
+template <int TM>
+__device__ __forceinline__ bool find_place(const ActArgs& a, int lane, Place& p) {
+  const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
+  int tiles_all = 0;
+  if (!a.offsets) {
+    tiles_all = (int)((a.rows + TM - 1) / TM);
+  } else {
+    for (int b = 0; b < a.e; b += 64) {
+      int r0, n = 0;
+      if (b + lane < a.e) expert_rows(a, b + lane, r0, n);
+      tiles_all += __builtin_amdgcn_readlane(lanes_scan((n + TM - 1) / TM), 63);
+    }
+  }
+  const int64_t total = (int64_t)tiles_all * a.ncol * a.ks;
+  const int64_t per = (total + 7) / 8;
+  int64_t o = xcd * per + slot;
+  if (slot >= per || o >= total) return false;
+  p.sl = 0;
+  if (a.ks > 1) {
+    p.sl = (int)(o % a.ks);
+    o /= a.ks;
+  }
+  const int t = (int)(o / a.ncol);
+  int tiles, first;
+  p.expert = 0;
+  p.row0 = 0;
+  int rows;
+  if (!a.offsets) {
+    tiles = tiles_all;
+    first = 0;
+    rows = (int)a.rows;
+  } else {
+    int carry = 0;
+    tiles = first = rows = 0;
+    for (int b = 0; b < a.e; b += 64) {
+      int r0 = 0, n = 0;
+      if (b + lane < a.e) expert_rows(a, b + lane, r0, n);
+      const int mine = (n + TM - 1) / TM;
+      const int inc = lanes_scan(mine) + carry;
+      const uint64_t here = __ballot(t < inc);           // the first lane whose sum passes t
+      if (here) {
+        const int l = __builtin_ctzll(here);
+        p.expert = b + l;
+        tiles = __builtin_amdgcn_readlane(mine, l);
+        first = __builtin_amdgcn_readlane(inc, l) - tiles;
+        p.row0 = __builtin_amdgcn_readlane(r0, l);
+        rows = __builtin_amdgcn_readlane(n, l);
+        break;
+      }
+      carry = __builtin_amdgcn_readlane(inc, 63);
+    }
+  }
+  const int local = (int)(o - (int64_t)first * a.ncol);
+  int tm, tn;
+  banded_tile_coords<4>(local, tiles, a.ncol, tm, tn);
+  p.tile = tm;
+  p.col = tn;
+  p.row0 += tm * TM;
+  rows -= tm * TM;
+  p.rows = rows < TM ? rows : TM;
+  return true;
+}
+
+// The row of x that row r reads.
+__device__ __forceinline__ int64_t x_row(const ActArgs& a, int r) {
+  if (!a.row_slot) return r;
+  const int s = a.row_slot[r];
+  const int64_t t = s < 0 ? 0 : s / a.topk;
+  return t < a.x_rows ? t : a.x_rows - 1;
+}
+
+// ---------------------------------------------------------------- epilogue
+
+// erfc(x) = t exp(P(t) - x^2), t = 1 / (1 + |x| / 2), and 2 minus that below zero.  P: a
+// polynomial fitted at Chebyshev nodes to log(exp(x^2) erfc(x) / t) over x in [0, 14.6], off
+// by 7e-8; with the rounding of the exponent 2e-6 relative up to x = 5.  1 + erf(x) would lose
+// the lower tail's digits.
+__device__ __forceinline__ float erfc_tail(float x) {
+  const float z = __builtin_fabsf(x);
+  const float t = __builtin_amdgcn_rcpf(1.0f + 0.5f * z);
+  float q = 0.16738100f;
+  q = __builtin_fmaf(q, t, -0.80132526f);
+  q = __builtin_fmaf(q, t, 1.43554544f);
+  q = __builtin_fmaf(q, t, -1.06009936f);
+  q = __builtin_fmaf(q, t, 0.21378274f);
+  q = __builtin_fmaf(q, t, -0.15077300f);
+  q = __builtin_fmaf(q, t, 0.08468209f);
+  q = __builtin_fmaf(q, t, 0.37655020f);
+  q = __builtin_fmaf(q, t, 0.99975681f);
+  q = __builtin_fmaf(q, t, -1.26550055f);
+  const float e = t * __expf(__builtin_fmaf(-z, z, q));
+  return x < 0.0f ? 2.0f - e : e;
+}
+
+__device__ __forceinline__ float activate(float v, int act) {
+  // v / (1 + exp(-u)), 1 / (1 + exp) by the hardware reciprocal (1 ulp)
+  if (act == 1) return v * __builtin_amdgcn_rcpf(1.0f + __expf(-v));
+  if (act == 2) return 0.5f * v * erfc_tail(v * -0.70710678118654752f);
+  if (act == 3) {                                      // 1 + tanh(u) = 2 / (1 + exp(-2 u))
+    const float u = 1.5957691216057308f * (v + 0.044715f * v * v * v);
+    return v * __builtin_amdgcn_rcpf(1.0f + __expf(-u));
+  }
+  return v;
+}
+
+__device__ __forceinline__ float act_bits(uint16_t b, int bf) { return bf ? bf2f(b) : h2f(b); }
+
+// Output o of a row from its sums (u: the up projection's, where gated), before the residual.
+__device__ __forceinline__ float finish(const ActArgs& a, int expert, int64_t o, float v, float u) {
+  if (a.bias) {
+    const uint16_t* b = a.bias + (int64_t)expert * a.nw;
+    v += act_bits(b[o], a.bf);
+    if (a.gated) u += act_bits(b[a.n + o], a.bf);
+  }
+  v = activate(v, a.act);
+  return a.gated ? v * u : v;
+}
+
+// ---------------------------------------------------------------- few rows: weights streamed
+//
+// TB x 16 rows of one expert times CB blocks of 16 weight rows; the W waves of a work-group
+// share K in runs of whole 128-channel blocks.  A lane reads 16 bytes (32 codes) of one
+// weight row per block, straight into registers: nothing is staged, every byte of the weights
+// is read once and waits for nothing but memory.  v_mfma_f32_16x16x32_f16, rows as A, weights
+// as B.  g = 128: a block is one group, its integers q - z enter exactly and the group's sum is
+// scaled in fp32.  g = 32, 64: a lane's 32 codes are of one group and become
+// fp16((q - z) D) before the product, as in the prefill kernels.
+template <int G, int CB, int TB>
+__global__ __launch_bounds__(512) void linear_act_stream_kernel(const ActArgs a) {
+  extern __shared__ __attribute__((aligned(16))) float red[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int waves = blockDim.x >> 6;
+  Place p;
+  if (!find_place<16 * TB>(a, lane, p)) return;
+  const int r = lane & 15, c = lane >> 4;
+  const int k = (int)a.k;
+  // CB blocks: outputs col0 .. of the gate and the same of the up projection, or CB of outputs
+  const int half = a.gated ? CB / 2 : CB;
+  const int col0 = p.col * half * 16;
+
+  const uint16_t* xr[TB];
+#pragma unroll
+  for (int tb = 0; tb < TB; ++tb) {
+    int row = tb * 16 + r;
+    row = p.row0 + (row < p.rows ? row : p.rows - 1);
+    xr[tb] = a.x + x_row(a, row) * a.k;
+  }
+  const char* qb = reinterpret_cast<const char*>(a.qw + (int64_t)p.expert * a.nw * (a.k / 8));
+  const uint16_t* sb = a.sc + (int64_t)p.expert * a.nw * a.ng;
+  const uint32_t* zb = a.qz + (int64_t)p.expert * a.nw * a.nzw;
+  uint32_t qo[CB], so[CB], zo[CB];
+#pragma unroll
+  for (int cb = 0; cb < CB; ++cb) {
+    const int up = cb >= half;
+    int64_t o = col0 + (up ? cb - half : cb) * 16 + r;
+    o = (o < a.n ? o : a.n - 1) + (up ? a.n : 0);
+    qo[cb] = (uint32_t)(o * (k / 2));
+    so[cb] = (uint32_t)(o * a.ng);
+    zo[cb] = (uint32_t)(o * a.nzw);
+  }
+  const UnpackConsts uc = unpack_consts();
+  const int nb = (k + 127) / 128;
+  const int b0 = wave * a.per, b1 = b0 + a.per < nb ? b0 + a.per : nb;
+
+  floatx4_t acc[CB][TB];
+#pragma unroll
+  for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+    for (int tb = 0; tb < TB; ++tb) acc[cb][tb] = floatx4_t{};
+
+  constexpr int WN = 4;                              // blocks of a window: their loads fly together
+  for (int b = b0; b < b1; b += WN) {
+    uint4 wv[WN][CB];
+    uint32_t sw[WN][CB], zw[WN][CB];
+#pragma unroll
+    for (int i = 0; i < WN; ++i) {
+      const int bb = b + i < b1 ? b + i : b1 - 1;
+      const int kk = bb * 128 + 32 * c;
+      const int ks = kk < k ? kk : k - 32;           // the last block may be half a one (g < 128)
+      const int gr = ks / G;
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb) {
+        wv[i][cb] = *reinterpret_cast<const uint4*>(qb + qo[cb] + (uint32_t)(ks / 2));
+        sw[i][cb] = sb[so[cb] + gr];
+        zw[i][cb] = zb[zo[cb] + (gr >> 3)] >> (4 * (gr & 7));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < WN; ++i) {
+      if (b + i < b1) {
+        const int kk = (b + i) * 128 + 32 * c;
+        const bool in = G == 128 || kk < k;
+        const int ks = in ? kk : k - 32;
+        half8_t af[TB][4];
+#pragma unroll
+        for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            uint4 v = *reinterpret_cast<const uint4*>(xr[tb] + ks + 8 * s);
+            v = act8_h(v, a.bf != 0);
+            if (a.inv) {
+              const uint4 iv = *reinterpret_cast<const uint4*>(a.inv + ks + 8 * s);
+              v = __builtin_bit_cast(uint4, (half8_t)(__builtin_bit_cast(half8_t, v) * __builtin_bit_cast(half8_t, iv)));
+            }
+            if (!in) v = make_uint4(0, 0, 0, 0);
+            // channels in the order of the unpacked nibbles: (0, 4), (1, 5), (2, 6), (3, 7)
+            const uint32_t u0 = __builtin_amdgcn_perm(v.z, v.x, 0x05040100u);
+            const uint32_t u1 = __builtin_amdgcn_perm(v.z, v.x, 0x07060302u);
+            const uint32_t u2 = __builtin_amdgcn_perm(v.w, v.y, 0x05040100u);
+            const uint32_t u3 = __builtin_amdgcn_perm(v.w, v.y, 0x07060302u);
+            af[tb][s] = __builtin_bit_cast(half8_t, make_uint4(u0, u1, u2, u3));
+          }
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+          const uint32_t z = zw[i][cb] & 0xFu;
+          const half2_t o1024 = __builtin_bit_cast(half2_t, (0xE400u + z) * 0x10001u);
+          const half2_t o64 = __builtin_bit_cast(half2_t, (0xD400u + (z << 4)) * 0x10001u);
+          const uint32_t sbits = in ? sw[i][cb] : 0u;
+          const half2_t dd = __builtin_bit_cast(half2_t, sbits * 0x10001u);
+          floatx4_t part[TB];
+#pragma unroll
+          for (int tb = 0; tb < TB; ++tb) part[tb] = G == 128 ? floatx4_t{} : acc[cb][tb];
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            const uint32_t w = s == 0 ? wv[i][cb].x : s == 1 ? wv[i][cb].y : s == 2 ? wv[i][cb].z : wv[i][cb].w;
+            uint32_t u[4];
+            unpack_word(w, u, uc);
+            half2_t q[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              q[j] = __builtin_bit_cast(half2_t, u[j]) + (j & 1 ? o64 : o1024);
+              if (G != 128) q[j] = q[j] * dd;
+            }
+            const half8_t bfr = __builtin_bit_cast(
+                half8_t, make_uint4(__builtin_bit_cast(uint32_t, q[0]), __builtin_bit_cast(uint32_t, q[1]),
+                                    __builtin_bit_cast(uint32_t, q[2]), __builtin_bit_cast(uint32_t, q[3])));
+#pragma unroll
+            for (int tb = 0; tb < TB; ++tb)
+              part[tb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(af[tb][s], bfr, part[tb], 0, 0, 0);
+          }
+          if (G == 128) {
+            const float d = h2f((uint16_t)sbits);
+#pragma unroll
+            for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) acc[cb][tb][j] = __builtin_fmaf(part[tb][j], d, acc[cb][tb][j]);
+          } else {
+#pragma unroll
+            for (int tb = 0; tb < TB; ++tb) acc[cb][tb] = part[tb];
+          }
+        }
+      }
+    }
+  }
+  // ---- the waves' sums, added in wave order: [wave][block][row block][4][lane]
+  constexpr int kWaveFloats = CB * TB * 256;
+#pragma unroll
+  for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+    for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) red[wave * kWaveFloats + ((cb * TB + tb) * 4 + j) * 64 + lane] = acc[cb][tb][j];
+  __syncthreads();
+  const int outs = half * TB * 256;
+  for (int i = tid; i < outs; i += blockDim.x) {
+    float v = 0.0f, u = 0.0f;
+    for (int w = 0; w < waves; ++w) v += red[w * kWaveFloats + i];
+    if (a.gated)
+      for (int w = 0; w < waves; ++w) u += red[w * kWaveFloats + outs + i];
+    const int l = i & 63, j = (i >> 6) & 3, blk = i >> 8;
+    const int cb = blk / TB, tb = blk - cb * TB;
+    const int row = tb * 16 + (l >> 4) * 4 + j;
+    const int64_t o = col0 + cb * 16 + (l & 15);
+    if (row < p.rows && o < a.n) {
+      const int64_t at = (int64_t)(p.row0 + row) * a.n + o;
+      float f = finish(a, p.expert, o, v, u);
+      if (a.res) f += act_bits(a.res[at], a.bf);
+      a.y[at] = f2act(f, a.bf != 0);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- many rows: tiles
+//
+// BM rows x 256 weight rows of one expert, K-step 64, 4 waves side by side along the weight
+// rows, each BM x 64 in 32 x 32 blocks of v_mfma_f32_32x32x16_f16; gated, a wave's two blocks
+// are 32 outputs' gate rows and their up rows, so the product of the two needs no exchange.
+// Copies from global memory to LDS in a ring of three stages, two K-steps ahead, with explicit
+// waits (the compiler sees neither); weights become fp16((q - z) D) in registers.  Rows are
+// read in channel order (gathered by the copies' own addresses), so nibbles are unpacked in
+// pairs of neighbours: a byte permute and a mask per pair.
+constexpr int kTileBN = 256, kTileBK = 64, kTileStages = 3;
+constexpr int tile_stage_bytes(int bm) { return bm * 128 + kTileBN * 32 + 2 * kTileBN * 4; }
+
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// lane i copies 16 (4) bytes from sbase + voff to LDS bytes lds_base + 16 i (4 i)
+__device__ __forceinline__ void lds_copy16(uint32_t voff, const void* sbase, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :
+               : "v"(voff), "s"(sbase), "s"(lds_base)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void lds_copy4(uint32_t voff, const void* sbase, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+               :
+               : "v"(voff), "s"(sbase), "s"(lds_base)
+               : "memory", "m0");
+}
+#pragma clang diagnostic pop
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// a barrier without the fence of __syncthreads, which would wait for every copy in flight
+__device__ __forceinline__ void tile_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Masks and selectors of the unpack in channel order, opaque to constant folding: a VOP3
+// instruction takes no literal and one scalar operand.
+struct PairConsts {
+  uint32_t sel[4], mask, magic;
+};
+__device__ __forceinline__ PairConsts pair_consts() {
+  PairConsts p;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    p.sel[i] = 0x01040004u + 0x00010001u * i;        // bytes: code byte i, 0x64, code byte i, 0x54
+    asm volatile("" : "+s"(p.sel[i]));
+  }
+  p.mask = 0xFFF0FF0Fu;
+  asm volatile("" : "+s"(p.mask));
+  p.magic = 0x00005464u;
+  asm volatile("" : "+v"(p.magic));
+  return p;
+}
+
+template <int G, int KG, int BM>
+__global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_kernel(const ActArgs a) {
+  constexpr int BN = kTileBN, BK = kTileBK;
+  constexpr int BMB = BM / 32, BNB = 2;
+  constexpr int AR = BM / 32;                         // row copies of a wave and step, 8 rows each
+  constexpr int kCopies = AR + 2 + 2;                 // + 2 of packed words, scale and zero words
+  constexpr int kStage = tile_stage_bytes(BM);
+  constexpr int kA = BM * 128, kB = BN * 32;
+  __shared__ __attribute__((aligned(16))) unsigned char ring[kTileStages * KG * kStage];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int kgrp = wave >> 2, wv = wave & 3;
+  Place p;
+  if (!find_place<BM>(a, lane, p)) return;
+  const int k = (int)a.k;
+  const int nk = k / BK;
+  const int kt0 = (int)((int64_t)p.sl * nk / a.ks), kt1 = (int)((int64_t)(p.sl + 1) * nk / a.ks);
+  const int nr = (kt1 - kt0 + KG - 1) / KG;           // round P: K group g takes K-step kt0 + KG P + g
+
+  const uint32_t ring_lds = (uint32_t)(uintptr_t)(&ring[0]) + (uint32_t)(kgrp * kStage);
+  const unsigned char* ring_g = ring + kgrp * kStage;
+  // ---- copy sources: a wave-uniform base and the lane's 32-bit byte offset
+  const int a_lr = lane >> 3, a_p = lane & 7;
+  // rows: their own addresses when gathered (x below 4 GiB), else from the tile's first row
+  const char* xb = reinterpret_cast<const char*>(a.x + (a.row_slot ? 0 : (int64_t)p.row0 * a.k));
+  uint32_t a_voff[AR];
+#pragma unroll
+  for (int i = 0; i < AR; ++i) {
+    const int lrow = wv * (BM / 4) + 8 * i + a_lr;
+    const int row = lrow < p.rows ? lrow : p.rows - 1;
+    const int64_t src = a.row_slot ? x_row(a, p.row0 + row) : row;
+    a_voff[i] = (uint32_t)((src * a.k + (a_p ^ ((lrow >> 1) & 7)) * 8) * 2);
+  }
+  // weight row of the tile's column lcol: gated, 32 gate rows and their 32 up rows per wave
+  const int span = a.gated ? 128 : 256;
+  const int64_t col0 = (int64_t)p.col * span;
+  auto weight_row = [&](int lcol) -> int64_t {
+    if (!a.gated) {
+      const int64_t o = col0 + lcol;
+      return o < a.n ? o : a.n - 1;
+    }
+    const int64_t o = col0 + (lcol >> 6) * 32 + (lcol & 31);
+    return (o < a.n ? o : a.n - 1) + (lcol & 32 ? a.n : 0);
+  };
+  const char* qb = reinterpret_cast<const char*>(a.qw + (int64_t)p.expert * a.nw * (a.k / 8));
+  const char* zb = reinterpret_cast<const char*>(a.qz + (int64_t)p.expert * a.nw * a.nzw);
+  // scales in whole words: an expert may begin, and a row with an odd number of groups
+  // does begin, in the middle of one
+  const int64_t s_first = (int64_t)p.expert * a.nw * a.ng;
+  const char* sb = reinterpret_cast<const char*>(a.sc + (s_first & ~1ll));
+  const uint32_t s_odd = (uint32_t)(s_first & 1);
+  uint32_t b_voff[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int lcol = wv * 64 + 32 * h + (lane >> 1);
+    b_voff[h] = (uint32_t)(weight_row(lcol) * (k / 2) + (((lane & 1) ^ ((lcol >> 2) & 1)) * 16));
+  }
+  const int64_t sz_row = weight_row(wv * 64 + lane);
+  const uint32_t s_idx = (uint32_t)(sz_row * a.ng) + s_odd, z_voff = (uint32_t)(sz_row * a.nzw * 4);
+  auto load = [&](int rnd, int st) {
+    int kt = kt0 + KG * rnd + kgrp;
+    kt = kt < kt1 ? kt : kt1 - 1;
+    const uint32_t base = ring_lds + (uint32_t)(st * KG * kStage);
+    const char* xk = xb + (int64_t)kt * BK * 2;
+#pragma unroll
+    for (int i = 0; i < AR; ++i) lds_copy16(a_voff[i], xk, base + (uint32_t)((wv * (BM / 4) + 8 * i) * 128));
+    const char* qk = qb + (int64_t)kt * 32;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) lds_copy16(b_voff[h], qk, base + (uint32_t)(kA + (wv * 64 + 32 * h) * 32));
+    const int g0 = kt * BK / G;
+    lds_copy4(((s_idx + (uint32_t)g0) >> 1) * 4, sb, base + (uint32_t)(kA + kB + wv * 256));
+    lds_copy4(z_voff, zb + (int64_t)(g0 >> 3) * 4, base + (uint32_t)(kA + kB + BN * 4 + wv * 256));
+  };
+
+  floatx16_t acc[BMB][BNB];
+#pragma unroll
+  for (int i = 0; i < BMB; ++i)
+#pragma unroll
+    for (int j = 0; j < BNB; ++j) acc[i][j] = floatx16_t{};
+  const PairConsts pc = pair_consts();
+  // ---- fragments: rows from chunk (4 (lane / 32) + s) ^ swizzle(row); words of column j, half c
+  const int bj = lane & 31, bc = lane >> 5;
+  uint32_t a_base[BMB];
+#pragma unroll
+  for (int bm = 0; bm < BMB; ++bm) {
+    const int row = bm * 32 + bj;
+    a_base[bm] = (uint32_t)(row * 128 + ((4 * bc) ^ ((row >> 1) & 7)) * 16);
+  }
+  uint32_t b_off[BNB], s_off[BNB], z_off[BNB], s_par[BNB];
+#pragma unroll
+  for (int bn = 0; bn < BNB; ++bn) {
+    const int lcol = wv * 64 + bn * 32 + bj;
+    b_off[bn] = (uint32_t)(kA + lcol * 32 + ((bc ^ ((lcol >> 2) & 1)) * 16));
+    s_off[bn] = (uint32_t)(kA + kB + lcol * 4);
+    z_off[bn] = (uint32_t)(kA + kB + BN * 4 + lcol * 4);
+    s_par[bn] = ((uint32_t)(weight_row(lcol) * a.ng) + s_odd) & 1;
+  }
+  struct BSet {
+    uint4 wb[BNB];
+    half2_t dd[BNB], off[BNB];
+  };
+  // what a wave copied itself needs only its own wait: the step's words, scale and zero
+  auto prep = [&](int rnd, int st, BSet& r) {
+    const unsigned char* s = ring_g + st * KG * kStage;
+    const int grp = ((kt0 + KG * rnd + kgrp) * BK + 32 * bc) / G;
+#pragma unroll
+    for (int bn = 0; bn < BNB; ++bn) {
+      r.wb[bn] = *reinterpret_cast<const uint4*>(s + b_off[bn]);
+      const uint32_t sw = *reinterpret_cast<const uint32_t*>(s + s_off[bn]);
+      const uint32_t zw = *reinterpret_cast<const uint32_t*>(s + z_off[bn]);
+      const uint32_t d = (sw >> (16 * ((s_par[bn] + (uint32_t)grp) & 1))) & 0xFFFFu;
+      const uint32_t z = (zw >> (4 * (grp & 7))) & 0xFu;
+      r.dd[bn] = __builtin_bit_cast(half2_t, d | (d << 16));
+      r.off[bn] = __builtin_bit_cast(half2_t, 0xD400E400u + z + (z << 20));       // (-1024 - z, -64 - z)
+    }
+  };
+  auto dequant = [&](const BSet& r, int s, half8_t (&out)[BNB]) {
+#pragma unroll
+    for (int bn = 0; bn < BNB; ++bn) {
+      const uint32_t w = s == 0 ? r.wb[bn].x : s == 1 ? r.wb[bn].y : s == 2 ? r.wb[bn].z : r.wb[bn].w;
+      uint32_t q[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t u = __builtin_amdgcn_perm(w, pc.magic, pc.sel[j]) & pc.mask;
+        q[j] = __builtin_bit_cast(uint32_t, (half2_t)((__builtin_bit_cast(half2_t, u) + r.off[bn]) * r.dd[bn]));
+      }
+      out[bn] = __builtin_bit_cast(half8_t, make_uint4(q[0], q[1], q[2], q[3]));
+    }
+  };
+  BSet r0, r1;
+  half8_t bq[BNB];
+  // Round P in stage st: meet, then four 16-channel sub-steps.  Each sub-step's products run
+  // while the next one's weights are unpacked; the copies of round P + 2 go out after the
+  // first sub-step, into the stage round P - 1 used; the last sub-step waits for the wave's
+  // own copies of round P + 1 and prepares its weights.
+  auto step = [&](int rnd, int st, int stn, int stp, const BSet& r, BSet& rn) {
+    __builtin_amdgcn_sched_barrier(0);
+    tile_barrier();
+    if (KG == 1 || kt0 + KG * rnd + kgrp < kt1) {
+      const unsigned char* cur = ring_g + st * KG * kStage;
+      half8_t af[BMB];
+#pragma unroll
+      for (int bm = 0; bm < BMB; ++bm) af[bm] = *reinterpret_cast<const half8_t*>(cur + a_base[bm]);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        half8_t bqn[BNB];
+        if (s < 3) {
+          dequant(r, s + 1, bqn);
+        } else {
+          wait_copies<kCopies>();
+          prep(rnd + 1, stp, rn);
+          dequant(rn, 0, bqn);
+        }
+#pragma unroll
+        for (int bm = 0; bm < BMB; ++bm) {
+#pragma unroll
+          for (int bn = 0; bn < BNB; ++bn)
+            acc[bm][bn] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[bm], bq[bn], acc[bm][bn], 0, 0, 0);
+          if (s < 3) af[bm] = *reinterpret_cast<const half8_t*>(cur + (a_base[bm] ^ (uint32_t)(16 * (s + 1))));
+        }
+        if (s == 0) load(rnd + 2, stn);
+#pragma unroll
+        for (int bn = 0; bn < BNB; ++bn) bq[bn] = bqn[bn];
+      }
+    } else {                                          // the second K group's share of an odd last round
+      load(rnd + 2, stn);
+      wait_copies<kCopies>();
+      prep(rnd + 1, stp, rn);
+      dequant(rn, 0, bq);
+    }
+  };
+  load(0, 0);
+  load(1, 1);
+  wait_copies<kCopies>();
+  prep(0, 0, r0);
+  dequant(r0, 0, bq);
+  int rp = 0;
+  for (; rp + 3 <= nr; rp += 3) {
+    step(rp, 0, 2, 1, r0, r1);
+    step(rp + 1, 1, 0, 2, r1, r0);
+    step(rp + 2, 2, 1, 0, r0, r1);
+    r0 = r1;
+  }
+  if (rp < nr) {
+    step(rp, 0, 2, 1, r0, r1);
+    r0 = r1;
+  }
+  if (rp + 1 < nr) step(rp + 1, 1, 0, 2, r0, r1);
+  wait_copies<0>();                                   // the look-ahead has landed before the LDS is used again
+  tile_barrier();
+
+  // ---- two K groups: the second hands its sums over through LDS
+  if constexpr (KG == 2) {
+    float* hand = reinterpret_cast<float*>(ring) + wv * (BMB * BNB * 16 * 64);
+    if (kgrp == 1) {
+#pragma unroll
+      for (int bm = 0; bm < BMB; ++bm)
+#pragma unroll
+        for (int bn = 0; bn < BNB; ++bn)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<float4*>(hand + (((bm * BNB + bn) * 4 + q) * 64 + lane) * 4) =
+                make_float4(acc[bm][bn][4 * q], acc[bm][bn][4 * q + 1], acc[bm][bn][4 * q + 2], acc[bm][bn][4 * q + 3]);
+    }
+    __syncthreads();
+    if (kgrp == 1) return;
+#pragma unroll
+    for (int bm = 0; bm < BMB; ++bm)
+#pragma unroll
+      for (int bn = 0; bn < BNB; ++bn)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float4 v = *reinterpret_cast<const float4*>(hand + (((bm * BNB + bn) * 4 + q) * 64 + lane) * 4);
+          acc[bm][bn][4 * q] += v.x;
+          acc[bm][bn][4 * q + 1] += v.y;
+          acc[bm][bn][4 * q + 2] += v.z;
+          acc[bm][bn][4 * q + 3] += v.w;
+        }
+  }
+
+  // ---- epilogue: value i of lane l in block (bm, bn) is row 8 (i / 4) + 4 (l / 32) + i % 4, column l % 32.
+  // 32 rows at a time through the wave's own LDS: fp32, 8 neighbouring outputs to a lane.
+  const int outs = a.gated ? 32 : 64;                 // outputs of the wave
+  const int64_t wcol = col0 + wv * outs;
+  if (a.ks > 1) {                                     // a slice's sums, [slice][row][pitch]: columns in output order
+    const int64_t np = (a.n + 3) & ~3ll, pitch = a.gated ? 2 * np : np;
+    float* dst = a.part + ((int64_t)p.sl * a.rows + p.row0) * pitch;
+#pragma unroll
+    for (int bm = 0; bm < BMB; ++bm)
+#pragma unroll
+      for (int bn = 0; bn < BNB; ++bn)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int row = bm * 32 + 8 * (i / 4) + 4 * bc + (i % 4);
+          const int64_t o = wcol + (a.gated ? bj : bn * 32 + bj);
+          if (row < p.rows && o < a.n) dst[row * pitch + (a.gated && bn ? np : 0) + o] = acc[bm][bn][i];
+        }
+    return;
+  }
+  constexpr int ER = 68;                              // floats of a staged row: two lane halves 16 banks apart
+  float* ep = reinterpret_cast<float*>(ring) + (KG == 2 ? wv * (BMB * BNB * 16 * 64) : wv * 32 * ER);
+  static_assert(KG == 1 ? 4 * 32 * ER * 4 <= kTileStages * kStage : 32 * ER <= BMB * BNB * 16 * 64, "");
+  auto al = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
+  const bool vec = a.n % 8 == 0 && al(a.y) && al(a.res);
+  const uint16_t* bias = a.bias ? a.bias + (int64_t)p.expert * a.nw : nullptr;
+  const int lsh = a.gated ? 2 : 3;                    // 4 or 8 lanes to a row
+  const int c8 = (lane & ((1 << lsh) - 1)) * 8;
+  const int64_t o = wcol + c8;
+  float bv[8], bu[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int64_t oj = o + j < a.n ? o + j : a.n - 1;
+    bv[j] = bias ? act_bits(bias[oj], a.bf) : 0.0f;
+    bu[j] = bias && a.gated ? act_bits(bias[a.n + oj], a.bf) : 0.0f;
+  }
+#pragma unroll
+  for (int bm = 0; bm < BMB; ++bm) {
+#pragma unroll
+    for (int bn = 0; bn < BNB; ++bn)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) ep[(8 * (i / 4) + 4 * bc + (i % 4)) * ER + bn * 32 + bj] = acc[bm][bn][i];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll 1
+    for (int q = 0; q < 32; q += 64 >> lsh) {
+      const int row = q + (lane >> lsh);
+      if (bm * 32 + row < p.rows && o < a.n) {
+        const float4 lo = *reinterpret_cast<const float4*>(ep + row * ER + c8);
+        const float4 hi = *reinterpret_cast<const float4*>(ep + row * ER + c8 + 4);
+        float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = activate(v[j] + bv[j], a.act);
+        if (a.gated) {
+          const float4 ul = *reinterpret_cast<const float4*>(ep + row * ER + 32 + c8);
+          const float4 uh = *reinterpret_cast<const float4*>(ep + row * ER + 32 + c8 + 4);
+          const float u[8] = {ul.x, ul.y, ul.z, ul.w, uh.x, uh.y, uh.z, uh.w};
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] *= u[j] + bu[j];
+        }
+        const int64_t at = (int64_t)(p.row0 + bm * 32 + row) * a.n + o;
+        if (vec) {
+          if (a.res) {
+            const uint4 rv = *reinterpret_cast<const uint4*>(a.res + at);
+            const uint32_t ru[4] = {rv.x, rv.y, rv.z, rv.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += act_bits((uint16_t)(j & 1 ? ru[j / 2] >> 16 : ru[j / 2]), a.bf);
+          }
+          uint32_t u[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            u[j] = (uint32_t)f2act(v[2 * j], a.bf != 0) | (uint32_t)f2act(v[2 * j + 1], a.bf != 0) << 16;
+          *reinterpret_cast<uint4*>(a.y + at) = make_uint4(u[0], u[1], u[2], u[3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (o + j < a.n) {
+              if (a.res) v[j] += act_bits(a.res[at + j], a.bf);
+              a.y[at + j] = f2act(v[j], a.bf != 0);
+            }
+        }
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+}
+
+// Sums the K slices in slice order and finishes the outputs: a thread takes 4 of a row.
+__global__ __launch_bounds__(256) void linear_act_join_kernel(const ActArgs a) {
+  const int64_t np = (a.n + 3) & ~3ll, pitch = a.gated ? 2 * np : np;
+  const int64_t quads = np / 4;
+  const int64_t unit = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = unit / quads;
+  if (row >= a.rows) return;
+  int expert = 0;
+  if (a.offsets) {
+    int r0, cnt;
+    expert_rows(a, a.e - 1, r0, cnt);
+    if (row >= r0 + cnt) return;
+    if (a.bias) {                                     // the last expert that begins at or before the row
+      int lo = 0, hi = a.e - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (a.offsets[mid] <= row) lo = mid;
+        else hi = mid - 1;
+      }
+      expert = lo;
+    }
+  }
+  const int64_t o = (unit - row * quads) * 4;
+  float v[4] = {0, 0, 0, 0}, u[4] = {0, 0, 0, 0};
+  for (int s = 0; s < a.ks; ++s) {
+    const float* src = a.part + ((int64_t)s * a.rows + row) * pitch + o;
+    const float4 f = *reinterpret_cast<const float4*>(src);
+    v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
+    if (a.gated) {
+      const float4 h = *reinterpret_cast<const float4*>(src + np);
+      u[0] += h.x; u[1] += h.y; u[2] += h.z; u[3] += h.w;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (o + j < a.n) {
+      const int64_t at = row * a.n + o + j;
+      float f = finish(a, expert, o + j, v[j], u[j]);
+      if (a.res) f += act_bits(a.res[at], a.bf);
+      a.y[at] = f2act(f, a.bf != 0);
+    }
+}
+
+// x~ for the tile kernel: fp16(x), times inv_s rounded once, where x is bf16 or inv_s is given.
+__global__ __launch_bounds__(256) void linear_act_prep_kernel(const ActArgs a, uint16_t* __restrict__ out) {
+  const int64_t chunks = a.x_rows * (a.k / 8);
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= chunks) return;
+  uint4 v = reinterpret_cast<const uint4*>(a.x)[i];
+  v = act8_h(v, a.bf != 0);
+  if (a.inv) {
+    const uint4 iv = reinterpret_cast<const uint4*>(a.inv)[i % (a.k / 8)];
+    v = __builtin_bit_cast(uint4, (half8_t)(__builtin_bit_cast(half8_t, v) * __builtin_bit_cast(half8_t, iv)));
+  }
+  reinterpret_cast<uint4*>(out)[i] = v;
+}
+
+// ---------------------------------------------------------------- plan
+
+struct ActPlan {
+  bool stream;
+  int cb, tb, waves, per;      // stream
+  int bm, kg, ks;              // tile
+  bool prep;
+  int64_t ncol, units;         // column blocks; upper bound of the units
+  size_t x_bytes, part_bytes;
+};
+
+static size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+static ActPlan act_plan(const ActArgs& a) {
+  ActPlan p{};
+  const int64_t active = a.offsets ? (a.e < a.rows ? a.e : a.rows) : 1;
+  const int64_t avg = a.offsets ? (a.rows + a.e - 1) / a.e : a.rows;      // rows of a matrix, about
+  auto tiles = [&](int tm) { return a.offsets ? a.rows / tm + active : (a.rows + tm - 1) / tm; };
+  p.ks = 1;
+  p.kg = 1;
+  if (avg <= 32) {
+    p.stream = true;
+    p.tb = avg <= 16 ? 1 : 2;
+    p.cb = 2;
+    const int nb = (int)((a.k + 127) / 128);
+    p.waves = 8;
+    p.per = (nb + 7) / 8;
+    if (p.per > 2) p.per = (p.per + 3) / 4 * 4;
+    p.waves = (nb + p.per - 1) / p.per;
+    const int outs = (a.gated ? p.cb / 2 : p.cb) * 16;
+    p.ncol = (a.n + outs - 1) / outs;
+    p.units = tiles(16 * p.tb) * p.ncol;
+    return p;
+  }
+  p.bm = avg <= 64 ? 64 : 128;
+  const int outs = a.gated ? 128 : 256;
+  p.ncol = (a.n + outs - 1) / outs;
+  const int64_t t = tiles(p.bm) * p.ncol;
+  const int nk = (int)(a.k / 64);
+  if (!a.offsets && t < 256 && a.rows <= 512) {
+    int64_t ks = 256 / t;
+    ks = ks > 16 ? 16 : ks;
+    ks = ks > nk / 2 ? nk / 2 : ks;
+    p.ks = ks < 1 ? 1 : (int)ks;
+  }
+  if (p.ks == 1 && t <= 256) p.kg = 2;
+  p.units = t * p.ks;
+  p.prep = a.bf || a.inv;
+  if (p.prep) p.x_bytes = up256((size_t)a.x_rows * a.k * 2);
+  if (p.ks > 1) {
+    const int64_t np = (a.n + 3) & ~3ll;
+    p.part_bytes = up256((size_t)p.ks * a.rows * (a.gated ? 2 * np : np) * 4);
+  }
+  return p;
+}
+
+size_t linear_act_scratch_bytes(const ActArgs& a) {
+  const ActPlan p = act_plan(a);
+  return p.x_bytes + p.part_bytes;
+}
+
+bool linear_act_fits(const ActArgs& a) {
+  const ActPlan p = act_plan(a);
+  const int64_t threads = p.stream ? 64 * p.waves : 256 * p.kg;
+  return p.units <= (1ll << 31) / threads && a.x_rows * (a.k / 8) <= (1ll << 31) &&
+         a.rows * ((a.n + 3) / 4) <= (1ll << 31);
+}
+
+template <int G, int CB, int TB>
+static hipError_t run_stream(const ActArgs& a, const ActPlan& p, hipStream_t stream) {
+  const size_t lds = (size_t)p.waves * CB * TB * 1024;
+  if (lds > 65536) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(linear_act_stream_kernel<G, CB, TB>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((linear_act_stream_kernel<G, CB, TB>), dim3((unsigned)((p.units + 7) / 8 * 8)), dim3(p.waves * 64),
+                     lds, stream, a);
+  return hipGetLastError();
+}
+
+template <int G, int KG, int BM>
+static hipError_t run_tile(const ActArgs& a, const ActPlan& p, hipStream_t stream) {
+  hipLaunchKernelGGL((linear_act_tile_kernel<G, KG, BM>), dim3((unsigned)((p.units + 7) / 8 * 8)), dim3(256 * KG), 0,
+                     stream, a);
+  return hipGetLastError();
+}
+
+template <int G>
+static hipError_t run_act(const ActArgs& a, const ActPlan& p, hipStream_t stream) {
+  if (p.stream) {
+    if (p.tb == 1) return run_stream<G, 2, 1>(a, p, stream);
+    return run_stream<G, 2, 2>(a, p, stream);
+  }
+  if (p.bm == 64) return p.kg == 2 ? run_tile<G, 2, 64>(a, p, stream) : run_tile<G, 1, 64>(a, p, stream);
+  return p.kg == 2 ? run_tile<G, 2, 128>(a, p, stream) : run_tile<G, 1, 128>(a, p, stream);
+}
+
+hipError_t launch_linear_act(const ActArgs& args, void* scratch, hipStream_t stream) {
+  ActArgs a = args;
+  const ActPlan p = act_plan(a);
+  a.ng = (int32_t)(a.k / a.g);
+  a.nzw = (a.ng + 7) / 8;
+  a.ncol = (int32_t)p.ncol;
+  a.ks = p.ks;
+  a.per = p.per;
+  char* base = (char*)scratch;
+  if (p.prep) {
+    uint16_t* xt = (uint16_t*)base;
+    const int64_t chunks = a.x_rows * (a.k / 8);
+    hipLaunchKernelGGL(linear_act_prep_kernel, dim3((unsigned)((chunks + 255) / 256)), dim3(256), 0, stream, a, xt);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    a.x = xt;
+  }
+  a.part = (float*)(base + p.x_bytes);
+  hipError_t e;
+  if (a.g == 128) e = run_act<128>(a, p, stream);
+  else if (a.g == 64) e = run_act<64>(a, p, stream);
+  else e = run_act<32>(a, p, stream);
+  if (e != hipSuccess || p.ks == 1) return e;
+  const int64_t quads = ((a.n + 3) / 4) * a.rows;
+  hipLaunchKernelGGL(linear_act_join_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace awq
