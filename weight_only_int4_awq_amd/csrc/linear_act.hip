@@ -18,79 +18,104 @@ namespace awq {
 struct Place {
   int expert, row0, rows;      // rows of the tile: row0 .. row0 + rows - 1, at least one
   int col, sl;                 // column block, slice of K
-  int tile;                    // row tile within the expert
 };
 
-// Rows of expert i, held within the rows there are whatever the array says.
+// Rows of expert i (none behind the last), held within the rows there are whatever the array
+// says.  Every lane loads, so that loads of several runs of experts fly together.
 __device__ __forceinline__ void expert_rows(const ActArgs& a, int i, int& r0, int& n) {
   const int cap = (int)a.rows;
-  int s = a.offsets[i], t = a.offsets[i + 1];
+  const int j = i < a.e ? i : a.e - 1;
+  int s = a.offsets[j], t = a.offsets[j + 1];
   s = s < 0 ? 0 : (s > cap ? cap : s);
   t = t < s ? s : (t > cap ? cap : t);
   r0 = s;
-  n = t - s;
+  n = i < a.e ? t - s : 0;
 }
 
 // Unit blockIdx.x of the tiles of TM rows x column blocks x K slices: every XCD takes a
 // contiguous run of the order, in which the tiles of an expert follow one another (bands of
 // four row tiles, column by column), so work-groups that share weights or rows share an L2.
+// Units are below 2^24 (the host checks), so quotients are exact in fp32 and one step.
 // False: nothing to do.
+__device__ __forceinline__ int quot(int x, int y) {
+  int q = (int)((float)x * __builtin_amdgcn_rcpf((float)y));
+  const int rem = x - q * y;
+  q += rem >= y ? 1 : 0;
+  q -= rem < 0 ? 1 : 0;
+  return __builtin_amdgcn_readfirstlane(q);
+}
+
 template <int TM>
 __device__ __forceinline__ bool find_place(const ActArgs& a, int lane, Place& p) {
   const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
+  constexpr int KEEP = 2;                                // experts 0 .. 127 are looked up once
+  int r0[KEEP], n[KEEP], inc[KEEP];
   int tiles_all = 0;
   if (!a.offsets) {
     tiles_all = (int)((a.rows + TM - 1) / TM);
   } else {
-    for (int b = 0; b < a.e; b += 64) {
-      int r0, n = 0;
-      if (b + lane < a.e) expert_rows(a, b + lane, r0, n);
-      tiles_all += __builtin_amdgcn_readlane(lanes_scan((n + TM - 1) / TM), 63);
+#pragma unroll
+    for (int j = 0; j < KEEP; ++j) expert_rows(a, 64 * j + lane, r0[j], n[j]);
+#pragma unroll
+    for (int j = 0; j < KEEP; ++j) {
+      inc[j] = wave_scan((n[j] + TM - 1) / TM) + tiles_all;
+      tiles_all = __builtin_amdgcn_readlane(inc[j], 63);
+    }
+    for (int b = 64 * KEEP; b < a.e; b += 64) {
+      int first, cnt;
+      expert_rows(a, b + lane, first, cnt);
+      tiles_all += __builtin_amdgcn_readlane(wave_scan((cnt + TM - 1) / TM), 63);
     }
   }
-  const int64_t total = (int64_t)tiles_all * a.ncol * a.ks;
-  const int64_t per = (total + 7) / 8;
-  int64_t o = xcd * per + slot;
+  const int total = tiles_all * a.ncol * a.ks;
+  const int per = (total + 7) / 8;
+  int o = xcd * per + slot;
   if (slot >= per || o >= total) return false;
   p.sl = 0;
   if (a.ks > 1) {
-    p.sl = (int)(o % a.ks);
-    o /= a.ks;
+    const int q = quot(o, a.ks);
+    p.sl = o - q * a.ks;
+    o = q;
   }
-  const int t = (int)(o / a.ncol);
-  int tiles, first;
+  int tiles = tiles_all, first = 0, rows = (int)a.rows;
   p.expert = 0;
   p.row0 = 0;
-  int rows;
-  if (!a.offsets) {
-    tiles = tiles_all;
-    first = 0;
-    rows = (int)a.rows;
-  } else {
-    int carry = 0;
-    tiles = first = rows = 0;
-    for (int b = 0; b < a.e; b += 64) {
-      int r0 = 0, n = 0;
-      if (b + lane < a.e) expert_rows(a, b + lane, r0, n);
-      const int mine = (n + TM - 1) / TM;
-      const int inc = lanes_scan(mine) + carry;
-      const uint64_t here = __ballot(t < inc);           // the first lane whose sum passes t
-      if (here) {
+  if (a.offsets) {
+    const int t = quot(o, a.ncol);
+    bool found = false;
+    int last = 0;
+    auto take = [&](int base, int r, int cnt, int sum) {   // the first lane whose sum passes t
+      const uint64_t here = __ballot(t < sum);
+      if (here && !found) {
         const int l = __builtin_ctzll(here);
-        p.expert = b + l;
-        tiles = __builtin_amdgcn_readlane(mine, l);
-        first = __builtin_amdgcn_readlane(inc, l) - tiles;
-        p.row0 = __builtin_amdgcn_readlane(r0, l);
-        rows = __builtin_amdgcn_readlane(n, l);
-        break;
+        found = true;
+        p.expert = base + l;
+        rows = __builtin_amdgcn_readlane(cnt, l);
+        tiles = (rows + TM - 1) / TM;
+        first = __builtin_amdgcn_readlane(sum, l) - tiles;
+        p.row0 = __builtin_amdgcn_readlane(r, l);
       }
-      carry = __builtin_amdgcn_readlane(inc, 63);
+      last = __builtin_amdgcn_readlane(sum, 63);
+    };
+#pragma unroll
+    for (int j = 0; j < KEEP; ++j) take(64 * j, r0[j], n[j], inc[j]);
+    for (int b = 64 * KEEP; !found && b < a.e; b += 64) {
+      int f, cnt;
+      expert_rows(a, b + lane, f, cnt);
+      take(b, f, cnt, wave_scan((cnt + TM - 1) / TM) + last);
     }
   }
-  const int local = (int)(o - (int64_t)first * a.ncol);
+  const int local = o - first * a.ncol;
   int tm, tn;
-  banded_tile_coords<4>(local, tiles, a.ncol, tm, tn);
-  p.tile = tm;
+  if (tiles <= 4) {
+    tn = quot(local, tiles);
+    tm = local - tn * tiles;
+  } else {
+    const int band = quot(local, 4 * a.ncol), left = tiles - 4 * band;
+    const int wide = left < 4 ? left : 4, in = local - band * 4 * a.ncol;
+    tn = quot(in, wide);
+    tm = 4 * band + in - tn * wide;
+  }
   p.col = tn;
   p.row0 += tm * TM;
   rows -= tm * TM;
@@ -99,11 +124,16 @@ __device__ __forceinline__ bool find_place(const ActArgs& a, int lane, Place& p)
 }
 
 // The row of x that row r reads.
-__device__ __forceinline__ int64_t x_row(const ActArgs& a, int r) {
+__device__ __forceinline__ int x_row(const ActArgs& a, int r) {
   if (!a.row_slot) return r;
-  const int s = a.row_slot[r];
-  const int64_t t = s < 0 ? 0 : s / a.topk;
-  return t < a.x_rows ? t : a.x_rows - 1;
+  const uint32_t s = (uint32_t)(a.row_slot[r] < 0 ? 0 : a.row_slot[r]);
+  // the quotient in fp32: off by one below 2^24, which is mended; a slot beyond the rows of x
+  // is no slot, and whatever it gives is held within them
+  int t = (int)((float)s * __builtin_amdgcn_rcpf((float)a.topk));
+  const int rem = (int)(s - (uint32_t)t * (uint32_t)a.topk);
+  t += rem < 0 ? -1 : rem >= a.topk ? 1 : 0;
+  t = t < 0 ? 0 : t;
+  return t < (int)a.x_rows ? t : (int)a.x_rows - 1;
 }
 
 // ---------------------------------------------------------------- epilogue
@@ -155,166 +185,216 @@ __device__ __forceinline__ float finish(const ActArgs& a, int expert, int64_t o,
 
 // ---------------------------------------------------------------- few rows: weights streamed
 //
-// TB x 16 rows of one expert times CB blocks of 16 weight rows; the W waves of a work-group
-// share K in runs of whole 128-channel blocks.  A lane reads 16 bytes (32 codes) of one
-// weight row per block, straight into registers: nothing is staged, every byte of the weights
-// is read once and waits for nothing but memory.  v_mfma_f32_16x16x32_f16, rows as A, weights
-// as B.  g = 128: a block is one group, its integers q - z enter exactly and the group's sum is
-// scaled in fp32.  g = 32, 64: a lane's 32 codes are of one group and become
-// fp16((q - z) D) before the product, as in the prefill kernels.
-template <int G, int CB, int TB>
-__global__ __launch_bounds__(512) void linear_act_stream_kernel(const ActArgs a) {
-  extern __shared__ __attribute__((aligned(16))) float red[];
+// Up to TM rows of one expert times CB blocks of 16 weight rows; the W waves of a work-group
+// share K in runs of four 128-channel blocks.  A lane reads 16 bytes (32 codes) of one weight
+// row per block, straight into registers: every byte of the weights is read once and waits
+// for nothing but memory, all of a run asked for before the first is used.  The rows of a run
+// (512 channels; 256 where TM = 16) go through the wave's own LDS: scaled, rounded to fp16 and
+// put in the order of the unpacked nibbles once, then read as operands.
+// v_mfma_f32_16x16x32_f16, rows as A, weights as B.  g = 128: a block is one group, its
+// integers q - z enter exactly and the group's sum is scaled in fp32.  g = 32, 64: a lane's 32
+// codes are of one group and become fp16((q - z) D) before the product, as in the tiles.
+constexpr int kRun = 4;                              // blocks of a run
+template <int TM>
+struct StreamLds {
+  static constexpr int SB = TM == 16 ? 2 : 4;        // blocks staged at a time
+  static constexpr int STRIDE = SB * 256 + 16;       // bytes of a staged row: 16 rows on 64 banks
+  static constexpr int WAVE = TM * STRIDE;
+};
+
+// Scales and zero points of a lane's codes in the blocks of a run, as they are loaded.
+// QUADS (g = 128, rows of a multiple of four groups): a run's scales are 8 aligned bytes.
+template <int G, int CB, bool QUADS>
+struct RunScales {
+  uint32_t s[CB][QUADS ? 2 : kRun];                  // fp16 bits, two to a word or one
+  uint32_t z[CB][G == 32 ? 2 : 1];                   // words of zero points
+};
+
+template <int G, int CB, int TM, bool QUADS>
+__global__ __launch_bounds__(512, 2) void linear_act_stream_kernel(const ActArgs a) {
+  static_assert((TM == 8 || TM == 16) && (G == 128 || !QUADS), "");
+  constexpr int SB = StreamLds<TM>::SB, STRIDE = StreamLds<TM>::STRIDE;
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int waves = blockDim.x >> 6;
   Place p;
-  if (!find_place<16 * TB>(a, lane, p)) return;
+  if (!find_place<TM>(a, lane, p)) return;
   const int r = lane & 15, c = lane >> 4;
   const int k = (int)a.k;
   // CB blocks: outputs col0 .. of the gate and the same of the up projection, or CB of outputs
   const int half = a.gated ? CB / 2 : CB;
   const int col0 = p.col * half * 16;
-
-  const uint16_t* xr[TB];
-#pragma unroll
-  for (int tb = 0; tb < TB; ++tb) {
-    int row = tb * 16 + r;
-    row = p.row0 + (row < p.rows ? row : p.rows - 1);
-    xr[tb] = a.x + x_row(a, row) * a.k;
-  }
+  // lane i: the row of x that row i of the tile reads; asked for first, the rows wait for it
+  const int src = x_row(a, p.row0 + (r < p.rows ? r : p.rows - 1));
   const char* qb = reinterpret_cast<const char*>(a.qw + (int64_t)p.expert * a.nw * (a.k / 8));
-  const uint16_t* sb = a.sc + (int64_t)p.expert * a.nw * a.ng;
-  const uint32_t* zb = a.qz + (int64_t)p.expert * a.nw * a.nzw;
-  uint32_t qo[CB], so[CB], zo[CB];
+  const char* sb = reinterpret_cast<const char*>(a.sc + (int64_t)p.expert * a.nw * a.ng);
+  const char* zb = reinterpret_cast<const char*>(a.qz + (int64_t)p.expert * a.nw * a.nzw);
+  uint32_t row_w[CB];
 #pragma unroll
   for (int cb = 0; cb < CB; ++cb) {
     const int up = cb >= half;
-    int64_t o = col0 + (up ? cb - half : cb) * 16 + r;
-    o = (o < a.n ? o : a.n - 1) + (up ? a.n : 0);
-    qo[cb] = (uint32_t)(o * (k / 2));
-    so[cb] = (uint32_t)(o * a.ng);
-    zo[cb] = (uint32_t)(o * a.nzw);
+    const uint32_t o = (uint32_t)(col0 + (up ? cb - half : cb) * 16 + r), n = (uint32_t)a.n;
+    row_w[cb] = (o < n ? o : n - 1) + (up ? n : 0);
   }
   const UnpackConsts uc = unpack_consts();
   const int nb = (k + 127) / 128;
   const int b0 = wave * a.per, b1 = b0 + a.per < nb ? b0 + a.per : nb;
 
-  floatx4_t acc[CB][TB];
+  // the lane's 32 channels of block b: its first one, held within the row
+  auto channel = [&](int b) {
+    const int kk = b * 128 + 32 * c;
+    return kk < k ? kk : k - 32;
+  };
+  auto load_w = [&](int b, uint4 (&w)[kRun][CB], RunScales<G, CB, QUADS>& rs) {
 #pragma unroll
-  for (int cb = 0; cb < CB; ++cb)
+    for (int cb = 0; cb < CB; ++cb) {                  // first: what returns in order is waited for in order
+      const uint32_t so = row_w[cb] * (uint32_t)(a.ng * 2), zo = row_w[cb] * (uint32_t)(a.nzw * 4);
+      if constexpr (QUADS) {
+        const uint2 v = *reinterpret_cast<const uint2*>(sb + (so + (uint32_t)b * 2));
+        rs.s[cb][0] = v.x;
+        rs.s[cb][1] = v.y;
+      } else {
 #pragma unroll
-    for (int tb = 0; tb < TB; ++tb) acc[cb][tb] = floatx4_t{};
+        for (int i = 0; i < kRun; ++i)
+          rs.s[cb][i] = *reinterpret_cast<const uint16_t*>(
+              sb + (so + (uint32_t)(channel(b + i < b1 ? b + i : b1 - 1) / G) * 2));
+      }
+      // 8 zero points to a word: a run of four groups, eight or sixteen
+      constexpr int ZW = G == 32 ? 2 : 1;
+#pragma unroll
+      for (int j = 0; j < ZW; ++j) {
+        int w4 = b * (128 / G) / 8 + j;
+        w4 = w4 < a.nzw ? w4 : a.nzw - 1;
+        rs.z[cb][j] = *reinterpret_cast<const uint32_t*>(zb + (zo + (uint32_t)w4 * 4));
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      const uint32_t off = (uint32_t)channel(b + i < b1 ? b + i : b1 - 1) / 2;
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb)
+        w[i][cb] = *reinterpret_cast<const uint4*>(qb + (row_w[cb] * (uint32_t)(k / 2) + off));
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // ---- the rows' channels of SB blocks: 16 bytes to a lane, 64 or 32 lanes to a row
+  constexpr int XL = 8;                              // loads of a lane, all in flight
+  unsigned char* stage = lds + wave * StreamLds<TM>::WAVE;
+  const int xc = SB == 4 ? lane : lane & 31, xh = SB == 4 ? 0 : lane >> 5;
+  auto load_x = [&](int b, uint4 (&x)[XL], uint4& iv) {
+    const int ch = b * 128 + 8 * xc;
+    const int cc = ch < k ? ch : k - 8;
+#pragma unroll
+    for (int i = 0; i < XL; ++i) {
+      if (SB == 4) {
+        if (i < p.rows)
+          x[i] = *reinterpret_cast<const uint4*>(a.x + (int64_t)__builtin_amdgcn_readlane(src, i) * a.k + cc);
+      } else if (2 * i < p.rows) {
+        const int s0 = __builtin_amdgcn_readlane(src, 2 * i), s1 = __builtin_amdgcn_readlane(src, 2 * i + 1);
+        x[i] = *reinterpret_cast<const uint4*>(a.x + (int64_t)(xh ? s1 : s0) * a.k + cc);
+      }
+    }
+    if (a.inv) iv = *reinterpret_cast<const uint4*>(a.inv + cc);
+  };
+  auto store_x = [&](int b, const uint4 (&x)[XL], const uint4& iv) {
+    const bool in = b * 128 + 8 * xc < k;            // the last block may be half a one (g < 128)
+#pragma unroll
+    for (int i = 0; i < XL; ++i)
+      if ((SB == 4 ? i : 2 * i) < p.rows) {
+        uint4 v = act8_h(x[i], a.bf != 0);
+        if (a.inv) v = __builtin_bit_cast(uint4, (half8_t)(__builtin_bit_cast(half8_t, v) * __builtin_bit_cast(half8_t, iv)));
+        // channels in the order of the unpacked nibbles: (0, 4), (1, 5), (2, 6), (3, 7)
+        uint4 u = make_uint4(__builtin_amdgcn_perm(v.z, v.x, 0x05040100u), __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
+                             __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u));
+        if (!in) u = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(stage + (SB == 4 ? i : 2 * i + xh) * STRIDE + xc * 16) = u;
+      }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  };
 
-  constexpr int WN = 4;                              // blocks of a window: their loads fly together
-  for (int b = b0; b < b1; b += WN) {
-    uint4 wv[WN][CB];
-    uint32_t sw[WN][CB], zw[WN][CB];
+  floatx4_t acc[CB];
 #pragma unroll
-    for (int i = 0; i < WN; ++i) {
-      const int bb = b + i < b1 ? b + i : b1 - 1;
-      const int kk = bb * 128 + 32 * c;
-      const int ks = kk < k ? kk : k - 32;           // the last block may be half a one (g < 128)
-      const int gr = ks / G;
+  for (int cb = 0; cb < CB; ++cb) acc[cb] = floatx4_t{};
+  const unsigned char* frag = stage + (TM == 16 ? r : r & 7) * STRIDE + c * 64;
+  auto block = [&](int b, int i, const uint4 (&w)[CB], const RunScales<G, CB, QUADS>& rs) {
+    half8_t af[4];
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb) {
-        wv[i][cb] = *reinterpret_cast<const uint4*>(qb + qo[cb] + (uint32_t)(ks / 2));
-        sw[i][cb] = sb[so[cb] + gr];
-        zw[i][cb] = zb[zo[cb] + (gr >> 3)] >> (4 * (gr & 7));
-      }
-    }
+    for (int s = 0; s < 4; ++s) af[s] = *reinterpret_cast<const half8_t*>(frag + (i % SB) * 256 + s * 16);
+    const bool in = G == 128 || b * 128 + 32 * c < k;
 #pragma unroll
-    for (int i = 0; i < WN; ++i) {
-      if (b + i < b1) {
-        const int kk = (b + i) * 128 + 32 * c;
-        const bool in = G == 128 || kk < k;
-        const int ks = in ? kk : k - 32;
-        half8_t af[TB][4];
+    for (int cb = 0; cb < CB; ++cb) {
+      // fields of the zero word: the block's group within the eight of a word
+      const int gr = G == 128 ? b & 7 : G == 64 ? (2 * i + (c >> 1)) : (4 * (i & 1) + c);
+      const uint32_t z = (rs.z[cb][G == 32 ? i >> 1 : 0] >> (4 * gr)) & 0xFu;
+      uint32_t d = QUADS ? (rs.s[cb][i >> 1] >> (16 * (i & 1))) & 0xFFFFu : rs.s[cb][QUADS ? 0 : i];
+      if (!in) d = 0;
+      const half2_t o1024 = __builtin_bit_cast(half2_t, (0xE400u + z) * 0x10001u);
+      const half2_t o64 = __builtin_bit_cast(half2_t, (0xD400u + (z << 4)) * 0x10001u);
+      const half2_t dd = __builtin_bit_cast(half2_t, d * 0x10001u);
+      floatx4_t part = G == 128 ? floatx4_t{} : acc[cb];
 #pragma unroll
-        for (int tb = 0; tb < TB; ++tb)
+      for (int s = 0; s < 4; ++s) {
+        const uint32_t word = s == 0 ? w[cb].x : s == 1 ? w[cb].y : s == 2 ? w[cb].z : w[cb].w;
+        uint32_t u[4];
+        unpack_word(word, u, uc);
 #pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            uint4 v = *reinterpret_cast<const uint4*>(xr[tb] + ks + 8 * s);
-            v = act8_h(v, a.bf != 0);
-            if (a.inv) {
-              const uint4 iv = *reinterpret_cast<const uint4*>(a.inv + ks + 8 * s);
-              v = __builtin_bit_cast(uint4, (half8_t)(__builtin_bit_cast(half8_t, v) * __builtin_bit_cast(half8_t, iv)));
-            }
-            if (!in) v = make_uint4(0, 0, 0, 0);
-            // channels in the order of the unpacked nibbles: (0, 4), (1, 5), (2, 6), (3, 7)
-            const uint32_t u0 = __builtin_amdgcn_perm(v.z, v.x, 0x05040100u);
-            const uint32_t u1 = __builtin_amdgcn_perm(v.z, v.x, 0x07060302u);
-            const uint32_t u2 = __builtin_amdgcn_perm(v.w, v.y, 0x05040100u);
-            const uint32_t u3 = __builtin_amdgcn_perm(v.w, v.y, 0x07060302u);
-            af[tb][s] = __builtin_bit_cast(half8_t, make_uint4(u0, u1, u2, u3));
-          }
-#pragma unroll
-        for (int cb = 0; cb < CB; ++cb) {
-          const uint32_t z = zw[i][cb] & 0xFu;
-          const half2_t o1024 = __builtin_bit_cast(half2_t, (0xE400u + z) * 0x10001u);
-          const half2_t o64 = __builtin_bit_cast(half2_t, (0xD400u + (z << 4)) * 0x10001u);
-          const uint32_t sbits = in ? sw[i][cb] : 0u;
-          const half2_t dd = __builtin_bit_cast(half2_t, sbits * 0x10001u);
-          floatx4_t part[TB];
-#pragma unroll
-          for (int tb = 0; tb < TB; ++tb) part[tb] = G == 128 ? floatx4_t{} : acc[cb][tb];
-#pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            const uint32_t w = s == 0 ? wv[i][cb].x : s == 1 ? wv[i][cb].y : s == 2 ? wv[i][cb].z : wv[i][cb].w;
-            uint32_t u[4];
-            unpack_word(w, u, uc);
-            half2_t q[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              q[j] = __builtin_bit_cast(half2_t, u[j]) + (j & 1 ? o64 : o1024);
-              if (G != 128) q[j] = q[j] * dd;
-            }
-            const half8_t bfr = __builtin_bit_cast(
-                half8_t, make_uint4(__builtin_bit_cast(uint32_t, q[0]), __builtin_bit_cast(uint32_t, q[1]),
-                                    __builtin_bit_cast(uint32_t, q[2]), __builtin_bit_cast(uint32_t, q[3])));
-#pragma unroll
-            for (int tb = 0; tb < TB; ++tb)
-              part[tb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(af[tb][s], bfr, part[tb], 0, 0, 0);
-          }
-          if (G == 128) {
-            const float d = h2f((uint16_t)sbits);
-#pragma unroll
-            for (int tb = 0; tb < TB; ++tb)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) acc[cb][tb][j] = __builtin_fmaf(part[tb][j], d, acc[cb][tb][j]);
-          } else {
-#pragma unroll
-            for (int tb = 0; tb < TB; ++tb) acc[cb][tb] = part[tb];
-          }
+        for (int j = 0; j < 4; ++j) {
+          half2_t q = __builtin_bit_cast(half2_t, u[j]) + (j & 1 ? o64 : o1024);
+          if (G != 128) q = q * dd;
+          u[j] = __builtin_bit_cast(uint32_t, q);
         }
+        part = __builtin_amdgcn_mfma_f32_16x16x32_f16(af[s], __builtin_bit_cast(half8_t, make_uint4(u[0], u[1], u[2], u[3])),
+                                                      part, 0, 0, 0);
+      }
+      if (G == 128) {
+        const float df = h2f((uint16_t)d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[cb][j] = __builtin_fmaf(part[j], df, acc[cb][j]);
+      } else {
+        acc[cb] = part;
       }
     }
+  };
+
+  for (int b = b0; b < b1; b += kRun) {
+    uint4 w[kRun][CB], x[XL], iv = make_uint4(0, 0, 0, 0);
+    RunScales<G, CB, QUADS> rs;
+    load_x(b, x, iv);
+    load_w(b, w, rs);
+    store_x(b, x, iv);
+    if (SB == 2 && b + 2 < b1) load_x(b + 2, x, iv);
+    block(b, 0, w[0], rs);
+    if (b + 1 < b1) block(b + 1, 1, w[1], rs);
+    if (SB == 2 && b + 2 < b1) store_x(b + 2, x, iv);
+    if (b + 2 < b1) block(b + 2, 2, w[2], rs);
+    if (b + 3 < b1) block(b + 3, 3, w[3], rs);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
-  // ---- the waves' sums, added in wave order: [wave][block][row block][4][lane]
-  constexpr int kWaveFloats = CB * TB * 256;
+  // ---- the waves' sums, added in wave order: [wave][block][4][lane]
+  __syncthreads();
+  float* red = reinterpret_cast<float*>(lds);
 #pragma unroll
   for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
-    for (int tb = 0; tb < TB; ++tb)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) red[wave * kWaveFloats + ((cb * TB + tb) * 4 + j) * 64 + lane] = acc[cb][tb][j];
+    for (int j = 0; j < 4; ++j) red[(wave * CB + cb) * 256 + j * 64 + lane] = acc[cb][j];
   __syncthreads();
-  const int outs = half * TB * 256;
+  const int outs = half * 256;
   for (int i = tid; i < outs; i += blockDim.x) {
-    float v = 0.0f, u = 0.0f;
-    for (int w = 0; w < waves; ++w) v += red[w * kWaveFloats + i];
-    if (a.gated)
-      for (int w = 0; w < waves; ++w) u += red[w * kWaveFloats + outs + i];
-    const int l = i & 63, j = (i >> 6) & 3, blk = i >> 8;
-    const int cb = blk / TB, tb = blk - cb * TB;
-    const int row = tb * 16 + (l >> 4) * 4 + j;
+    const int l = i & 63, j = (i >> 6) & 3, cb = i >> 8;
+    const int row = (l >> 4) * 4 + j;
     const int64_t o = col0 + cb * 16 + (l & 15);
-    if (row < p.rows && o < a.n) {
-      const int64_t at = (int64_t)(p.row0 + row) * a.n + o;
-      float f = finish(a, p.expert, o, v, u);
-      if (a.res) f += act_bits(a.res[at], a.bf);
-      a.y[at] = f2act(f, a.bf != 0);
+    if (row >= p.rows || o >= a.n) continue;
+    float v = 0.0f, u = 0.0f;
+    for (int w = 0; w < waves; ++w) {
+      v += red[w * CB * 256 + i];
+      if (a.gated) u += red[w * CB * 256 + outs + i];
     }
+    const int64_t at = (int64_t)(p.row0 + row) * a.n + o;
+    float f = finish(a, p.expert, o, v, u);
+    if (a.res) f += act_bits(a.res[at], a.bf);
+    a.y[at] = f2act(f, a.bf != 0);
   }
 }
 
@@ -406,8 +486,8 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
   for (int i = 0; i < AR; ++i) {
     const int lrow = wv * (BM / 4) + 8 * i + a_lr;
     const int row = lrow < p.rows ? lrow : p.rows - 1;
-    const int64_t src = a.row_slot ? x_row(a, p.row0 + row) : row;
-    a_voff[i] = (uint32_t)((src * a.k + (a_p ^ ((lrow >> 1) & 7)) * 8) * 2);
+    const int src = a.row_slot ? x_row(a, p.row0 + row) : row;
+    a_voff[i] = (uint32_t)(((int64_t)src * a.k + (a_p ^ ((lrow >> 1) & 7)) * 8) * 2);
   }
   // weight row of the tile's column lcol: gated, 32 gate rows and their 32 up rows per wave
   const int span = a.gated ? 128 : 256;
@@ -616,8 +696,11 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
     return;
   }
   constexpr int ER = 68;                              // floats of a staged row: two lane halves 16 banks apart
-  float* ep = reinterpret_cast<float*>(ring) + (KG == 2 ? wv * (BMB * BNB * 16 * 64) : wv * 32 * ER);
-  static_assert(KG == 1 ? 4 * 32 * ER * 4 <= kTileStages * kStage : 32 * ER <= BMB * BNB * 16 * 64, "");
+  // (two K groups: behind the hand-over area, which other waves may still read)
+  constexpr int kHand = KG == 2 ? 4 * BMB * BNB * 16 * 64 : 0;
+  constexpr bool kBehind = (kHand + 4 * 32 * ER) * 4 <= kTileStages * KG * kStage;
+  static_assert(kBehind || 32 * ER <= BMB * BNB * 16 * 64, "else within the wave's own part of it");
+  float* ep = reinterpret_cast<float*>(ring) + (kBehind ? kHand + wv * 32 * ER : wv * (BMB * BNB * 16 * 64));
   auto al = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
   const bool vec = a.n % 8 == 0 && al(a.y) && al(a.res);
   const uint16_t* bias = a.bias ? a.bias + (int64_t)p.expert * a.nw : nullptr;
@@ -742,7 +825,7 @@ __global__ __launch_bounds__(256) void linear_act_prep_kernel(const ActArgs a, u
 
 struct ActPlan {
   bool stream;
-  int cb, tb, waves, per;      // stream
+  int cb, tm, waves, per;      // stream
   int bm, kg, ks;              // tile
   bool prep;
   int64_t ncol, units;         // column blocks; upper bound of the units
@@ -758,21 +841,19 @@ static ActPlan act_plan(const ActArgs& a) {
   auto tiles = [&](int tm) { return a.offsets ? a.rows / tm + active : (a.rows + tm - 1) / tm; };
   p.ks = 1;
   p.kg = 1;
-  if (avg <= 32) {
+  if (avg <= 16) {
     p.stream = true;
-    p.tb = avg <= 16 ? 1 : 2;
+    p.tm = avg <= 8 ? 8 : 16;
     p.cb = 2;
-    const int nb = (int)((a.k + 127) / 128);
-    p.waves = 8;
-    p.per = (nb + 7) / 8;
-    if (p.per > 2) p.per = (p.per + 3) / 4 * 4;
+    const int nb = (int)((a.k + 127) / 128), runs = (nb + kRun - 1) / kRun;
+    p.per = (runs + 3) / 4 * kRun;                   // whole runs, up to 4 waves
     p.waves = (nb + p.per - 1) / p.per;
     const int outs = (a.gated ? p.cb / 2 : p.cb) * 16;
     p.ncol = (a.n + outs - 1) / outs;
-    p.units = tiles(16 * p.tb) * p.ncol;
+    p.units = tiles(p.tm) * p.ncol;
     return p;
   }
-  p.bm = avg <= 64 ? 64 : 128;
+  p.bm = avg <= 32 ? 32 : avg <= 64 ? 64 : 128;
   const int outs = a.gated ? 128 : 256;
   p.ncol = (a.n + outs - 1) / outs;
   const int64_t t = tiles(p.bm) * p.ncol;
@@ -802,21 +883,27 @@ size_t linear_act_scratch_bytes(const ActArgs& a) {
 bool linear_act_fits(const ActArgs& a) {
   const ActPlan p = act_plan(a);
   const int64_t threads = p.stream ? 64 * p.waves : 256 * p.kg;
-  return p.units <= (1ll << 31) / threads && a.x_rows * (a.k / 8) <= (1ll << 31) &&
+  return p.units <= (1ll << 31) / threads && p.units < (1 << 24) && a.x_rows * (a.k / 8) <= (1ll << 31) &&
          a.rows * ((a.n + 3) / 4) <= (1ll << 31);
 }
 
-template <int G, int CB, int TB>
+template <int G, int CB, int TM>
 static hipError_t run_stream(const ActArgs& a, const ActPlan& p, hipStream_t stream) {
-  const size_t lds = (size_t)p.waves * CB * TB * 1024;
-  if (lds > 65536) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(linear_act_stream_kernel<G, CB, TB>),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if (e != hipSuccess) return e;
+  const size_t x = (size_t)p.waves * StreamLds<TM>::WAVE, red = (size_t)p.waves * CB * 1024;
+  const size_t lds = x > red ? x : red;
+  auto go = [&](auto kernel) {
+    if (lds > 65536) {
+      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+      if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((p.units + 7) / 8 * 8)), dim3(p.waves * 64), lds, stream, a);
+    return hipGetLastError();
+  };
+  if constexpr (G == 128) {
+    if (a.ng % 4 == 0) return go(linear_act_stream_kernel<G, CB, TM, true>);
   }
-  hipLaunchKernelGGL((linear_act_stream_kernel<G, CB, TB>), dim3((unsigned)((p.units + 7) / 8 * 8)), dim3(p.waves * 64),
-                     lds, stream, a);
-  return hipGetLastError();
+  return go(linear_act_stream_kernel<G, CB, TM, false>);
 }
 
 template <int G, int KG, int BM>
@@ -829,9 +916,9 @@ static hipError_t run_tile(const ActArgs& a, const ActPlan& p, hipStream_t strea
 template <int G>
 static hipError_t run_act(const ActArgs& a, const ActPlan& p, hipStream_t stream) {
   if (p.stream) {
-    if (p.tb == 1) return run_stream<G, 2, 1>(a, p, stream);
-    return run_stream<G, 2, 2>(a, p, stream);
+    return p.tm == 8 ? run_stream<G, 2, 8>(a, p, stream) : run_stream<G, 2, 16>(a, p, stream);
   }
+  if (p.bm == 32) return p.kg == 2 ? run_tile<G, 2, 32>(a, p, stream) : run_tile<G, 1, 32>(a, p, stream);
   if (p.bm == 64) return p.kg == 2 ? run_tile<G, 2, 64>(a, p, stream) : run_tile<G, 1, 64>(a, p, stream);
   return p.kg == 2 ? run_tile<G, 2, 128>(a, p, stream) : run_tile<G, 1, 128>(a, p, stream);
 }

@@ -174,7 +174,7 @@ __device__ __forceinline__ void scan_experts(const int* tot, int* start, int e, 
   int carry = 0;
   for (int b = 0; b < e; b += 64) {
     const int x = b + lane < e ? tot[b + lane] : 0;
-    const int inc = lanes_scan(x);
+    const int inc = wave_scan(x);
     if (b + lane < e) start[b + lane] = carry + inc - x;
     carry += __builtin_amdgcn_readlane(inc, 63);
   }
