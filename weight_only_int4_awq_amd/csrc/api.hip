@@ -810,8 +810,8 @@ static awq_status act_sizes(const char* fn, awq::ActArgs& a) {
     return fail(s, msg, x, z);
   };
   if (!group_ok(a.g)) return err(AWQ_ERR_SHAPE, "g=%lld not in {32,64,128}", a.g);
-  if (a.k < 64 || a.k > 0x7FFFFFFF || a.k % a.g || a.k % 64)
-    return err(AWQ_ERR_SHAPE, "k=%lld not a positive multiple of 64 and g=%lld", a.k, a.g);
+  if (a.k < 64 || a.k > (1 << 23) || a.k % a.g || a.k % 64)
+    return err(AWQ_ERR_SHAPE, "k=%lld not a multiple of 64 and g=%lld up to 2^23", a.k, a.g);
   if (a.n < 1 || a.n > 0x7FFFFFFF) return err(AWQ_ERR_SHAPE, "n=%lld out of range", a.n);
   a.nw = a.gated ? 2 * a.n : a.n;
   if (a.nw * (a.k / 2) >= (1ll << 32)) return err(AWQ_ERR_SHAPE, "packed weights of n=%lld, k=%lld reach 4 GiB", a.n, a.k);

@@ -32,103 +32,118 @@ __device__ __forceinline__ void expert_rows(const ActArgs& a, int i, int& r0, in
   n = i < a.e ? t - s : 0;
 }
 
-// Unit blockIdx.x of the tiles of TM rows x column blocks x K slices: every XCD takes a
-// contiguous run of the order, in which the tiles of an expert follow one another (bands of
-// four row tiles, column by column), so work-groups that share weights or rows share an L2.
-// Units are below 2^24 (the host checks), so quotients are exact in fp32 and one step.
-// False: nothing to do.
+// x / y for 0 <= x < 2^24, 0 < y: exact in fp32 and one step.
 __device__ __forceinline__ int quot(int x, int y) {
   int q = (int)((float)x * __builtin_amdgcn_rcpf((float)y));
   const int rem = x - q * y;
   q += rem >= y ? 1 : 0;
   q -= rem < 0 ? 1 : 0;
-  return __builtin_amdgcn_readfirstlane(q);
+  return uniform(q);
 }
 
-template <int TM>
-__device__ __forceinline__ bool find_place(const ActArgs& a, int lane, Place& p) {
-  const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
-  constexpr int KEEP = 2;                                // experts 0 .. 127 are looked up once
-  int r0[KEEP], n[KEEP], inc[KEEP];
-  int tiles_all = 0;
-  if (!a.offsets) {
-    tiles_all = (int)((a.rows + TM - 1) / TM);
-  } else {
+// The units of a launch: tiles of 2^lt rows of each expert x column blocks x K slices, in an
+// order in which the tiles of an expert follow one another (bands of four row tiles, column by
+// column), so that work-groups next to one another share weights or rows.  Units are below
+// 2^24 (the host checks).
+struct Units {
+  int lt;                                                // tiles of 2^lt rows
+  static constexpr int KEEP = 2;                         // experts 0 .. 127 are looked up once
+  int r0[KEEP], n[KEEP], inc[KEEP];                      // lane l: experts l, l + 64: rows, tiles up to it
+  int tiles_all;
+
+  __device__ __forceinline__ int tiles_of(int rows_) const { return (rows_ + (1 << lt) - 1) >> lt; }
+
+  __device__ __forceinline__ int count(const ActArgs& a, int lane) {
+    if (!a.offsets) {
+      tiles_all = tiles_of((int)a.rows);
+    } else {
+      tiles_all = 0;
 #pragma unroll
-    for (int j = 0; j < KEEP; ++j) expert_rows(a, 64 * j + lane, r0[j], n[j]);
+      for (int j = 0; j < KEEP; ++j) expert_rows(a, 64 * j + lane, r0[j], n[j]);
 #pragma unroll
-    for (int j = 0; j < KEEP; ++j) {
-      inc[j] = wave_scan((n[j] + TM - 1) / TM) + tiles_all;
-      tiles_all = __builtin_amdgcn_readlane(inc[j], 63);
-    }
-    for (int b = 64 * KEEP; b < a.e; b += 64) {
-      int first, cnt;
-      expert_rows(a, b + lane, first, cnt);
-      tiles_all += __builtin_amdgcn_readlane(wave_scan((cnt + TM - 1) / TM), 63);
-    }
-  }
-  const int total = tiles_all * a.ncol * a.ks;
-  const int per = (total + 7) / 8;
-  int o = xcd * per + slot;
-  if (slot >= per || o >= total) return false;
-  p.sl = 0;
-  if (a.ks > 1) {
-    const int q = quot(o, a.ks);
-    p.sl = o - q * a.ks;
-    o = q;
-  }
-  int tiles = tiles_all, first = 0, rows = (int)a.rows;
-  p.expert = 0;
-  p.row0 = 0;
-  if (a.offsets) {
-    const int t = quot(o, a.ncol);
-    bool found = false;
-    int last = 0;
-    auto take = [&](int base, int r, int cnt, int sum) {   // the first lane whose sum passes t
-      const uint64_t here = __ballot(t < sum);
-      if (here && !found) {
-        const int l = __builtin_ctzll(here);
-        found = true;
-        p.expert = base + l;
-        rows = __builtin_amdgcn_readlane(cnt, l);
-        tiles = (rows + TM - 1) / TM;
-        first = __builtin_amdgcn_readlane(sum, l) - tiles;
-        p.row0 = __builtin_amdgcn_readlane(r, l);
+      for (int j = 0; j < KEEP; ++j) {
+        inc[j] = wave_scan(tiles_of(n[j])) + tiles_all;
+        tiles_all = __builtin_amdgcn_readlane(inc[j], 63);
       }
-      last = __builtin_amdgcn_readlane(sum, 63);
-    };
-#pragma unroll
-    for (int j = 0; j < KEEP; ++j) take(64 * j, r0[j], n[j], inc[j]);
-    for (int b = 64 * KEEP; !found && b < a.e; b += 64) {
-      int f, cnt;
-      expert_rows(a, b + lane, f, cnt);
-      take(b, f, cnt, wave_scan((cnt + TM - 1) / TM) + last);
+      for (int b = 64 * KEEP; b < a.e; b += 64) {
+        int first, cnt;
+        expert_rows(a, b + lane, first, cnt);
+        tiles_all += __builtin_amdgcn_readlane(wave_scan(tiles_of(cnt)), 63);
+      }
     }
+    return tiles_all * a.ncol * a.ks;
   }
-  const int local = o - first * a.ncol;
-  int tm, tn;
-  if (tiles <= 4) {
-    tn = quot(local, tiles);
-    tm = local - tn * tiles;
-  } else {
-    const int band = quot(local, 4 * a.ncol), left = tiles - 4 * band;
-    const int wide = left < 4 ? left : 4, in = local - band * 4 * a.ncol;
-    tn = quot(in, wide);
-    tm = 4 * band + in - tn * wide;
+
+  __device__ __forceinline__ void at(const ActArgs& a, int lane, int o, Place& p) const {
+    p.sl = 0;
+    if (a.ks > 1) {
+      const int q = quot(o, a.ks);
+      p.sl = o - q * a.ks;
+      o = q;
+    }
+    int tiles = tiles_all, first = 0, rows = (int)a.rows;
+    p.expert = 0;
+    p.row0 = 0;
+    if (a.offsets) {
+      const int t = quot(o, a.ncol);
+      bool found = false;
+      int last = 0;
+      auto take = [&](int base, int r, int cnt, int sum) {   // the first lane whose sum passes t
+        const uint64_t here = __ballot(t < sum);
+        if (here && !found) {
+          const int l = __builtin_ctzll(here);
+          found = true;
+          p.expert = base + l;
+          rows = __builtin_amdgcn_readlane(cnt, l);
+          tiles = tiles_of(rows);
+          first = __builtin_amdgcn_readlane(sum, l) - tiles;
+          p.row0 = __builtin_amdgcn_readlane(r, l);
+        }
+        last = __builtin_amdgcn_readlane(sum, 63);
+      };
+#pragma unroll
+      for (int j = 0; j < KEEP; ++j) take(64 * j, r0[j], n[j], inc[j]);
+      for (int b = 64 * KEEP; !found && b < a.e; b += 64) {
+        int f, cnt;
+        expert_rows(a, b + lane, f, cnt);
+        take(b, f, cnt, wave_scan(tiles_of(cnt)) + last);
+      }
+    }
+    const int local = o - first * a.ncol;
+    int tm, tn;
+    if (tiles <= 4) {
+      tn = tiles == 1 ? local : quot(local, tiles);
+      tm = local - tn * tiles;
+    } else {
+      const int band = quot(local, 4 * a.ncol), left = tiles - 4 * band;
+      const int wide = left < 4 ? left : 4, in = local - band * 4 * a.ncol;
+      tn = quot(in, wide);
+      tm = 4 * band + in - tn * wide;
+    }
+    p.col = tn;
+    p.row0 += tm << lt;
+    rows -= tm << lt;
+    p.rows = rows < 1 << lt ? rows : 1 << lt;
   }
-  p.col = tn;
-  p.row0 += tm * TM;
-  rows -= tm * TM;
-  p.rows = rows < TM ? rows : TM;
+};
+
+// The one unit of this work-group: every XCD takes a contiguous run of the order.  False:
+// nothing to do.
+__device__ __forceinline__ bool find_place(const ActArgs& a, int lane, int lt, Place& p) {
+  Units units;
+  units.lt = lt;
+  const int total = units.count(a, lane);
+  const int per = (total + 7) / 8, slot = blockIdx.x >> 3;
+  const int o = (blockIdx.x & 7) * per + slot;
+  if (slot >= per || o >= total) return false;
+  units.at(a, lane, o, p);
   return true;
 }
 
-// The row of x that row r reads.
-__device__ __forceinline__ int x_row(const ActArgs& a, int r) {
-  if (!a.row_slot) return r;
-  const uint32_t s = (uint32_t)(a.row_slot[r] < 0 ? 0 : a.row_slot[r]);
-  // the quotient in fp32: off by one below 2^24, which is mended; a slot beyond the rows of x
-  // is no slot, and whatever it gives is held within them
+// The row of x that a slot reads, held within the rows there are whatever the plan says: the
+// quotient in fp32 is off by one at most below 2^24, which is mended.
+__device__ __forceinline__ int slot_token(const ActArgs& a, int slot) {
+  const uint32_t s = (uint32_t)(slot < 0 ? 0 : slot);
   int t = (int)((float)s * __builtin_amdgcn_rcpf((float)a.topk));
   const int rem = (int)(s - (uint32_t)t * (uint32_t)a.topk);
   t += rem < 0 ? -1 : rem >= a.topk ? 1 : 0;
@@ -183,6 +198,35 @@ __device__ __forceinline__ float finish(const ActArgs& a, int expert, int64_t o,
   return a.gated ? v * u : v;
 }
 
+// ---------------------------------------------------------------- copies to LDS
+
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// lane i copies 16 (4) bytes from sbase + voff to LDS bytes lds_base + 16 i (4 i)
+__device__ __forceinline__ void lds_copy16(uint32_t voff, const void* sbase, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :
+               : "v"(voff), "s"(sbase), "s"(lds_base)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void lds_copy4(uint32_t voff, const void* sbase, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+               :
+               : "v"(voff), "s"(sbase), "s"(lds_base)
+               : "memory", "m0");
+}
+#pragma clang diagnostic pop
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// a barrier without the fence of __syncthreads, which would wait for every copy in flight
+__device__ __forceinline__ void tile_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // ---------------------------------------------------------------- few rows: weights streamed
 //
 // Up to TM rows of one expert times CB blocks of 16 weight rows; the W waves of a work-group
@@ -219,14 +263,15 @@ __global__ __launch_bounds__(512, 2) void linear_act_stream_kernel(const ActArgs
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int waves = blockDim.x >> 6;
   Place p;
-  if (!find_place<TM>(a, lane, p)) return;
+  if (!find_place(a, lane, TM == 16 ? 4 : 3, p)) return;
   const int r = lane & 15, c = lane >> 4;
   const int k = (int)a.k;
   // CB blocks: outputs col0 .. of the gate and the same of the up projection, or CB of outputs
   const int half = a.gated ? CB / 2 : CB;
   const int col0 = p.col * half * 16;
   // lane i: the row of x that row i of the tile reads; asked for first, the rows wait for it
-  const int src = x_row(a, p.row0 + (r < p.rows ? r : p.rows - 1));
+  const int row_i = p.row0 + (r < p.rows ? r : p.rows - 1);
+  const int src = a.row_slot ? slot_token(a, a.row_slot[row_i]) : row_i;
   const char* qb = reinterpret_cast<const char*>(a.qw + (int64_t)p.expert * a.nw * (a.k / 8));
   const char* sb = reinterpret_cast<const char*>(a.sc + (int64_t)p.expert * a.nw * a.ng);
   const char* zb = reinterpret_cast<const char*>(a.qz + (int64_t)p.expert * a.nw * a.nzw);
@@ -407,35 +452,12 @@ __global__ __launch_bounds__(512, 2) void linear_act_stream_kernel(const ActArgs
 // waits (the compiler sees neither); weights become fp16((q - z) D) in registers.  Rows are
 // read in channel order (gathered by the copies' own addresses), so nibbles are unpacked in
 // pairs of neighbours: a byte permute and a mask per pair.
-constexpr int kTileBN = 256, kTileBK = 64, kTileStages = 3;
-constexpr int tile_stage_bytes(int bm) { return bm * 128 + kTileBN * 32 + 2 * kTileBN * 4; }
-
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-// lane i copies 16 (4) bytes from sbase + voff to LDS bytes lds_base + 16 i (4 i)
-__device__ __forceinline__ void lds_copy16(uint32_t voff, const void* sbase, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-               :
-               : "v"(voff), "s"(sbase), "s"(lds_base)
-               : "memory", "m0");
-}
-__device__ __forceinline__ void lds_copy4(uint32_t voff, const void* sbase, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
-               :
-               : "v"(voff), "s"(sbase), "s"(lds_base)
-               : "memory", "m0");
-}
-#pragma clang diagnostic pop
-template <int N>
-__device__ __forceinline__ void wait_copies() {
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-// a barrier without the fence of __syncthreads, which would wait for every copy in flight
-__device__ __forceinline__ void tile_barrier() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
+constexpr int kTileBN = 256, kTileBK = 64;
+constexpr int kTileStages = 3;
+constexpr int tile_stage_bytes(int bm) { return bm * 128 + kTileBN * 32; }
+// Per K group: two words of scales and two of zero points of every column, and a place for copies
+// of nothing.
+constexpr int kTileScales = 4 * kTileBN * 4 + 4 * 256;
 
 // Masks and selectors of the unpack in channel order, opaque to constant folding: a VOP3
 // instruction takes no literal and one scalar operand.
@@ -462,14 +484,14 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
   constexpr int BMB = BM / 32, BNB = 2;
   constexpr int AR = BM / 32;                         // row copies of a wave and step, 8 rows each
   constexpr int kCopies = AR + 2 + 2;                 // + 2 of packed words, scale and zero words
-  constexpr int kStage = tile_stage_bytes(BM);
+  constexpr int kStage = tile_stage_bytes(BM), ST = kTileStages;
   constexpr int kA = BM * 128, kB = BN * 32;
-  __shared__ __attribute__((aligned(16))) unsigned char ring[kTileStages * KG * kStage];
+  __shared__ __attribute__((aligned(16))) unsigned char ring[KG * (ST * kStage + kTileScales)];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int kgrp = wave >> 2, wv = wave & 3;
   Place p;
-  if (!find_place<BM>(a, lane, p)) return;
+  if (!find_place(a, lane, BM == 32 ? 5 : BM == 64 ? 6 : 7, p)) return;
   const int k = (int)a.k;
   const int nk = k / BK;
   const int kt0 = (int)((int64_t)p.sl * nk / a.ks), kt1 = (int)((int64_t)(p.sl + 1) * nk / a.ks);
@@ -477,6 +499,8 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
 
   const uint32_t ring_lds = (uint32_t)(uintptr_t)(&ring[0]) + (uint32_t)(kgrp * kStage);
   const unsigned char* ring_g = ring + kgrp * kStage;
+  const uint32_t words_lds = (uint32_t)(uintptr_t)(&ring[0]) + (uint32_t)(KG * ST * kStage + kgrp * kTileScales);
+  const unsigned char* words_g = ring + KG * ST * kStage + kgrp * kTileScales;
   // ---- copy sources: a wave-uniform base and the lane's 32-bit byte offset
   const int a_lr = lane >> 3, a_p = lane & 7;
   // rows: their own addresses when gathered (x below 4 GiB), else from the tile's first row
@@ -486,7 +510,7 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
   for (int i = 0; i < AR; ++i) {
     const int lrow = wv * (BM / 4) + 8 * i + a_lr;
     const int row = lrow < p.rows ? lrow : p.rows - 1;
-    const int src = a.row_slot ? x_row(a, p.row0 + row) : row;
+    const int src = a.row_slot ? slot_token(a, a.row_slot[p.row0 + row]) : row;
     a_voff[i] = (uint32_t)(((int64_t)src * a.k + (a_p ^ ((lrow >> 1) & 7)) * 8) * 2);
   }
   // weight row of the tile's column lcol: gated, 32 gate rows and their 32 up rows per wave
@@ -514,6 +538,12 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
     b_voff[h] = (uint32_t)(weight_row(lcol) * (k / 2) + (((lane & 1) ^ ((lcol >> 2) & 1)) * 16));
   }
   const int64_t sz_row = weight_row(wv * 64 + lane);
+  const bool s_turn = (a.ng & 1) != 0;               // rows begin in either half of a word: new words every group
+  // place of the scale word of group g: where a K group's rounds are two words apart, by pairs
+  auto s_place = [&](int g) {
+    const int word = s_turn ? g : g >> 1;
+    return (KG == 2 && (G == 32 || (G == 64 && s_turn)) ? word >> 1 : word) & 1;
+  };
   const uint32_t s_idx = (uint32_t)(sz_row * a.ng) + s_odd, z_voff = (uint32_t)(sz_row * a.nzw * 4);
   auto load = [&](int rnd, int st) {
     int kt = kt0 + KG * rnd + kgrp;
@@ -525,9 +555,17 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
     const char* qk = qb + (int64_t)kt * 32;
 #pragma unroll
     for (int h = 0; h < 2; ++h) lds_copy16(b_voff[h], qk, base + (uint32_t)(kA + (wv * 64 + 32 * h) * 32));
-    const int g0 = kt * BK / G;
-    lds_copy4(((s_idx + (uint32_t)g0) >> 1) * 4, sb, base + (uint32_t)(kA + kB + wv * 256));
-    lds_copy4(z_voff, zb + (int64_t)(g0 >> 3) * 4, base + (uint32_t)(kA + kB + BN * 4 + wv * 256));
+    // A word holds two groups' scales, or eight groups' zero points, and serves until the next:
+    // 64 columns lie on 64 lines, so the copies between are of one line, to nowhere (the waits
+    // count copies).  A word is read into registers a round ahead, so two places take turns.
+    const int g0 = kt * BK / G, gp = rnd > 0 ? (kt0 + KG * (rnd - 1) + kgrp) * BK / G : -64;
+    const bool past = kt0 + KG * rnd + kgrp >= kt1;
+    const bool s_new = !past && (s_turn ? g0 != gp : g0 >> 1 != gp >> 1), z_new = !past && g0 >> 3 != gp >> 3;
+    const uint32_t nowhere = words_lds + (uint32_t)(4 * BN * 4 + wv * 256);
+    lds_copy4(s_new ? ((s_idx + (uint32_t)g0) >> 1) * 4 : 0u, sb,
+              s_new ? words_lds + (uint32_t)(s_place(g0) * BN * 4 + wv * 256) : nowhere);
+    lds_copy4(z_new ? z_voff + (uint32_t)(g0 >> 3) * 4 : 0u, zb,
+              z_new ? words_lds + (uint32_t)((2 + ((g0 >> 3) & 1)) * BN * 4 + wv * 256) : nowhere);
   };
 
   floatx16_t acc[BMB][BNB];
@@ -544,13 +582,12 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
     const int row = bm * 32 + bj;
     a_base[bm] = (uint32_t)(row * 128 + ((4 * bc) ^ ((row >> 1) & 7)) * 16);
   }
-  uint32_t b_off[BNB], s_off[BNB], z_off[BNB], s_par[BNB];
+  uint32_t b_off[BNB], s_off[BNB], s_par[BNB];
 #pragma unroll
   for (int bn = 0; bn < BNB; ++bn) {
     const int lcol = wv * 64 + bn * 32 + bj;
     b_off[bn] = (uint32_t)(kA + lcol * 32 + ((bc ^ ((lcol >> 2) & 1)) * 16));
-    s_off[bn] = (uint32_t)(kA + kB + lcol * 4);
-    z_off[bn] = (uint32_t)(kA + kB + BN * 4 + lcol * 4);
+    s_off[bn] = (uint32_t)(lcol * 4);
     s_par[bn] = ((uint32_t)(weight_row(lcol) * a.ng) + s_odd) & 1;
   }
   struct BSet {
@@ -560,12 +597,12 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
   // what a wave copied itself needs only its own wait: the step's words, scale and zero
   auto prep = [&](int rnd, int st, BSet& r) {
     const unsigned char* s = ring_g + st * KG * kStage;
-    const int grp = ((kt0 + KG * rnd + kgrp) * BK + 32 * bc) / G;
+    const int g0 = (kt0 + KG * rnd + kgrp) * BK / G, grp = g0 + (G == 32 ? bc : 0);
 #pragma unroll
     for (int bn = 0; bn < BNB; ++bn) {
       r.wb[bn] = *reinterpret_cast<const uint4*>(s + b_off[bn]);
-      const uint32_t sw = *reinterpret_cast<const uint32_t*>(s + s_off[bn]);
-      const uint32_t zw = *reinterpret_cast<const uint32_t*>(s + z_off[bn]);
+      const uint32_t sw = *reinterpret_cast<const uint32_t*>(words_g + s_place(g0) * BN * 4 + s_off[bn]);
+      const uint32_t zw = *reinterpret_cast<const uint32_t*>(words_g + (2 + ((g0 >> 3) & 1)) * BN * 4 + s_off[bn]);
       const uint32_t d = (sw >> (16 * ((s_par[bn] + (uint32_t)grp) & 1))) & 0xFFFFu;
       const uint32_t z = (zw >> (4 * (grp & 7))) & 0xFu;
       r.dd[bn] = __builtin_bit_cast(half2_t, d | (d << 16));
@@ -585,13 +622,14 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
       out[bn] = __builtin_bit_cast(half8_t, make_uint4(q[0], q[1], q[2], q[3]));
     }
   };
-  BSet r0, r1;
+  BSet rs[2];
   half8_t bq[BNB];
-  // Round P in stage st: meet, then four 16-channel sub-steps.  Each sub-step's products run
-  // while the next one's weights are unpacked; the copies of round P + 2 go out after the
+  // Round P in stage P % ST: meet, then four 16-channel sub-steps.  Each sub-step's products run
+  // while the next one's weights are unpacked; the copies of round P + ST - 1 go out after the
   // first sub-step, into the stage round P - 1 used; the last sub-step waits for the wave's
   // own copies of round P + 1 and prepares its weights.
-  auto step = [&](int rnd, int st, int stn, int stp, const BSet& r, BSet& rn) {
+  auto step = [&](int rnd, int st, const BSet& r, BSet& rn) {
+    const int stn = (st + ST - 1) % ST, stp = (st + 1) % ST;
     __builtin_amdgcn_sched_barrier(0);
     tile_barrier();
     if (KG == 1 || kt0 + KG * rnd + kgrp < kt1) {
@@ -605,7 +643,7 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
         if (s < 3) {
           dequant(r, s + 1, bqn);
         } else {
-          wait_copies<kCopies>();
+          wait_copies<kCopies * (ST - 2)>();
           prep(rnd + 1, stp, rn);
           dequant(rn, 0, bqn);
         }
@@ -616,34 +654,31 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
             acc[bm][bn] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[bm], bq[bn], acc[bm][bn], 0, 0, 0);
           if (s < 3) af[bm] = *reinterpret_cast<const half8_t*>(cur + (a_base[bm] ^ (uint32_t)(16 * (s + 1))));
         }
-        if (s == 0) load(rnd + 2, stn);
+        if (s == 0) load(rnd + ST - 1, stn);
 #pragma unroll
         for (int bn = 0; bn < BNB; ++bn) bq[bn] = bqn[bn];
       }
     } else {                                          // the second K group's share of an odd last round
-      load(rnd + 2, stn);
-      wait_copies<kCopies>();
+      load(rnd + ST - 1, stn);
+      wait_copies<kCopies * (ST - 2)>();
       prep(rnd + 1, stp, rn);
       dequant(rn, 0, bq);
     }
   };
-  load(0, 0);
-  load(1, 1);
-  wait_copies<kCopies>();
-  prep(0, 0, r0);
-  dequant(r0, 0, bq);
+#pragma unroll
+  for (int i = 0; i < ST - 1; ++i) load(i, i);
+  wait_copies<kCopies * (ST - 2)>();
+  prep(0, 0, rs[0]);
+  dequant(rs[0], 0, bq);
   int rp = 0;
-  for (; rp + 3 <= nr; rp += 3) {
-    step(rp, 0, 2, 1, r0, r1);
-    step(rp + 1, 1, 0, 2, r1, r0);
-    step(rp + 2, 2, 1, 0, r0, r1);
-    r0 = r1;
+  for (; rp + ST <= nr; rp += ST) {
+#pragma unroll
+    for (int i = 0; i < ST; ++i) step(rp + i, i, rs[i & 1], rs[1 - (i & 1)]);
+    if (ST & 1) rs[0] = rs[1];
   }
-  if (rp < nr) {
-    step(rp, 0, 2, 1, r0, r1);
-    r0 = r1;
-  }
-  if (rp + 1 < nr) step(rp + 1, 1, 0, 2, r0, r1);
+#pragma unroll
+  for (int i = 0; i < ST - 1; ++i)
+    if (rp + i < nr) step(rp + i, i, rs[i & 1], rs[1 - (i & 1)]);
   wait_copies<0>();                                   // the look-ahead has landed before the LDS is used again
   tile_barrier();
 
@@ -698,7 +733,8 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
   constexpr int ER = 68;                              // floats of a staged row: two lane halves 16 banks apart
   // (two K groups: behind the hand-over area, which other waves may still read)
   constexpr int kHand = KG == 2 ? 4 * BMB * BNB * 16 * 64 : 0;
-  constexpr bool kBehind = (kHand + 4 * 32 * ER) * 4 <= kTileStages * KG * kStage;
+  constexpr bool kBehind = (kHand + 4 * 32 * ER) * 4 <= (int)sizeof(ring);
+  static_assert(kCopies * (ST - 1) < 64, "the wait counter");
   static_assert(kBehind || 32 * ER <= BMB * BNB * 16 * 64, "else within the wave's own part of it");
   float* ep = reinterpret_cast<float*>(ring) + (kBehind ? kHand + wv * 32 * ER : wv * (BMB * BNB * 16 * 64));
   auto al = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
@@ -841,7 +877,8 @@ static ActPlan act_plan(const ActArgs& a) {
   auto tiles = [&](int tm) { return a.offsets ? a.rows / tm + active : (a.rows + tm - 1) / tm; };
   p.ks = 1;
   p.kg = 1;
-  if (avg <= 16) {
+  const int64_t bytes = a.nw * (a.k / 2);            // of a matrix
+  if (a.offsets ? avg <= 12 : avg <= 16 || (avg <= 512 && (avg + 15) / 16 * bytes <= (36 << 20))) {
     p.stream = true;
     p.tm = avg <= 8 ? 8 : 16;
     p.cb = 2;
@@ -853,11 +890,12 @@ static ActPlan act_plan(const ActArgs& a) {
     p.units = tiles(p.tm) * p.ncol;
     return p;
   }
-  p.bm = avg <= 32 ? 32 : avg <= 64 ? 64 : 128;
   const int outs = a.gated ? 128 : 256;
   p.ncol = (a.n + outs - 1) / outs;
-  const int64_t t = tiles(p.bm) * p.ncol;
   const int nk = (int)(a.k / 64);
+  const int64_t steps = tiles(128) * p.ncol * nk;    // K-steps of all 128-row tiles
+  p.bm = avg <= 32 || steps <= 1024 ? 32 : avg <= 64 || steps <= 3000 ? 64 : 128;
+  const int64_t t = tiles(p.bm) * p.ncol;
   if (!a.offsets && t < 256 && a.rows <= 512) {
     int64_t ks = 256 / t;
     ks = ks > 16 ? 16 : ks;
@@ -882,8 +920,7 @@ size_t linear_act_scratch_bytes(const ActArgs& a) {
 
 bool linear_act_fits(const ActArgs& a) {
   const ActPlan p = act_plan(a);
-  const int64_t threads = p.stream ? 64 * p.waves : 256 * p.kg;
-  return p.units <= (1ll << 31) / threads && p.units < (1 << 24) && a.x_rows * (a.k / 8) <= (1ll << 31) &&
+  return p.units < (1 << 22) && a.x_rows * (a.k / 8) <= (1ll << 31) &&
          a.rows * ((a.n + 3) / 4) <= (1ll << 31);
 }
 
