@@ -12,7 +12,7 @@ namespace awq {
 __device__ __forceinline__ uint32_t lanes_max(uint32_t x) {
 #define AWQ_LANES_MAX(CTRL, ROWS)                                                                      \
   {                                                                                                    \
-    const uint32_t o_ = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xf, false);      \
+    const uint32_t o_ = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xf, true);       \
     x = x > o_ ? x : o_;                                                                               \
   }
   AWQ_LANES_MAX(0x111, 0xf)

@@ -55,22 +55,26 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
-// One token by one wave: lane l holds experts l, l + 64, ...  Lane j < topk ends with
-// choice j; -1 and weight 0 where fewer experts are open; all weights NaN where a
-// logit is NaN.
+// A token's logits: lane l holds experts l, l + 64, ...; -inf behind the last.
 template <int NPL>
-__device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int lane, int& id, float& w) {
+__device__ __forceinline__ void load_token(const RouteArgs& a, int64_t t, int lane, float (&v)[NPL]) {
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const int x = lane + 64 * i;
+    v[i] = x < a.e ? load_logit(a, t * a.e + x) : -__builtin_inff();
+  }
+}
+
+// One token by one wave.  Lane j < topk ends with choice j; -1 and weight 0 where fewer
+// experts are open; all weights NaN where a logit is NaN.
+template <int NPL>
+__device__ __forceinline__ void route_token(const RouteArgs& a, const float (&v)[NPL], int lane, int& id, float& w) {
   uint32_t key[NPL];
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
-    const int x = lane + 64 * i;
-    key[i] = 0;
-    if (x < a.e) {
-      const float v = load_logit(a, t * a.e + x);
-      key[i] = order_key(v);
-      bad |= v != v;
-    }
+    key[i] = order_key(v[i]);
+    bad |= v[i] != v[i];
   }
   auto value = [](uint32_t k) {
     return __builtin_bit_cast(float, k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
@@ -96,14 +100,11 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int l
   uint32_t best = first;
   for (int j = 0; j < a.topk && best > kClosedKey; ++j) {
     // the lowest expert that holds the maximum
-    int at = 0x7FFFFFFF;
+    int at = -1;
 #pragma unroll
-    for (int i = NPL - 1; i >= 0; --i)
-      if (key[i] == best) at = lane + 64 * i;
-    if (NPL == 1) {
-      at = __builtin_ctzll(__ballot(at != 0x7FFFFFFF));
-    } else {
-      at = (int)~lanes_max(~(uint32_t)at);
+    for (int i = NPL - 1; i >= 0; --i) {
+      const uint64_t here = __ballot(key[i] == best);
+      at = here ? 64 * i + __builtin_ctzll(here) : at;
     }
 #pragma unroll
     for (int i = 0; i < NPL; ++i)
@@ -153,18 +154,24 @@ __device__ __forceinline__ void rank_slots(int s0, int s1, int e, int wave, int 
   }
 }
 
-// Tokens [t0, t1) by the work-group's waves; choices to `ids` and `weights`, and to LDS
-// when the caller places them itself.
-template <int NPL>
-__device__ __forceinline__ void route_chunk(const RouteArgs& a, int t0, int t1, int wave, int lane, int* lds_ids) {
+// Tokens [t0, t1) by the work-group's waves, the next one's logits asked for ahead; choices to
+// ids and weights, and each(token - t0, expert) in lane j for choice j.
+template <int NPL, class Each>
+__device__ __forceinline__ void route_chunk(const RouteArgs& a, int t0, int t1, int wave, int lane, Each each) {
+  float next[NPL];
+  if (t0 + wave < t1) load_token<NPL>(a, t0 + wave, lane, next);
   for (int t = t0 + wave; t < t1; t += kRouteWaves) {
+    float v[NPL];
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) v[i] = next[i];
+    if (t + kRouteWaves < t1) load_token<NPL>(a, t + kRouteWaves, lane, next);
     int id;
     float w;
-    route_token<NPL>(a, t, lane, id, w);
+    route_token<NPL>(a, v, lane, id, w);
     if (lane < a.topk) {
       a.ids[(int64_t)t * a.topk + lane] = id;
       a.weights[(int64_t)t * a.topk + lane] = w;
-      if (lds_ids) lds_ids[(t - t0) * a.topk + lane] = id;
+      each(t - t0, id);
     }
   }
 }
@@ -195,7 +202,7 @@ __global__ __launch_bounds__(kRouteWaves * 64) void moe_route_small_kernel(const
   int* tot = hist + kRouteWaves * e;
   int* start = tot + e;
   for (int i = tid; i < kRouteWaves * e; i += kRouteWaves * 64) hist[i] = 0;
-  route_chunk<NPL>(a, 0, a.t, wave, lane, ids);
+  route_chunk<NPL>(a, 0, a.t, wave, lane, [&](int t, int id) { ids[t * a.topk + lane] = id; });
   __syncthreads();
   const int bits = 32 - __builtin_clz(e);
   rank_slots(0, slots, e, wave, lane, bits, hist, [&](int s) { return ids[s]; },
@@ -234,16 +241,9 @@ __global__ __launch_bounds__(kRouteWaves * 64) void moe_route_kernel(const Route
   const int t0 = blockIdx.x * a.chunk, t1 = t0 + a.chunk < a.t ? t0 + a.chunk : a.t;
   for (int i = tid; i < a.e; i += kRouteWaves * 64) hist[i] = 0;
   __syncthreads();
-  for (int t = t0 + wave; t < t1; t += kRouteWaves) {
-    int id;
-    float w;
-    route_token<NPL>(a, t, lane, id, w);
-    if (lane < a.topk) {
-      a.ids[(int64_t)t * a.topk + lane] = id;
-      a.weights[(int64_t)t * a.topk + lane] = w;
-      if (id >= 0) atomicAdd(&hist[id], 1);           // a count: the order of the additions does not show
-    }
-  }
+  route_chunk<NPL>(a, t0, t1, wave, lane, [&](int, int id) {
+    if (id >= 0) atomicAdd(&hist[id], 1);             // a count: the order of the additions does not show
+  });
   __syncthreads();
   for (int i = tid; i < a.e; i += kRouteWaves * 64) a.counts[(int64_t)blockIdx.x * a.e + i] = hist[i];
 }
@@ -311,13 +311,13 @@ __global__ __launch_bounds__(kRouteWaves * 64) void moe_place_kernel(const Route
   }
 }
 
-// Tokens one work-group takes: all of up to kRouteSmall, else chunks of at least 64 in at
+// Tokens one work-group takes: all of up to kRouteSmall, else chunks of at least 32 in at
 // most 256 work-groups.
-constexpr int kRouteSmall = 64;
+constexpr int kRouteSmall = 48;
 static int route_chunk_tokens(int64_t t) {
   int64_t c = (t + 255) / 256;
   c = (c + 15) / 16 * 16;
-  return (int)(c < 64 ? 64 : c);
+  return (int)(c < 32 ? 32 : c);
 }
 static bool route_small(int64_t t) { return t <= kRouteSmall; }
 
