@@ -452,9 +452,9 @@ __global__ __launch_bounds__(512, 2) void linear_act_stream_kernel(const ActArgs
 // waits (the compiler sees neither); weights become fp16((q - z) D) in registers.  Rows are
 // read in channel order (gathered by the copies' own addresses), so nibbles are unpacked in
 // pairs of neighbours: a byte permute and a mask per pair.
-constexpr int kTileBN = 256, kTileBK = 64;
+constexpr int kTileBN = 256;
 constexpr int kTileStages = 3;
-constexpr int tile_stage_bytes(int bm) { return bm * 128 + kTileBN * 32; }
+constexpr int tile_stage_bytes(int bm, int bk) { return bm * bk * 2 + kTileBN * bk / 2; }
 // Per K group: two words of scales and two of zero points of every column, and a place for copies
 // of nothing.
 constexpr int kTileScales = 4 * kTileBN * 4 + 4 * 256;
@@ -478,14 +478,16 @@ __device__ __forceinline__ PairConsts pair_consts() {
   return p;
 }
 
-template <int G, int KG, int BM>
+template <int G, int KG, int BM, int BK>
 __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_kernel(const ActArgs a) {
-  constexpr int BN = kTileBN, BK = kTileBK;
+  static_assert(BK == 64 || (BK == 128 && G >= 64), "a lane's half of a K-step is of one group");
+  constexpr int BN = kTileBN;
+  constexpr int CH = BK / 8, BCH = BK / 32, NS = BK / 16;   // 16-byte chunks of a row and of a weight row, sub-steps
   constexpr int BMB = BM / 32, BNB = 2;
-  constexpr int AR = BM / 32;                         // row copies of a wave and step, 8 rows each
-  constexpr int kCopies = AR + 2 + 2;                 // + 2 of packed words, scale and zero words
-  constexpr int kStage = tile_stage_bytes(BM), ST = kTileStages;
-  constexpr int kA = BM * 128, kB = BN * 32;
+  constexpr int RPC = 64 / CH, AR = BM / 4 / RPC;     // rows of a copy, row copies of a wave and step
+  constexpr int kCopies = AR + BCH + 2;               // + those of packed words, scale and zero words
+  constexpr int kStage = tile_stage_bytes(BM, BK), ST = kTileStages;
+  constexpr int kA = BM * BK * 2;
   __shared__ __attribute__((aligned(16))) unsigned char ring[KG * (ST * kStage + kTileScales)];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -502,16 +504,19 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
   const uint32_t words_lds = (uint32_t)(uintptr_t)(&ring[0]) + (uint32_t)(KG * ST * kStage + kgrp * kTileScales);
   const unsigned char* words_g = ring + KG * ST * kStage + kgrp * kTileScales;
   // ---- copy sources: a wave-uniform base and the lane's 32-bit byte offset
-  const int a_lr = lane >> 3, a_p = lane & 7;
+  const int a_lr = lane / CH, a_p = lane % CH;
+  // chunks lie XOR-swizzled so that 16 rows' (columns') chunks fall on all banks
+  auto a_swz = [](int row) { return BK == 64 ? (row >> 1) & 7 : row & 15; };
+  auto b_swz = [](int col) { return (col >> 2) & (BCH - 1); };
   // rows: their own addresses when gathered (x below 4 GiB), else from the tile's first row
   const char* xb = reinterpret_cast<const char*>(a.x + (a.row_slot ? 0 : (int64_t)p.row0 * a.k));
   uint32_t a_voff[AR];
 #pragma unroll
   for (int i = 0; i < AR; ++i) {
-    const int lrow = wv * (BM / 4) + 8 * i + a_lr;
+    const int lrow = wv * (BM / 4) + RPC * i + a_lr;
     const int row = lrow < p.rows ? lrow : p.rows - 1;
     const int src = a.row_slot ? slot_token(a, a.row_slot[p.row0 + row]) : row;
-    a_voff[i] = (uint32_t)(((int64_t)src * a.k + (a_p ^ ((lrow >> 1) & 7)) * 8) * 2);
+    a_voff[i] = (uint32_t)(((int64_t)src * a.k + (a_p ^ a_swz(lrow)) * 8) * 2);
   }
   // weight row of the tile's column lcol: gated, 32 gate rows and their 32 up rows per wave
   const int span = a.gated ? 128 : 256;
@@ -531,18 +536,18 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
   const int64_t s_first = (int64_t)p.expert * a.nw * a.ng;
   const char* sb = reinterpret_cast<const char*>(a.sc + (s_first & ~1ll));
   const uint32_t s_odd = (uint32_t)(s_first & 1);
-  uint32_t b_voff[2];
+  uint32_t b_voff[BCH];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int lcol = wv * 64 + 32 * h + (lane >> 1);
-    b_voff[h] = (uint32_t)(weight_row(lcol) * (k / 2) + (((lane & 1) ^ ((lcol >> 2) & 1)) * 16));
+  for (int h = 0; h < BCH; ++h) {
+    const int lcol = wv * 64 + 64 / BCH * h + lane / BCH;
+    b_voff[h] = (uint32_t)(weight_row(lcol) * (k / 2) + (((lane % BCH) ^ b_swz(lcol)) * 16));
   }
   const int64_t sz_row = weight_row(wv * 64 + lane);
   const bool s_turn = (a.ng & 1) != 0;               // rows begin in either half of a word: new words every group
   // place of the scale word of group g: where a K group's rounds are two words apart, by pairs
   auto s_place = [&](int g) {
     const int word = s_turn ? g : g >> 1;
-    return (KG == 2 && (G == 32 || (G == 64 && s_turn)) ? word >> 1 : word) & 1;
+    return (KG * BK >= (s_turn ? 2 : 4) * G ? word >> 1 : word) & 1;
   };
   const uint32_t s_idx = (uint32_t)(sz_row * a.ng) + s_odd, z_voff = (uint32_t)(sz_row * a.nzw * 4);
   auto load = [&](int rnd, int st) {
@@ -551,10 +556,10 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
     const uint32_t base = ring_lds + (uint32_t)(st * KG * kStage);
     const char* xk = xb + (int64_t)kt * BK * 2;
 #pragma unroll
-    for (int i = 0; i < AR; ++i) lds_copy16(a_voff[i], xk, base + (uint32_t)((wv * (BM / 4) + 8 * i) * 128));
-    const char* qk = qb + (int64_t)kt * 32;
+    for (int i = 0; i < AR; ++i) lds_copy16(a_voff[i], xk, base + (uint32_t)((wv * (BM / 4) + RPC * i) * BK * 2));
+    const char* qk = qb + (int64_t)kt * (BK / 2);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) lds_copy16(b_voff[h], qk, base + (uint32_t)(kA + (wv * 64 + 32 * h) * 32));
+    for (int h = 0; h < BCH; ++h) lds_copy16(b_voff[h], qk, base + (uint32_t)(kA + (wv * 64 + 64 / BCH * h) * (BK / 2)));
     // A word holds two groups' scales, or eight groups' zero points, and serves until the next:
     // 64 columns lie on 64 lines, so the copies between are of one line, to nowhere (the waits
     // count copies).  A word is read into registers a round ahead, so two places take turns.
@@ -574,33 +579,34 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
 #pragma unroll
     for (int j = 0; j < BNB; ++j) acc[i][j] = floatx16_t{};
   const PairConsts pc = pair_consts();
-  // ---- fragments: rows from chunk (4 (lane / 32) + s) ^ swizzle(row); words of column j, half c
+  // ---- fragments: rows from chunk (CH / 2 (lane / 32) + s) ^ swizzle(row); words of column j, half c
   const int bj = lane & 31, bc = lane >> 5;
   uint32_t a_base[BMB];
 #pragma unroll
   for (int bm = 0; bm < BMB; ++bm) {
     const int row = bm * 32 + bj;
-    a_base[bm] = (uint32_t)(row * 128 + ((4 * bc) ^ ((row >> 1) & 7)) * 16);
+    a_base[bm] = (uint32_t)(row * BK * 2 + ((CH / 2 * bc) ^ a_swz(row)) * 16);
   }
   uint32_t b_off[BNB], s_off[BNB], s_par[BNB];
 #pragma unroll
   for (int bn = 0; bn < BNB; ++bn) {
     const int lcol = wv * 64 + bn * 32 + bj;
-    b_off[bn] = (uint32_t)(kA + lcol * 32 + ((bc ^ ((lcol >> 2) & 1)) * 16));
+    b_off[bn] = (uint32_t)(kA + lcol * (BK / 2) + ((BCH / 2 * bc) ^ b_swz(lcol)) * 16);
     s_off[bn] = (uint32_t)(lcol * 4);
     s_par[bn] = ((uint32_t)(weight_row(lcol) * a.ng) + s_odd) & 1;
   }
   struct BSet {
-    uint4 wb[BNB];
+    uint4 wb[BNB][BCH / 2];
     half2_t dd[BNB], off[BNB];
   };
   // what a wave copied itself needs only its own wait: the step's words, scale and zero
   auto prep = [&](int rnd, int st, BSet& r) {
     const unsigned char* s = ring_g + st * KG * kStage;
-    const int g0 = (kt0 + KG * rnd + kgrp) * BK / G, grp = g0 + (G == 32 ? bc : 0);
+    const int g0 = (kt0 + KG * rnd + kgrp) * BK / G, grp = ((kt0 + KG * rnd + kgrp) * BK + BK / 2 * bc) / G;
 #pragma unroll
     for (int bn = 0; bn < BNB; ++bn) {
-      r.wb[bn] = *reinterpret_cast<const uint4*>(s + b_off[bn]);
+#pragma unroll
+      for (int h = 0; h < BCH / 2; ++h) r.wb[bn][h] = *reinterpret_cast<const uint4*>(s + (b_off[bn] ^ (uint32_t)(16 * h)));
       const uint32_t sw = *reinterpret_cast<const uint32_t*>(words_g + s_place(g0) * BN * 4 + s_off[bn]);
       const uint32_t zw = *reinterpret_cast<const uint32_t*>(words_g + (2 + ((g0 >> 3) & 1)) * BN * 4 + s_off[bn]);
       const uint32_t d = (sw >> (16 * ((s_par[bn] + (uint32_t)grp) & 1))) & 0xFFFFu;
@@ -612,7 +618,8 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
   auto dequant = [&](const BSet& r, int s, half8_t (&out)[BNB]) {
 #pragma unroll
     for (int bn = 0; bn < BNB; ++bn) {
-      const uint32_t w = s == 0 ? r.wb[bn].x : s == 1 ? r.wb[bn].y : s == 2 ? r.wb[bn].z : r.wb[bn].w;
+      const uint4 wv4 = r.wb[bn][s >> 2];
+      const uint32_t w = (s & 3) == 0 ? wv4.x : (s & 3) == 1 ? wv4.y : (s & 3) == 2 ? wv4.z : wv4.w;
       uint32_t q[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -624,7 +631,7 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
   };
   BSet rs[2];
   half8_t bq[BNB];
-  // Round P in stage P % ST: meet, then four 16-channel sub-steps.  Each sub-step's products run
+  // Round P in stage P % ST: meet, then sub-steps of 16 channels.  Each sub-step's products run
   // while the next one's weights are unpacked; the copies of round P + ST - 1 go out after the
   // first sub-step, into the stage round P - 1 used; the last sub-step waits for the wave's
   // own copies of round P + 1 and prepares its weights.
@@ -638,9 +645,9 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
 #pragma unroll
       for (int bm = 0; bm < BMB; ++bm) af[bm] = *reinterpret_cast<const half8_t*>(cur + a_base[bm]);
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
+      for (int s = 0; s < NS; ++s) {
         half8_t bqn[BNB];
-        if (s < 3) {
+        if (s < NS - 1) {
           dequant(r, s + 1, bqn);
         } else {
           wait_copies<kCopies * (ST - 2)>();
@@ -652,7 +659,7 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
 #pragma unroll
           for (int bn = 0; bn < BNB; ++bn)
             acc[bm][bn] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[bm], bq[bn], acc[bm][bn], 0, 0, 0);
-          if (s < 3) af[bm] = *reinterpret_cast<const half8_t*>(cur + (a_base[bm] ^ (uint32_t)(16 * (s + 1))));
+          if (s < NS - 1) af[bm] = *reinterpret_cast<const half8_t*>(cur + (a_base[bm] ^ (uint32_t)(16 * (s + 1))));
         }
         if (s == 0) load(rnd + ST - 1, stn);
 #pragma unroll
@@ -862,7 +869,7 @@ __global__ __launch_bounds__(256) void linear_act_prep_kernel(const ActArgs a, u
 struct ActPlan {
   bool stream;
   int cb, tm, waves, per;      // stream
-  int bm, kg, ks;              // tile
+  int bm, bk, kg, ks;          // tile
   bool prep;
   int64_t ncol, units;         // column blocks; upper bound of the units
   size_t x_bytes, part_bytes;
@@ -896,6 +903,7 @@ static ActPlan act_plan(const ActArgs& a) {
   const int64_t steps = tiles(128) * p.ncol * nk;    // K-steps of all 128-row tiles
   p.bm = avg <= 32 || steps <= 1024 ? 32 : avg <= 64 || steps <= 3000 ? 64 : 128;
   const int64_t t = tiles(p.bm) * p.ncol;
+  p.bk = p.bm == 32 && a.g >= 64 && a.k % 128 == 0 ? 128 : 64;
   if (!a.offsets && t < 256 && a.rows <= 512) {
     int64_t ks = 256 / t;
     ks = ks > 16 ? 16 : ks;
@@ -943,9 +951,9 @@ static hipError_t run_stream(const ActArgs& a, const ActPlan& p, hipStream_t str
   return go(linear_act_stream_kernel<G, CB, TM, false>);
 }
 
-template <int G, int KG, int BM>
+template <int G, int KG, int BM, int BK = 64>
 static hipError_t run_tile(const ActArgs& a, const ActPlan& p, hipStream_t stream) {
-  hipLaunchKernelGGL((linear_act_tile_kernel<G, KG, BM>), dim3((unsigned)((p.units + 7) / 8 * 8)), dim3(256 * KG), 0,
+  hipLaunchKernelGGL((linear_act_tile_kernel<G, KG, BM, BK>), dim3((unsigned)((p.units + 7) / 8 * 8)), dim3(256 * KG), 0,
                      stream, a);
   return hipGetLastError();
 }
@@ -954,6 +962,9 @@ template <int G>
 static hipError_t run_act(const ActArgs& a, const ActPlan& p, hipStream_t stream) {
   if (p.stream) {
     return p.tm == 8 ? run_stream<G, 2, 8>(a, p, stream) : run_stream<G, 2, 16>(a, p, stream);
+  }
+  if constexpr (G >= 64) {
+    if (p.bm == 32 && p.bk == 128) return p.kg == 2 ? run_tile<G, 2, 32, 128>(a, p, stream) : run_tile<G, 1, 32, 128>(a, p, stream);
   }
   if (p.bm == 32) return p.kg == 2 ? run_tile<G, 2, 32>(a, p, stream) : run_tile<G, 1, 32>(a, p, stream);
   if (p.bm == 64) return p.kg == 2 ? run_tile<G, 2, 64>(a, p, stream) : run_tile<G, 1, 64>(a, p, stream);
