@@ -624,8 +624,9 @@ awq_status awq_attn_kv8_bf16(const awq_kv8_cache* cache, int64_t rows, int64_t m
  *   scales and qzeros 4-byte aligned.  workspace:
  *   awq_linear_act_workspace_size(m, n, k, g, gated, inv_s16 != NULL, bf16) bytes,
  *   256-byte aligned (NULL if that is 0).
- *   Limits: g in {32, 64, 128}; k % g == 0; k % 64 == 0; 0 <= m <= 2^27; packed weights
- *   below 4 GiB; m * n/4, m * k/8 <= 2^31.
+ *   Limits: g in {32, 64, 128}; k % g == 0; k % 64 == 0; k <= 2^23; 0 <= m <= 2^27; packed
+ *   weights below 4 GiB; m * n/4, m * k/8 <= 2^31; what one launch holds: m * n below some
+ *   2^35 (2^36 up to 512 rows).
  * ------------------------------------------------------------------------- */
 enum { AWQ_ACT_NONE = 0, AWQ_ACT_SILU = 1, AWQ_ACT_GELU = 2, AWQ_ACT_GELU_TANH = 3 };
 size_t awq_linear_act_workspace_size(int64_t m, int64_t n, int64_t k, int32_t g, int32_t gated,
@@ -677,8 +678,9 @@ awq_status awq_linear_w4a16_act_bf16(const uint16_t* x, const uint32_t* qweight,
  *   awq_fold_inv_scale_rows).  Row r of y [rows][n] reads x[row_slot[r] / topk] of
  *   x [x_rows][k], or with row_slot NULL x[r] of x [rows][k] (x_rows is not read).
  *   offsets and row_slot are device data and not checked on the host: whatever they
- *   hold, nothing outside the tensors is read or written.  Rows of y that no expert
- *   has are not written.  rows: what row_slot and y hold, at least offsets[e].  The
+ *   hold, nothing outside the tensors is read or written.  Under offsets that do not
+ *   ascend within 0 .. rows nothing is written; a slot outside those of x gives a row
+ *   of x all the same.  Rows of y that no expert has are not written.  rows: what row_slot and y hold, at least offsets[e].  The
  *   number of rows and experts chooses between kernels; results are right for any
  *   split of the rows.
  *   workspace: awq_moe_linear_workspace_size(rows, x_rows, e, n, k, g, gated,

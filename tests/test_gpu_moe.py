@@ -90,6 +90,21 @@ def test_dense_longer(P, m, n, k, g, gated):
     dense(P, m, n, k, g, BF16, "silu" if gated else "none", gated)
 
 
+# every form of the tiles: rows, K-step, K groups, K slices, with odd numbers of groups and ragged ends
+@pytest.mark.parametrize("m,n,k,g,gated", [(600, 2000, 128, 64, False), (600, 2040, 192, 64, False), (600, 1000, 160 * 2, 32, True),
+                                           (2000, 4090, 64, 64, False), (2000, 4096, 128, 128, False), (2000, 2050, 64, 32, True),
+                                           (640, 4096, 1024, 128, False), (640, 2048, 1088, 64, True), (640, 4000, 960, 32, False),
+                                           (1500, 8192, 320, 64, False), (1500, 4096, 384, 128, True), (1500, 8200, 320, 32, False),
+                                           (640, 4096, 2688, 128, False), (640, 4096, 2752, 64, False), (640, 2048, 2720 - 32, 32, True),
+                                           (1100, 8192, 1408, 128, False), (1100, 4100, 1984, 64, True), (1100, 8192, 1472, 32, False),
+                                           (24, 16384, 4096, 128, False), (24, 8192, 4160, 64, True), (24, 16384, 4096, 32, False),
+                                           (40, 8192, 4096, 128, False), (50, 4096, 4160, 64, True), (40, 8192, 4096, 32, False),
+                                           (200, 4096, 4224, 128, True), (200, 8192, 4160, 64, False), (200, 8192, 4096, 32, False)])
+def test_dense_tiles(P, m, n, k, g, gated):
+    i = m + n + k
+    dense(P, m, n, k, g, (F16, BF16)[i // 64 % 2], ("none", "silu")[gated], gated, bool(i // 32 % 2), bool(i // 128 % 2), not gated)
+
+
 def test_dense_extremes(P):
     """Activations at their ends, scales of zero and NaN, inputs with inf and NaN: as in float64, and only where they belong."""
     k, n, g = 128, 40, 128
@@ -236,25 +251,72 @@ def test_grouped(P, counts, gather):
     grouped(P, counts, 24, 320, 64, BF16, gather, "gelu_tanh", True, False, False, topk=1)
 
 
-def test_grouped_many_experts(P):
+@pytest.mark.parametrize("e,most", [(1024, 4), (129, 30), (200, 90)])
+def test_grouped_many_experts(P, e, most):
     g = gen(3)
-    counts = torch.randint(0, 4, (1024,), generator=g).tolist()
+    counts = torch.randint(0, most, (e,), generator=g).tolist()
     grouped(P, counts, 16, 64, 64, F16, True, "silu", True)
+    grouped(P, counts, 40, 128, 128, BF16, False, "none", False, True, True)
 
 
-@pytest.mark.parametrize("bad", [[0, -3, 2, 9], [5, 1, 0, 4], [0, 4, 1000000, 2000000000], [-2 ** 31, 2 ** 31 - 1, -1, 3]])
+@pytest.mark.parametrize("bad", [[0, -3, 2, 9], [5, 1, 0, 4], [0, 4, 1000000, 2000000000], [-2 ** 31, 2 ** 31 - 1, -1, 3],
+                                 [0, 9, 9, 8], [-1, 2, 3, 4]])
 @pytest.mark.parametrize("rows", [9, 150])
-def test_grouped_bad_plans_stay_inside(P, bad, rows):
-    """Offsets and slots of any value: nothing outside the tensors is written, and the call returns."""
+def test_grouped_plans_out_of_order_write_nothing(P, bad, rows):
+    e, n, k = 3, 40, 128
+    ge = gen(1)
+    qw, sc, qz = (t.to(DEV) for t in R.packed(ge, (e,), n, k, 128))
+    x = tokens(ge, 4, k, F16).to(DEV)
+    slots = torch.arange(rows, dtype=torch.int32, device=DEV) % 8
+    out, whole = guarded(rows, n, F16)
+    out.fill_(-5)
+    P.awq_moe_linear_w4a16(x, qw, sc, qz, torch.tensor(bad, dtype=torch.int32, device=DEV), slots, 2, out=out)
+    torch.cuda.synchronize()
+    assert whole() and bool((out == -5).all())
+    many = torch.zeros(1025, dtype=torch.int32)                                  # the bad one among many experts
+    many[700:] = rows
+    many[900] = rows + 1
+    qw, sc, qz = (t[:1].repeat(1024, 1, 1).contiguous() for t in (qw, sc, qz))
+    P.awq_moe_linear_w4a16(x, qw, sc, qz, many.to(DEV), slots, 2, out=out)
+    torch.cuda.synchronize()
+    assert whole() and bool((out == -5).all())
+
+
+@pytest.mark.parametrize("bad", [[0, 3, 3, 9], [2, 2, 8, 9]])
+@pytest.mark.parametrize("rows", [9, 150])
+def test_grouped_any_slots_stay_inside(P, bad, rows):
+    """Slots of any value: nothing outside the tensors is read or written, and the call returns."""
     e, n, k = 3, 40, 128
     ge = gen(1)
     qw, sc, qz = (t.to(DEV) for t in R.packed(ge, (e,), n, k, 128))
     x = tokens(ge, 4, k, F16).to(DEV)
     slots = torch.tensor([2 ** 31 - 1, -5, 7, 0, 3, -2 ** 31, 100, 8, 1] * 17, dtype=torch.int32)[:rows].to(DEV)
     out, whole = guarded(rows, n, F16)
+    out.fill_(-5)
     P.awq_moe_linear_w4a16(x, qw, sc, qz, torch.tensor(bad, dtype=torch.int32, device=DEV), slots, 2, out=out)
     torch.cuda.synchronize()
-    assert whole()
+    assert whole() and bool((out[:bad[0]] == -5).all() and (out[bad[-1]:] == -5).all() and out[bad[0]:bad[-1]].isfinite().all())
+
+
+@pytest.mark.parametrize("topk", [1, 3, 4, 32])
+@pytest.mark.parametrize("rows", [12, 300])
+def test_far_slots(P, topk, rows):
+    """Tokens up to the last of an x of nearly 4 GiB, slots up to 2^27."""
+    k, n, g = 64, 48, 64
+    t = min((1 << 31) // k - 1, (1 << 27) // topk)
+    ge = gen(topk)
+    p = R.packed(ge, (2,), n, k, g)
+    x = torch.empty(t, k, dtype=F16, device=DEV)
+    far = torch.unique(torch.cat((torch.arange(t - rows // 2, t), torch.randint(0, t, (rows,), generator=ge))))[-rows:]
+    slots = (far * topk + torch.randint(0, topk, far.shape, generator=ge)).int()
+    xs = tokens(ge, len(far), k, F16)
+    x[far.to(DEV)] = xs.to(DEV)
+    r = len(far)
+    y = P.awq_moe_linear_w4a16(x, *(q.to(DEV) for q in p), torch.tensor([0, r // 3, r], dtype=torch.int32, device=DEV),
+                               slots.to(DEV), topk, g=g).cpu()
+    for j, (a, z) in enumerate(((0, r // 3), (r // 3, r))):
+        v, bound = R.linear(xs[a:z], R.weights(*(q[j] for q in p), g), None, None, "none", False, None, F16)
+        R.check(y[a:z], v, bound, (topk, j))
 
 
 # ---------------------------------------------------------------- combination

@@ -156,6 +156,7 @@ struct ActArgs {
   int32_t e, topk, g, act, gated, bf;
   // the plan
   int32_t ng, nzw, ncol, ks, per;
+  uint32_t topk_inv;
 };
 // Scratch bytes, and whether one launch holds the call's work-groups (rows, x_rows, n, k, e, g,
 // gated, bf, inv and offsets are looked at, the pointers only for being null).

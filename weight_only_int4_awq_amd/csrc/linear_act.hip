@@ -20,16 +20,14 @@ struct Place {
   int col, sl;                 // column block, slice of K
 };
 
-// Rows of expert i (none behind the last), held within the rows there are whatever the array
-// says.  Every lane loads, so that loads of several runs of experts fly together.
-__device__ __forceinline__ void expert_rows(const ActArgs& a, int i, int& r0, int& n) {
-  const int cap = (int)a.rows;
+// Rows of expert i (none behind the last).  Every lane loads, so that loads of several runs of
+// experts fly together.  False: the offsets do not ascend within the rows there are.
+__device__ __forceinline__ bool expert_rows(const ActArgs& a, int i, int& r0, int& n) {
   const int j = i < a.e ? i : a.e - 1;
-  int s = a.offsets[j], t = a.offsets[j + 1];
-  s = s < 0 ? 0 : (s > cap ? cap : s);
-  t = t < s ? s : (t > cap ? cap : t);
+  const int s = a.offsets[j], t = a.offsets[j + 1];
   r0 = s;
   n = i < a.e ? t - s : 0;
+  return s >= 0 && t >= s && t <= (int)a.rows;
 }
 
 // x / y for 0 <= x < 2^24, 0 < y: exact in fp32 and one step.
@@ -53,13 +51,21 @@ struct Units {
 
   __device__ __forceinline__ int tiles_of(int rows_) const { return (rows_ + (1 << lt) - 1) >> lt; }
 
+  // How many there are; none under offsets that do not ascend within the rows (ascending ones
+  // share the rows out, so the sums below stay within the host's bound).
   __device__ __forceinline__ int count(const ActArgs& a, int lane) {
     if (!a.offsets) {
       tiles_all = tiles_of((int)a.rows);
     } else {
       tiles_all = 0;
+      bool ok = true;
 #pragma unroll
-      for (int j = 0; j < KEEP; ++j) expert_rows(a, 64 * j + lane, r0[j], n[j]);
+      for (int j = 0; j < KEEP; ++j) ok &= expert_rows(a, 64 * j + lane, r0[j], n[j]);
+      for (int b = 64 * KEEP; b < a.e; b += 64) {
+        int first, cnt;
+        ok &= expert_rows(a, b + lane, first, cnt);
+      }
+      if (__ballot(!ok)) return 0;
 #pragma unroll
       for (int j = 0; j < KEEP; ++j) {
         inc[j] = wave_scan(tiles_of(n[j])) + tiles_all;
@@ -140,15 +146,14 @@ __device__ __forceinline__ bool find_place(const ActArgs& a, int lane, int lt, P
   return true;
 }
 
-// The row of x that a slot reads, held within the rows there are whatever the plan says: the
-// quotient in fp32 is off by one at most below 2^24, which is mended.
+// The row of x that a slot reads, held within the rows there are whatever the plan says.
+// slot / topk as the upper half of slot * ceil(2^32 / topk): exact where slot times the
+// rounding of the second (below topk <= 32) stays below 2^32, so for all slots up to 2^27.
 __device__ __forceinline__ int slot_token(const ActArgs& a, int slot) {
   const uint32_t s = (uint32_t)(slot < 0 ? 0 : slot);
-  int t = (int)((float)s * __builtin_amdgcn_rcpf((float)a.topk));
-  const int rem = (int)(s - (uint32_t)t * (uint32_t)a.topk);
-  t += rem < 0 ? -1 : rem >= a.topk ? 1 : 0;
-  t = t < 0 ? 0 : t;
-  return t < (int)a.x_rows ? t : (int)a.x_rows - 1;
+  const uint32_t t = a.topk == 1 ? s : __umulhi(s, a.topk_inv);
+  const uint32_t last = (uint32_t)a.x_rows - 1;
+  return (int)(t < last ? t : last);
 }
 
 // ---------------------------------------------------------------- epilogue
@@ -229,8 +234,9 @@ __device__ __forceinline__ void tile_barrier() {
 
 // ---------------------------------------------------------------- few rows: weights streamed
 //
-// Up to TM rows of one expert times CB blocks of 16 weight rows; the W waves of a work-group
-// share K in runs of four 128-channel blocks.  A lane reads 16 bytes (32 codes) of one weight
+// Up to TM rows of one expert times two blocks of 16 weight rows (gated: 16 outputs' gate rows
+// and their up rows); the W <= 4 waves of a work-group share K in runs of four 128-channel
+// blocks.  A lane reads 16 bytes (32 codes) of one weight
 // row per block, straight into registers: every byte of the weights is read once and waits
 // for nothing but memory, all of a run asked for before the first is used.  The rows of a run
 // (512 channels; 256 where TM = 16) go through the wave's own LDS: scaled, rounded to fp16 and
@@ -239,6 +245,7 @@ __device__ __forceinline__ void tile_barrier() {
 // integers q - z enter exactly and the group's sum is scaled in fp32.  g = 32, 64: a lane's 32
 // codes are of one group and become fp16((q - z) D) before the product, as in the tiles.
 constexpr int kRun = 4;                              // blocks of a run
+constexpr int kCB = 2;                                // blocks of 16 weight rows
 template <int TM>
 struct StreamLds {
   static constexpr int SB = TM == 16 ? 2 : 4;        // blocks staged at a time
@@ -248,14 +255,14 @@ struct StreamLds {
 
 // Scales and zero points of a lane's codes in the blocks of a run, as they are loaded.
 // QUADS (g = 128, rows of a multiple of four groups): a run's scales are 8 aligned bytes.
-template <int G, int CB, bool QUADS>
+template <int G, bool QUADS>
 struct RunScales {
-  uint32_t s[CB][QUADS ? 2 : kRun];                  // fp16 bits, two to a word or one
-  uint32_t z[CB][G == 32 ? 2 : 1];                   // words of zero points
+  uint32_t s[kCB][QUADS ? 2 : kRun];                  // fp16 bits, two to a word or one
+  uint32_t z[kCB][G == 32 ? 2 : 1];                   // words of zero points
 };
 
-template <int G, int CB, int TM, bool QUADS>
-__global__ __launch_bounds__(512, 2) void linear_act_stream_kernel(const ActArgs a) {
+template <int G, int TM, bool QUADS>
+__global__ __launch_bounds__(256, 2) void linear_act_stream_kernel(const ActArgs a) {
   static_assert((TM == 8 || TM == 16) && (G == 128 || !QUADS), "");
   constexpr int SB = StreamLds<TM>::SB, STRIDE = StreamLds<TM>::STRIDE;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
@@ -266,8 +273,8 @@ __global__ __launch_bounds__(512, 2) void linear_act_stream_kernel(const ActArgs
   if (!find_place(a, lane, TM == 16 ? 4 : 3, p)) return;
   const int r = lane & 15, c = lane >> 4;
   const int k = (int)a.k;
-  // CB blocks: outputs col0 .. of the gate and the same of the up projection, or CB of outputs
-  const int half = a.gated ? CB / 2 : CB;
+  // outputs col0 .. of the gate and the same of the up projection, or two blocks of outputs
+  const int half = a.gated ? kCB / 2 : kCB;
   const int col0 = p.col * half * 16;
   // lane i: the row of x that row i of the tile reads; asked for first, the rows wait for it
   const int row_i = p.row0 + (r < p.rows ? r : p.rows - 1);
@@ -275,9 +282,9 @@ __global__ __launch_bounds__(512, 2) void linear_act_stream_kernel(const ActArgs
   const char* qb = reinterpret_cast<const char*>(a.qw + (int64_t)p.expert * a.nw * (a.k / 8));
   const char* sb = reinterpret_cast<const char*>(a.sc + (int64_t)p.expert * a.nw * a.ng);
   const char* zb = reinterpret_cast<const char*>(a.qz + (int64_t)p.expert * a.nw * a.nzw);
-  uint32_t row_w[CB];
+  uint32_t row_w[kCB];
 #pragma unroll
-  for (int cb = 0; cb < CB; ++cb) {
+  for (int cb = 0; cb < kCB; ++cb) {
     const int up = cb >= half;
     const uint32_t o = (uint32_t)(col0 + (up ? cb - half : cb) * 16 + r), n = (uint32_t)a.n;
     row_w[cb] = (o < n ? o : n - 1) + (up ? n : 0);
@@ -291,9 +298,9 @@ __global__ __launch_bounds__(512, 2) void linear_act_stream_kernel(const ActArgs
     const int kk = b * 128 + 32 * c;
     return kk < k ? kk : k - 32;
   };
-  auto load_w = [&](int b, uint4 (&w)[kRun][CB], RunScales<G, CB, QUADS>& rs) {
+  auto load_w = [&](int b, uint4 (&w)[kRun][kCB], RunScales<G, QUADS>& rs) {
 #pragma unroll
-    for (int cb = 0; cb < CB; ++cb) {                  // first: what returns in order is waited for in order
+    for (int cb = 0; cb < kCB; ++cb) {                  // first: what returns in order is waited for in order
       const uint32_t so = row_w[cb] * (uint32_t)(a.ng * 2), zo = row_w[cb] * (uint32_t)(a.nzw * 4);
       if constexpr (QUADS) {
         const uint2 v = *reinterpret_cast<const uint2*>(sb + (so + (uint32_t)b * 2));
@@ -319,7 +326,7 @@ __global__ __launch_bounds__(512, 2) void linear_act_stream_kernel(const ActArgs
     for (int i = 0; i < kRun; ++i) {
       const uint32_t off = (uint32_t)channel(b + i < b1 ? b + i : b1 - 1) / 2;
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb)
+      for (int cb = 0; cb < kCB; ++cb)
         w[i][cb] = *reinterpret_cast<const uint4*>(qb + (row_w[cb] * (uint32_t)(k / 2) + off));
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -359,17 +366,17 @@ __global__ __launch_bounds__(512, 2) void linear_act_stream_kernel(const ActArgs
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   };
 
-  floatx4_t acc[CB];
+  floatx4_t acc[kCB];
 #pragma unroll
-  for (int cb = 0; cb < CB; ++cb) acc[cb] = floatx4_t{};
+  for (int cb = 0; cb < kCB; ++cb) acc[cb] = floatx4_t{};
   const unsigned char* frag = stage + (TM == 16 ? r : r & 7) * STRIDE + c * 64;
-  auto block = [&](int b, int i, const uint4 (&w)[CB], const RunScales<G, CB, QUADS>& rs) {
+  auto block = [&](int b, int i, const uint4 (&w)[kCB], const RunScales<G, QUADS>& rs) {
     half8_t af[4];
 #pragma unroll
     for (int s = 0; s < 4; ++s) af[s] = *reinterpret_cast<const half8_t*>(frag + (i % SB) * 256 + s * 16);
     const bool in = G == 128 || b * 128 + 32 * c < k;
 #pragma unroll
-    for (int cb = 0; cb < CB; ++cb) {
+    for (int cb = 0; cb < kCB; ++cb) {
       // fields of the zero word: the block's group within the eight of a word
       const int gr = G == 128 ? b & 7 : G == 64 ? (2 * i + (c >> 1)) : (4 * (i & 1) + c);
       const uint32_t z = (rs.z[cb][G == 32 ? i >> 1 : 0] >> (4 * gr)) & 0xFu;
@@ -404,8 +411,8 @@ __global__ __launch_bounds__(512, 2) void linear_act_stream_kernel(const ActArgs
   };
 
   for (int b = b0; b < b1; b += kRun) {
-    uint4 w[kRun][CB], x[XL], iv = make_uint4(0, 0, 0, 0);
-    RunScales<G, CB, QUADS> rs;
+    uint4 w[kRun][kCB], x[XL], iv = make_uint4(0, 0, 0, 0);
+    RunScales<G, QUADS> rs;
     load_x(b, x, iv);
     load_w(b, w, rs);
     store_x(b, x, iv);
@@ -421,9 +428,9 @@ __global__ __launch_bounds__(512, 2) void linear_act_stream_kernel(const ActArgs
   __syncthreads();
   float* red = reinterpret_cast<float*>(lds);
 #pragma unroll
-  for (int cb = 0; cb < CB; ++cb)
+  for (int cb = 0; cb < kCB; ++cb)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) red[(wave * CB + cb) * 256 + j * 64 + lane] = acc[cb][j];
+    for (int j = 0; j < 4; ++j) red[(wave * kCB + cb) * 256 + j * 64 + lane] = acc[cb][j];
   __syncthreads();
   const int outs = half * 256;
   for (int i = tid; i < outs; i += blockDim.x) {
@@ -433,8 +440,8 @@ __global__ __launch_bounds__(512, 2) void linear_act_stream_kernel(const ActArgs
     if (row >= p.rows || o >= a.n) continue;
     float v = 0.0f, u = 0.0f;
     for (int w = 0; w < waves; ++w) {
-      v += red[w * CB * 256 + i];
-      if (a.gated) u += red[w * CB * 256 + outs + i];
+      v += red[w * kCB * 256 + i];
+      if (a.gated) u += red[w * kCB * 256 + outs + i];
     }
     const int64_t at = (int64_t)(p.row0 + row) * a.n + o;
     float f = finish(a, p.expert, o, v, u);
@@ -807,28 +814,13 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
   }
 }
 
-// Sums the K slices in slice order and finishes the outputs: a thread takes 4 of a row.
+// Sums the K slices of one matrix in slice order and finishes the outputs: a thread takes 4 of a row.
 __global__ __launch_bounds__(256) void linear_act_join_kernel(const ActArgs a) {
   const int64_t np = (a.n + 3) & ~3ll, pitch = a.gated ? 2 * np : np;
   const int64_t quads = np / 4;
   const int64_t unit = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t row = unit / quads;
   if (row >= a.rows) return;
-  int expert = 0;
-  if (a.offsets) {
-    int r0, cnt;
-    expert_rows(a, a.e - 1, r0, cnt);
-    if (row >= r0 + cnt) return;
-    if (a.bias) {                                     // the last expert that begins at or before the row
-      int lo = 0, hi = a.e - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (a.offsets[mid] <= row) lo = mid;
-        else hi = mid - 1;
-      }
-      expert = lo;
-    }
-  }
   const int64_t o = (unit - row * quads) * 4;
   float v[4] = {0, 0, 0, 0}, u[4] = {0, 0, 0, 0};
   for (int s = 0; s < a.ks; ++s) {
@@ -844,7 +836,7 @@ __global__ __launch_bounds__(256) void linear_act_join_kernel(const ActArgs a) {
   for (int j = 0; j < 4; ++j)
     if (o + j < a.n) {
       const int64_t at = row * a.n + o + j;
-      float f = finish(a, expert, o + j, v[j], u[j]);
+      float f = finish(a, 0, o + j, v[j], u[j]);
       if (a.res) f += act_bits(a.res[at], a.bf);
       a.y[at] = f2act(f, a.bf != 0);
     }
@@ -865,11 +857,24 @@ __global__ __launch_bounds__(256) void linear_act_prep_kernel(const ActArgs a, u
 }
 
 // ---------------------------------------------------------------- plan
-
+//
+// Chosen by the sizes the host knows; the rows of an expert are taken as their mean.
+// Microseconds of both sides near the borders (captured, weights cold):
+//   streaming or tiles, one matrix: 4096 x 4096, 17 / 64 rows 11.5 / 15.5 against 18.4 / 25.8; 1024 x 4096,
+//     64 / 128 rows 11.5 / 12.0 against 18 / 23; 28672 x 4096 (59 MB), 16 / 17 rows 28 against 33 / 38 (tiles
+//     28 with K-steps of 128): past 16 rows streaming reads the weights again for every 16, which pays up
+//     to some 36 MB in all.
+//   streaming or tiles, experts of 2048 <- 1408, mean of 9 rows: 39 against 34; of 1024 x 2 <- 2048, 4 rows
+//     74 against 82, 8 rows 103 against 95: the border is at 6.
+//   tiles of 32, 64, 128 rows, by the K-steps that 128-row tiles would take in all: 4096 x 4096, 96 rows (1024)
+//     21 / 24 / 28, 256 rows (2048) 30 / 27 / 29.5; 4096 <- 14336, 96 rows (3584) 44 / 38 / 35.
+//   K-steps of 128 or 64 in 32-row tiles: 8 experts of 14336 x 2 <- 4096, 16 rows each 153 against 170.
+//   K slices: a matrix of few tiles is split until 256 work-groups have one (a join follows); two K groups
+//     in a work-group where that leaves at most one to a CU.
 struct ActPlan {
   bool stream;
-  int cb, tm, waves, per;      // stream
-  int bm, bk, kg, ks;          // tile
+  int tm, waves, per;          // stream: rows of a tile, waves, blocks of a wave
+  int bm, bk, kg, ks;          // tile: rows, K-step, K groups, K slices
   bool prep;
   int64_t ncol, units;         // column blocks; upper bound of the units
   size_t x_bytes, part_bytes;
@@ -880,19 +885,18 @@ static size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 static ActPlan act_plan(const ActArgs& a) {
   ActPlan p{};
   const int64_t active = a.offsets ? (a.e < a.rows ? a.e : a.rows) : 1;
-  const int64_t avg = a.offsets ? (a.rows + a.e - 1) / a.e : a.rows;      // rows of a matrix, about
-  auto tiles = [&](int tm) { return a.offsets ? a.rows / tm + active : (a.rows + tm - 1) / tm; };
+  const int64_t avg = a.offsets ? (a.rows + a.e - 1) / a.e : a.rows;
+  auto tiles = [&](int rows) { return a.offsets ? a.rows / rows + active : (a.rows + rows - 1) / rows; };
+  const int64_t bytes = a.nw * (a.k / 2);              // packed weights of a matrix
   p.ks = 1;
   p.kg = 1;
-  const int64_t bytes = a.nw * (a.k / 2);            // of a matrix
-  if (a.offsets ? avg <= 12 : avg <= 16 || (avg <= 512 && (avg + 15) / 16 * bytes <= (36 << 20))) {
+  if (a.offsets ? avg <= 6 : avg <= 16 || (avg <= 512 && (avg + 15) / 16 * bytes <= (36 << 20))) {
     p.stream = true;
     p.tm = avg <= 8 ? 8 : 16;
-    p.cb = 2;
     const int nb = (int)((a.k + 127) / 128), runs = (nb + kRun - 1) / kRun;
-    p.per = (runs + 3) / 4 * kRun;                   // whole runs, up to 4 waves
+    p.per = (runs + 3) / 4 * kRun;                     // whole runs, up to 4 waves
     p.waves = (nb + p.per - 1) / p.per;
-    const int outs = (a.gated ? p.cb / 2 : p.cb) * 16;
+    const int outs = (a.gated ? kCB / 2 : kCB) * 16;
     p.ncol = (a.n + outs - 1) / outs;
     p.units = tiles(p.tm) * p.ncol;
     return p;
@@ -900,14 +904,14 @@ static ActPlan act_plan(const ActArgs& a) {
   const int outs = a.gated ? 128 : 256;
   p.ncol = (a.n + outs - 1) / outs;
   const int nk = (int)(a.k / 64);
-  const int64_t steps = tiles(128) * p.ncol * nk;    // K-steps of all 128-row tiles
+  const int64_t steps = tiles(128) * p.ncol * nk;
   p.bm = avg <= 32 || steps <= 1024 ? 32 : avg <= 64 || steps <= 3000 ? 64 : 128;
-  const int64_t t = tiles(p.bm) * p.ncol;
   p.bk = p.bm == 32 && a.g >= 64 && a.k % 128 == 0 ? 128 : 64;
+  const int64_t t = tiles(p.bm) * p.ncol;
   if (!a.offsets && t < 256 && a.rows <= 512) {
     int64_t ks = 256 / t;
     ks = ks > 16 ? 16 : ks;
-    ks = ks > nk / 2 ? nk / 2 : ks;
+    ks = ks > nk / 2 ? nk / 2 : ks;                    // two K-steps of 64 to a slice
     p.ks = ks < 1 ? 1 : (int)ks;
   }
   if (p.ks == 1 && t <= 256) p.kg = 2;
@@ -927,48 +931,40 @@ size_t linear_act_scratch_bytes(const ActArgs& a) {
 }
 
 bool linear_act_fits(const ActArgs& a) {
-  const ActPlan p = act_plan(a);
-  return p.units < (1 << 22) && a.x_rows * (a.k / 8) <= (1ll << 31) &&
-         a.rows * ((a.n + 3) / 4) <= (1ll << 31);
+  return act_plan(a).units < (1 << 22) && a.x_rows * (a.k / 8) <= (1ll << 31) && a.rows * ((a.n + 3) / 4) <= (1ll << 31);
 }
 
-template <int G, int CB, int TM>
+template <int G, int TM>
 static hipError_t run_stream(const ActArgs& a, const ActPlan& p, hipStream_t stream) {
-  const size_t x = (size_t)p.waves * StreamLds<TM>::WAVE, red = (size_t)p.waves * CB * 1024;
-  const size_t lds = x > red ? x : red;
-  auto go = [&](auto kernel) {
-    if (lds > 65536) {
-      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                               hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-      if (e != hipSuccess) return e;
-    }
-    hipLaunchKernelGGL(kernel, dim3((unsigned)((p.units + 7) / 8 * 8)), dim3(p.waves * 64), lds, stream, a);
-    return hipGetLastError();
-  };
+  const size_t x = (size_t)p.waves * StreamLds<TM>::WAVE, red = (size_t)p.waves * kCB * 1024;
+  const size_t lds = x > red ? x : red;                // 33 KB at most
+  const dim3 grid((unsigned)((p.units + 7) / 8 * 8)), block(p.waves * 64);
   if constexpr (G == 128) {
-    if (a.ng % 4 == 0) return go(linear_act_stream_kernel<G, CB, TM, true>);
+    if (a.ng % 4 == 0) {
+      hipLaunchKernelGGL((linear_act_stream_kernel<G, TM, true>), grid, block, lds, stream, a);
+      return hipGetLastError();
+    }
   }
-  return go(linear_act_stream_kernel<G, CB, TM, false>);
+  hipLaunchKernelGGL((linear_act_stream_kernel<G, TM, false>), grid, block, lds, stream, a);
+  return hipGetLastError();
 }
 
-template <int G, int KG, int BM, int BK = 64>
+template <int G, int BM, int BK>
 static hipError_t run_tile(const ActArgs& a, const ActPlan& p, hipStream_t stream) {
-  hipLaunchKernelGGL((linear_act_tile_kernel<G, KG, BM, BK>), dim3((unsigned)((p.units + 7) / 8 * 8)), dim3(256 * KG), 0,
-                     stream, a);
+  const dim3 grid((unsigned)((p.units + 7) / 8 * 8));
+  if (p.kg == 2) hipLaunchKernelGGL((linear_act_tile_kernel<G, 2, BM, BK>), grid, dim3(512), 0, stream, a);
+  else hipLaunchKernelGGL((linear_act_tile_kernel<G, 1, BM, BK>), grid, dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
 template <int G>
 static hipError_t run_act(const ActArgs& a, const ActPlan& p, hipStream_t stream) {
-  if (p.stream) {
-    return p.tm == 8 ? run_stream<G, 2, 8>(a, p, stream) : run_stream<G, 2, 16>(a, p, stream);
-  }
+  if (p.stream) return p.tm == 8 ? run_stream<G, 8>(a, p, stream) : run_stream<G, 16>(a, p, stream);
   if constexpr (G >= 64) {
-    if (p.bm == 32 && p.bk == 128) return p.kg == 2 ? run_tile<G, 2, 32, 128>(a, p, stream) : run_tile<G, 1, 32, 128>(a, p, stream);
+    if (p.bk == 128) return run_tile<G, 32, 128>(a, p, stream);
   }
-  if (p.bm == 32) return p.kg == 2 ? run_tile<G, 2, 32>(a, p, stream) : run_tile<G, 1, 32>(a, p, stream);
-  if (p.bm == 64) return p.kg == 2 ? run_tile<G, 2, 64>(a, p, stream) : run_tile<G, 1, 64>(a, p, stream);
-  return p.kg == 2 ? run_tile<G, 2, 128>(a, p, stream) : run_tile<G, 1, 128>(a, p, stream);
+  if (p.bm == 32) return run_tile<G, 32, 64>(a, p, stream);
+  return p.bm == 64 ? run_tile<G, 64, 64>(a, p, stream) : run_tile<G, 128, 64>(a, p, stream);
 }
 
 hipError_t launch_linear_act(const ActArgs& args, void* scratch, hipStream_t stream) {
@@ -979,6 +975,7 @@ hipError_t launch_linear_act(const ActArgs& args, void* scratch, hipStream_t str
   a.ncol = (int32_t)p.ncol;
   a.ks = p.ks;
   a.per = p.per;
+  a.topk_inv = (uint32_t)(((1ull << 32) + a.topk - 1) / a.topk);   // (not read for 1)
   char* base = (char*)scratch;
   if (p.prep) {
     uint16_t* xt = (uint16_t*)base;
@@ -989,10 +986,7 @@ hipError_t launch_linear_act(const ActArgs& args, void* scratch, hipStream_t str
     a.x = xt;
   }
   a.part = (float*)(base + p.x_bytes);
-  hipError_t e;
-  if (a.g == 128) e = run_act<128>(a, p, stream);
-  else if (a.g == 64) e = run_act<64>(a, p, stream);
-  else e = run_act<32>(a, p, stream);
+  const hipError_t e = a.g == 128 ? run_act<128>(a, p, stream) : a.g == 64 ? run_act<64>(a, p, stream) : run_act<32>(a, p, stream);
   if (e != hipSuccess || p.ks == 1) return e;
   const int64_t quads = ((a.n + 3) / 4) * a.rows;
   hipLaunchKernelGGL(linear_act_join_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, a);

@@ -332,9 +332,11 @@ static hipError_t route_npl(RouteArgs& a, hipStream_t stream) {
   const int threads = kRouteWaves * 64;
   if (route_small(a.t)) {
     const size_t lds = ((size_t)2 * a.t * a.topk + (size_t)(kRouteWaves + 2) * a.e + 1) * 4;
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(moe_route_small_kernel<NPL>),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if (e != hipSuccess) return e;
+    if (lds > 65536) {
+      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(moe_route_small_kernel<NPL>),
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+      if (e != hipSuccess) return e;
+    }
     hipLaunchKernelGGL(moe_route_small_kernel<NPL>, dim3(1), dim3(threads), lds, stream, a);
     return hipGetLastError();
   }
@@ -342,9 +344,11 @@ static hipError_t route_npl(RouteArgs& a, hipStream_t stream) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const size_t lds = ((size_t)(kRouteWaves + 3) * a.e + 1) * 4;
-  e = hipFuncSetAttribute(reinterpret_cast<const void*>(moe_place_kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
-                          (int)lds);
-  if (e != hipSuccess) return e;
+  if (lds > 65536) {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(moe_place_kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                            (int)lds);
+    if (e != hipSuccess) return e;
+  }
   hipLaunchKernelGGL(moe_place_kernel, dim3(a.chunks), dim3(threads), lds, stream, a);
   return hipGetLastError();
 }
