@@ -615,7 +615,9 @@ awq_status awq_attn_kv8_bf16(const awq_kv8_cache* cache, int64_t rows, int64_t m
  *   normal distribution; AWQ_ACT_GELU_TANH v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2.
  *   Sums, bias, activation, product and residual are fp32, rounded once to the
  *   type of y.  x_tilde = fp16_rn(x inv_s16) or x; bf16 x is rounded once to fp16
- *   first (see awq_linear_w4a16_bf16 for its range); weights enter the products
+ *   first (see awq_linear_w4a16_bf16 for its range).  For up to four rows of a matrix
+ *   what fp16_rn(x inv_s16) lost is added again, as an fp16 of its own (x_tilde within
+ *   2^-22; nothing where the product is not finite).  Weights enter the products
  *   exactly or as fp16_rn((q - z) D), by the number of rows and g.
  *   Before the activation the sum is within 5e-3 * max(|v_ref|, rms of the row of
  *   v_ref) of the float64 value.
@@ -680,9 +682,9 @@ awq_status awq_linear_w4a16_act_bf16(const uint16_t* x, const uint32_t* qweight,
  *   offsets and row_slot are device data and not checked on the host: whatever they
  *   hold, nothing outside the tensors is read or written.  Under offsets that do not
  *   ascend within 0 .. rows nothing is written; a slot outside those of x gives a row
- *   of x all the same.  Rows of y that no expert has are not written.  rows: what row_slot and y hold, at least offsets[e].  The
- *   number of rows and experts chooses between kernels; results are right for any
- *   split of the rows.
+ *   of x all the same.  Rows of y that no expert has are not written.  rows: what
+ *   row_slot and y hold, at least offsets[e].  The number of rows and experts chooses
+ *   between kernels; results are right for any split of the rows.
  *   workspace: awq_moe_linear_workspace_size(rows, x_rows, e, n, k, g, gated,
  *     inv_s16 != NULL, bf16) bytes (x_rows = rows without row_slot), 256-byte aligned.
  *   Limits: those of awq_linear_w4a16_act with rows for m, packed weights of one expert

@@ -128,6 +128,43 @@ def test_dense_extremes(P):
             assert bool((got[:, 5] == 0).all())
 
 
+@pytest.mark.parametrize("rows", [1, 3, 4])
+@pytest.mark.parametrize("k,g", [(1024, 128), (1152, 128), (1024, 64), (320, 64), (1024, 32), (96 * 2, 32)])
+def test_few_rows_keep_the_product_with_the_inverse_scale(P, rows, k, g):
+    """Even channels give (1 + 2^-10)^2, odd ones -(1 + 2^-9): equal once rounded to fp16, 2^-20 apart.
+
+    Sums of the rounded products are multiples of 2^-9 below 2^13 and those of what was lost multiples of
+    2^-20 below 1, row by row times a power of two: exact in any order, and so is the result."""
+    n, e = 33, 3
+    x, inv = torch.full((rows, k), 1 + 2.0 ** -9), torch.ones(k)
+    x[:, ::2], inv[::2] = 1 + 2.0 ** -10, 1 + 2.0 ** -10
+    x *= 2.0 ** torch.arange(rows)[:, None]                            # rows apart from each other
+    x, inv = x.half().to(DEV), inv.half().to(DEV)
+    qw = torch.full((e, n, k // 8), 0x79797979, dtype=torch.int32, device=DEV)      # q - z = 1, -1, 1 ..
+    sc = torch.ones(e, n, k // g, dtype=torch.float16, device=DEV)
+    zeros = torch.zeros(e, n, (k // g + 7) // 8 * 8, dtype=torch.int64)
+    zeros[..., :k // g] = 8
+    words = sum(zeros[..., j::8] << (4 * j) for j in range(8))
+    qz = torch.where(words >= 2 ** 31, words - 2 ** 32, words).int().to(DEV)
+    want = (k * 2.0 ** -21 * 2.0 ** torch.arange(rows, dtype=torch.float64))[:, None].expand(rows, n)
+    y = P.awq_linear_w4a16_act(x, qw[0], sc[0], qz[0], inv, g=g)
+    assert torch.equal(y.cpu().double(), want)
+    offsets = torch.tensor([0, 0, rows, rows], dtype=torch.int32, device=DEV)
+    y = P.awq_moe_linear_w4a16(x, qw, sc, qz, offsets, inv_s16=inv, g=g)
+    assert torch.equal(y.cpu().double(), want)
+
+
+def test_few_rows_whose_product_leaves_the_range(P):
+    """x inv_s beyond fp16 is infinite, with its sign, for its own row alone."""
+    k, n = 256, 17
+    x = torch.ones(4, k)
+    x[1, 3], x[2, 200] = 60000, -60000
+    qw = torch.full((n, k // 8), -0x66666667, dtype=torch.int32, device=DEV)        # q = 9
+    sc, qz = torch.full((n, 2), 0.25).half().to(DEV), torch.full((n, 1), 0x88, dtype=torch.int32, device=DEV)
+    y = P.awq_linear_w4a16_act(x.half().to(DEV), qw, sc, qz, torch.full((k,), 2.0).half().to(DEV)).cpu()
+    assert (y[1] == math.inf).all() and (y[2] == -math.inf).all() and (y[[0, 3]] == 128).all()
+
+
 # ---------------------------------------------------------------- routing
 
 def check_route(P, logits, topk, scoring, renorm, scale):

@@ -236,11 +236,13 @@ __device__ __forceinline__ void tile_barrier() {
 //
 // Up to TM rows of one expert times two blocks of 16 weight rows (gated: 16 outputs' gate rows
 // and their up rows); the W <= 4 waves of a work-group share K in runs of four 128-channel
-// blocks.  A lane reads 16 bytes (32 codes) of one weight
-// row per block, straight into registers: every byte of the weights is read once and waits
-// for nothing but memory, all of a run asked for before the first is used.  The rows of a run
+// blocks.  A lane reads 16 bytes (32 codes) of one weight row per block, straight into
+// registers: every byte of the weights is read once and waits for nothing but memory, all of a
+// run asked for before the first is used.  The rows of a run
 // (512 channels; 256 where TM = 16) go through the wave's own LDS: scaled, rounded to fp16 and
-// put in the order of the unpacked nibbles once, then read as operands.
+// put in the order of the unpacked nibbles once, then read as operands.  Up to four rows times
+// inv_s16 enter as a pair: fp16 rounding loses 2^-11 of a product, and rows 4 .. 7 of the 8-row
+// tile, else idle, hold what was lost (one token, gate and up of 2 x 14336 x 4096: 18.0 -> 18.3 us).
 // v_mfma_f32_16x16x32_f16, rows as A, weights as B.  g = 128: a block is one group, its
 // integers q - z enter exactly and the group's sum is scaled in fp32.  g = 32, 64: a lane's 32
 // codes are of one group and become fp16((q - z) D) before the product, as in the tiles.
@@ -252,6 +254,17 @@ struct StreamLds {
   static constexpr int STRIDE = SB * 256 + 16;       // bytes of a staged row: 16 rows on 64 banks
   static constexpr int WAVE = TM * STRIDE;
 };
+
+// What fp16 lost of hi = x s, element by element; nothing where hi left fp16's range.
+__device__ __forceinline__ uint4 remainder8(const half8_t x, const half8_t s, const half8_t hi) {
+  half8_t lo;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float h = (float)hi[i];
+    lo[i] = (_Float16)(__builtin_fabsf(h) <= 65504.0f ? __builtin_fmaf((float)x[i], (float)s[i], -h) : 0.0f);
+  }
+  return __builtin_bit_cast(uint4, lo);
+}
 
 // Scales and zero points of a lane's codes in the blocks of a run, as they are loaded.
 // QUADS (g = 128, rows of a multiple of four groups): a run's scales are 8 aligned bytes.
@@ -271,6 +284,7 @@ __global__ __launch_bounds__(256, 2) void linear_act_stream_kernel(const ActArgs
   const int waves = blockDim.x >> 6;
   Place p;
   if (!find_place(a, lane, TM == 16 ? 4 : 3, p)) return;
+  const bool low = TM == 8 && a.inv && p.rows <= 4;    // rows 4 .. 7: what rounding rows 0 .. 3 lost
   const int r = lane & 15, c = lane >> 4;
   const int k = (int)a.k;
   // outputs col0 .. of the gate and the same of the up projection, or two blocks of outputs
@@ -352,16 +366,24 @@ __global__ __launch_bounds__(256, 2) void linear_act_stream_kernel(const ActArgs
   };
   auto store_x = [&](int b, const uint4 (&x)[XL], const uint4& iv) {
     const bool in = b * 128 + 8 * xc < k;            // the last block may be half a one (g < 128)
+    auto store = [&](int i, const uint4& v, bool part) {
+      // channels in the order of the unpacked nibbles: (0, 4), (1, 5), (2, 6), (3, 7)
+      uint4 u = make_uint4(__builtin_amdgcn_perm(v.z, v.x, 0x05040100u), __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
+                           __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u));
+      if (!in) u = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(stage + ((SB == 4 ? i : 2 * i + xh) + (part ? 4 : 0)) * STRIDE + xc * 16) = u;
+    };
 #pragma unroll
     for (int i = 0; i < XL; ++i)
       if ((SB == 4 ? i : 2 * i) < p.rows) {
         uint4 v = act8_h(x[i], a.bf != 0);
-        if (a.inv) v = __builtin_bit_cast(uint4, (half8_t)(__builtin_bit_cast(half8_t, v) * __builtin_bit_cast(half8_t, iv)));
-        // channels in the order of the unpacked nibbles: (0, 4), (1, 5), (2, 6), (3, 7)
-        uint4 u = make_uint4(__builtin_amdgcn_perm(v.z, v.x, 0x05040100u), __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
-                             __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u));
-        if (!in) u = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(stage + (SB == 4 ? i : 2 * i + xh) * STRIDE + xc * 16) = u;
+        if (a.inv) {
+          const half8_t xv = __builtin_bit_cast(half8_t, v), sv = __builtin_bit_cast(half8_t, iv);
+          const half8_t hi = xv * sv;
+          v = __builtin_bit_cast(uint4, hi);
+          if (low) store(i, remainder8(xv, sv, hi), true);
+        }
+        store(i, v, false);
       }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   };
@@ -440,8 +462,13 @@ __global__ __launch_bounds__(256, 2) void linear_act_stream_kernel(const ActArgs
     if (row >= p.rows || o >= a.n) continue;
     float v = 0.0f, u = 0.0f;
     for (int w = 0; w < waves; ++w) {
-      v += red[w * kCB * 256 + i];
-      if (a.gated) u += red[w * kCB * 256 + outs + i];
+      const float* s = red + w * kCB * 256 + i;
+      v += s[0];
+      if (a.gated) u += s[outs];
+      if (low) {                                       // row + 4: lane + 16
+        v += s[16];
+        if (a.gated) u += s[outs + 16];
+      }
     }
     const int64_t at = (int64_t)(p.row0 + row) * a.n + o;
     float f = finish(a, p.expert, o, v, u);
