@@ -623,7 +623,8 @@ awq_status awq_attn_kv8_bf16(const awq_kv8_cache* cache, int64_t rows, int64_t m
  *   v_ref) of the float64 value.
  *   x [m][k], residual, y [m][n], bias [n] ([2 n] gated): fp16 (bf16); bias and
  *   residual may be NULL; residual may be y.  x, inv_s16 and qweight 16-byte aligned,
- *   scales and qzeros 4-byte aligned.  workspace:
+ *   scales and qzeros 4-byte aligned (scales are read in whole words: of an odd number
+ *   of them also the two bytes behind the last, unused).  workspace:
  *   awq_linear_act_workspace_size(m, n, k, g, gated, inv_s16 != NULL, bf16) bytes,
  *   256-byte aligned (NULL if that is 0).
  *   Limits: g in {32, 64, 128}; k % g == 0; k % 64 == 0; k <= 2^23; 0 <= m <= 2^27; packed

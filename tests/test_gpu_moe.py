@@ -489,6 +489,73 @@ def test_two_streams(P):
             assert torch.equal(y, a) and all(torch.equal(u, w) for u, w in zip(r, ra))
 
 
+@pytest.mark.parametrize("t", [2, 120])
+def test_two_threads(P, t):
+    """The whole layer from two threads at once, a stream each, with the binding's own workspaces."""
+    import threading
+    ge = gen(40 + t)
+    e, topk, k, n = 6, 2, 256, 384
+    gate_up = tuple(q.to(DEV) for q in R.packed(ge, (e,), 2 * n, k, 128))
+    down = tuple(q.to(DEV) for q in R.packed(ge, (e,), k, n, 128))
+    xs = [tokens(ge, t, k, BF16).to(DEV) for _ in range(2)]
+    logits = [torch.randn(t, e, generator=ge).to(DEV) for _ in range(2)]
+    want = [block(P, x, v, gate_up, down, topk, BF16) for x, v in zip(xs, logits)]
+    torch.cuda.synchronize()
+    got, failed = [[], []], []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(20):
+                    got[i].append(block(P, xs[i], logits[i], gate_up, down, topk, BF16))
+            s.synchronize()
+        except BaseException as err:                  # noqa: BLE001
+            failed.append(err)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not failed, failed
+    for ys, w in zip(got, want):
+        assert len(ys) == 20 and all(torch.equal(y, w) for y in ys)
+
+
+def test_two_graphs_with_one_workspace(P):
+    """Captured with the same scratch and replayed in turn on one stream: each what it gives alone."""
+    ge = gen(50)
+    m, k, n, e = 100, 512, 768, 40
+    p = tuple(q.to(DEV) for q in R.packed(ge, (), n, k, 128))
+    inv = torch.exp(0.4 * torch.randn(k, generator=ge)).half().to(DEV)
+    ws = torch.zeros(max(P.awq_linear_act_workspace_size(m, n, k, 128, False, True, True),
+                         P.awq_moe_route_workspace_size(m, e)), dtype=torch.uint8, device=DEV)
+    xs = [torch.zeros(m, k, dtype=BF16, device=DEV) for _ in range(2)]
+    logits = [torch.zeros(m, e, device=DEV) for _ in range(2)]
+
+    def step(x, v, ws):
+        return (P.awq_linear_w4a16_act_bf16(x, *p, inv, act="silu", workspace=ws), *P.awq_moe_route(v, 4, workspace=ws))
+
+    step(xs[0], logits[0], ws)
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for x, v in zip(xs, logits):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(step(x, v, ws))
+        graphs.append(graph)
+    for _ in range(4):
+        for x, v in zip(xs, logits):
+            x.copy_(tokens(ge, m, k, BF16))
+            v.copy_(torch.randn(m, e, generator=ge))
+        for graph in graphs:
+            graph.replay()
+        for out, x, v in zip(outs, xs, logits):
+            assert all(torch.equal(a, b) for a, b in zip(out, step(x, v, None)))
+        torch.cuda.synchronize()
+
+
 def test_residual_in_place_and_far_offsets(P):
     """residual is out; and rows of y and x beyond 2^31 elements of a tensor."""
     ge = gen(6)

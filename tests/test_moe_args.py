@@ -140,3 +140,15 @@ def test_binding_refuses_host_tensors_and_names():
                  lambda: P.awq_moe_combine(x, [1.0], sr)):
         with pytest.raises((TypeError, ValueError)):
             call()
+
+
+def test_binding_refuses_groups_of_nothing():
+    torch = pytest.importorskip("torch")
+    import weight_only_int4_awq_amd as P
+    x = torch.zeros(2, 64, dtype=torch.float16)
+    qw, sc, qz = torch.zeros(8, 8, dtype=torch.int32), torch.zeros(8, 1, dtype=torch.float16), torch.zeros(8, 1, dtype=torch.int32)
+    for g in (0, -64):
+        with pytest.raises(ValueError, match="g must"):
+            P.awq_linear_w4a16_act(x, qw, sc, qz, g=g)
+        with pytest.raises(ValueError, match="g must"):
+            P.awq_moe_linear_w4a16(x, qw[None], sc[None], qz[None], torch.zeros(2, dtype=torch.int32), g=g)

@@ -819,6 +819,8 @@ def _linear_act(x, qweight, scales, qzeros, inv_s16, bias, act, gated, residual,
     f16, i32 = torch.float16, torch.int32
     dt = torch.bfloat16 if bf else f16
     act, gated = _act_code(act, gated)
+    if g < 1:
+        raise ValueError(f"g must be 32, 64 or 128 (got {g})")
     try:
         dev = x.get_device()
         m, k = x.shape
@@ -928,6 +930,8 @@ def _moe_linear(x, qweight, scales, qzeros, offsets, row_slot, topk, inv_s16, bi
     f16, i32 = torch.float16, torch.int32
     dt = torch.bfloat16 if bf else f16
     act, gated = _act_code(act, gated)
+    if g < 1:
+        raise ValueError(f"g must be 32, 64 or 128 (got {g})")
     try:
         dev = x.get_device()
         t, k = x.shape
