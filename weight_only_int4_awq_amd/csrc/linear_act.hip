@@ -723,40 +723,10 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
   wait_copies<0>();                                   // the look-ahead has landed before the LDS is used again
   tile_barrier();
 
-  // ---- two K groups: the second hands its sums over through LDS
-  if constexpr (KG == 2) {
-    float* hand = reinterpret_cast<float*>(ring) + wv * (BMB * BNB * 16 * 64);
-    if (kgrp == 1) {
-#pragma unroll
-      for (int bm = 0; bm < BMB; ++bm)
-#pragma unroll
-        for (int bn = 0; bn < BNB; ++bn)
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<float4*>(hand + (((bm * BNB + bn) * 4 + q) * 64 + lane) * 4) =
-                make_float4(acc[bm][bn][4 * q], acc[bm][bn][4 * q + 1], acc[bm][bn][4 * q + 2], acc[bm][bn][4 * q + 3]);
-    }
-    __syncthreads();
-    if (kgrp == 1) return;
-#pragma unroll
-    for (int bm = 0; bm < BMB; ++bm)
-#pragma unroll
-      for (int bn = 0; bn < BNB; ++bn)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float4 v = *reinterpret_cast<const float4*>(hand + (((bm * BNB + bn) * 4 + q) * 64 + lane) * 4);
-          acc[bm][bn][4 * q] += v.x;
-          acc[bm][bn][4 * q + 1] += v.y;
-          acc[bm][bn][4 * q + 2] += v.z;
-          acc[bm][bn][4 * q + 3] += v.w;
-        }
-  }
-
   // ---- epilogue: value i of lane l in block (bm, bn) is row 8 (i / 4) + 4 (l / 32) + i % 4, column l % 32.
-  // 32 rows at a time through the wave's own LDS: fp32, 8 neighbouring outputs to a lane.
   const int outs = a.gated ? 32 : 64;                 // outputs of the wave
   const int64_t wcol = col0 + wv * outs;
-  if (a.ks > 1) {                                     // a slice's sums, [slice][row][pitch]: columns in output order
+  if (KG == 1 && a.ks > 1) {                          // a slice's sums, [slice][row][pitch]: columns in output order
     const int64_t np = (a.n + 3) & ~3ll, pitch = a.gated ? 2 * np : np;
     float* dst = a.part + ((int64_t)p.sl * a.rows + p.row0) * pitch;
 #pragma unroll
@@ -771,13 +741,6 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
         }
     return;
   }
-  constexpr int ER = 68;                              // floats of a staged row: two lane halves 16 banks apart
-  // (two K groups: behind the hand-over area, which other waves may still read)
-  constexpr int kHand = KG == 2 ? 4 * BMB * BNB * 16 * 64 : 0;
-  constexpr bool kBehind = (kHand + 4 * 32 * ER) * 4 <= (int)sizeof(ring);
-  static_assert(kCopies * (ST - 1) < 64, "the wait counter");
-  static_assert(kBehind || 32 * ER <= BMB * BNB * 16 * 64, "else within the wave's own part of it");
-  float* ep = reinterpret_cast<float*>(ring) + (kBehind ? kHand + wv * 32 * ER : wv * (BMB * BNB * 16 * 64));
   auto al = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
   const bool vec = a.n % 8 == 0 && al(a.y) && al(a.res);
   const uint16_t* bias = a.bias ? a.bias + (int64_t)p.expert * a.nw : nullptr;
@@ -791,17 +754,78 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
     bv[j] = bias ? act_bits(bias[oj], a.bf) : 0.0f;
     bu[j] = bias && a.gated ? act_bits(bias[a.n + oj], a.bf) : 0.0f;
   }
+  // ---- two K groups: each finishes 16 rows of every 32 and hands the sums of the others over
+  // through LDS.  The staging below lies behind that area, or within the part that only the
+  // wave itself reads.
+  constexpr int ROWS = KG == 2 ? 16 : 32, NV = ROWS / 2;   // rows and values of a block that a wave finishes
+  const int row_g = KG == 2 ? 16 * kgrp : 0;
+  constexpr int kMine = BMB * BNB * 8 * 64;           // floats handed to a wave
+  if constexpr (KG == 2) {
+    float* hand = reinterpret_cast<float*>(ring) + (wv * 2 + (1 - kgrp)) * kMine;
+#pragma unroll
+    for (int bm = 0; bm < BMB; ++bm)
+#pragma unroll
+      for (int bn = 0; bn < BNB; ++bn)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float give[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float l = acc[bm][bn][4 * q + j], h = acc[bm][bn][8 + 4 * q + j];
+            give[j] = kgrp ? l : h;
+            acc[bm][bn][4 * q + j] = kgrp ? h : l;
+          }
+          *reinterpret_cast<float4*>(hand + (((bm * BNB + bn) * 2 + q) * 64 + lane) * 4) =
+              make_float4(give[0], give[1], give[2], give[3]);
+        }
+    __syncthreads();
+    hand = reinterpret_cast<float*>(ring) + (wv * 2 + kgrp) * kMine;
+#pragma unroll
+    for (int bm = 0; bm < BMB; ++bm)
+#pragma unroll
+      for (int bn = 0; bn < BNB; ++bn)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const float4 v = *reinterpret_cast<const float4*>(hand + (((bm * BNB + bn) * 2 + q) * 64 + lane) * 4);
+          acc[bm][bn][4 * q] += v.x;
+          acc[bm][bn][4 * q + 1] += v.y;
+          acc[bm][bn][4 * q + 2] += v.z;
+          acc[bm][bn][4 * q + 3] += v.w;
+        }
+  }
+
+  // ---- 32 rows at a time through the wave's own LDS: fp32, 8 neighbouring outputs to a lane
+  constexpr int ER = 68;                              // floats of a staged row: two lane halves 16 banks apart
+  constexpr int kHand = KG == 2 ? 8 * kMine : 0;
+  constexpr bool kBehind = (kHand + 4 * KG * ROWS * ER) * 4 <= (int)sizeof(ring);
+  static_assert(kCopies * (ST - 1) < 64, "the wait counter");
+  static_assert(kBehind || ROWS * ER <= kMine, "else within the part that only the wave reads");
+  float* ep = reinterpret_cast<float*>(ring) +
+              (kBehind ? kHand + wave * ROWS * ER : (wv * 2 + kgrp) * kMine);
+  constexpr int IT = ROWS / 8;                        // turns of a block, not gated
 #pragma unroll
   for (int bm = 0; bm < BMB; ++bm) {
+    const int first = bm * 32 + row_g;
+    uint32_t rv[IT][4] = {};
+    if (vec && a.res) {                               // a block's residual in flight together
+#pragma unroll
+      for (int t = 0; t < IT; ++t) {
+        const int row = first + t * (64 >> lsh) + (lane >> lsh);
+        if (t < ROWS >> (6 - lsh) && row < p.rows && o < a.n) {
+          const uint4 r = *reinterpret_cast<const uint4*>(a.res + (int64_t)(p.row0 + row) * a.n + o);
+          rv[t][0] = r.x; rv[t][1] = r.y; rv[t][2] = r.z; rv[t][3] = r.w;
+        }
+      }
+    }
 #pragma unroll
     for (int bn = 0; bn < BNB; ++bn)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) ep[(8 * (i / 4) + 4 * bc + (i % 4)) * ER + bn * 32 + bj] = acc[bm][bn][i];
+      for (int i = 0; i < NV; ++i) ep[(8 * (i / 4) + 4 * bc + (i % 4)) * ER + bn * 32 + bj] = acc[bm][bn][i];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll 1
-    for (int q = 0; q < 32; q += 64 >> lsh) {
-      const int row = q + (lane >> lsh);
-      if (bm * 32 + row < p.rows && o < a.n) {
+    for (int t = 0; t < ROWS >> (6 - lsh); ++t) {
+      const int row = t * (64 >> lsh) + (lane >> lsh);
+      if (first + row < p.rows && o < a.n) {
         const float4 lo = *reinterpret_cast<const float4*>(ep + row * ER + c8);
         const float4 hi = *reinterpret_cast<const float4*>(ep + row * ER + c8 + 4);
         float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
@@ -814,11 +838,16 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[j] *= u[j] + bu[j];
         }
-        const int64_t at = (int64_t)(p.row0 + bm * 32 + row) * a.n + o;
+        const int64_t at = (int64_t)(p.row0 + first + row) * a.n + o;
         if (vec) {
           if (a.res) {
-            const uint4 rv = *reinterpret_cast<const uint4*>(a.res + at);
-            const uint32_t ru[4] = {rv.x, rv.y, rv.z, rv.w};
+            uint32_t ru[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              ru[q] = rv[0][q];
+#pragma unroll
+              for (int i = 1; i < IT; ++i) ru[q] = t == i ? rv[i][q] : ru[q];
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] += act_bits((uint16_t)(j & 1 ? ru[j / 2] >> 16 : ru[j / 2]), a.bf);
           }
