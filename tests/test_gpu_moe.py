@@ -105,6 +105,13 @@ def test_dense_tiles(P, m, n, k, g, gated):
     dense(P, m, n, k, g, (F16, BF16)[i // 64 % 2], ("none", "silu")[gated], gated, bool(i // 32 % 2), bool(i // 128 % 2), not gated)
 
 
+@pytest.mark.parametrize("m,n,k,g,gated", [(600, 1000, 1024, 128, False), (530, 260, 960, 32, True), (600, 2040, 4096, 64, False),
+                                            (600, 2040, 8192, 128, False), (513, 1000, 7104, 64, True)])
+def test_dense_split_beyond_512_rows(P, m, n, k, g, gated):
+    """Matrices of few tiles, split along K: tiles of 32, 64 and 128 rows."""
+    dense(P, m, n, k, g, BF16 if gated else F16, "gelu" if gated else "none", gated, True, True, True)
+
+
 def test_dense_extremes(P):
     """Activations at their ends, scales of zero and NaN, inputs with inf and NaN: as in float64, and only where they belong."""
     k, n, g = 128, 40, 128

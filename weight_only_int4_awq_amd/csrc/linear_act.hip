@@ -6,8 +6,11 @@
 //
 // Rows of expert i are offsets[i] .. offsets[i + 1] - 1 and use its weights; the row counts
 // are device data, so work-groups find their expert and rows themselves and the grid is an
-// upper bound.  bf16 activations are rounded once to fp16.  Sums, bias, activation and
-// residual are fp32 with one rounding at the end.
+// upper bound.  Roundings: bf16 activations once to fp16 (exact within fp16's normal range:
+// the matrix instructions take one type, and the weights' integers need more than bf16's 8
+// bits once scaled); x inv_s once to fp16 (by pairs without loss where a few rows stream, see
+// there); weights exactly or as fp16((q - z) D), 2^-11 of a weight, as in the other linears of
+// many rows.  Sums, bias, activation and residual are fp32 with one rounding at the end.
 #include "decode_common.h"
 #include "moe_common.h"
 
@@ -246,6 +249,13 @@ __device__ __forceinline__ void tile_barrier() {
 // v_mfma_f32_16x16x32_f16, rows as A, weights as B.  g = 128: a block is one group, its
 // integers q - z enter exactly and the group's sum is scaled in fp32.  g = 32, 64: a lane's 32
 // codes are of one group and become fp16((q - z) D) before the product, as in the tiles.
+// Bound by the weights' bytes: one token on two of 8 experts (122 MB) 28.0 us, 4.4 TB/s; dense
+// gate and up of one token (61 MB) 14.4 us, 4.2; 64 tokens on 128 experts (256 MB) 71 us, 3.6:
+// there 8000 work-groups of one run to a wave each pay for their plan, their rows and their
+// first load (captured, weights cold: 78 us, without the plan 69, without rows too 54, the
+// weight loads alone 52).
+// Two blocks of 16 weight rows and up to 4 waves: four blocks or 8 waves leave too few work-
+// groups or registers (experts of 1 token 36 to 46 us against 33, captured, weights cold).
 constexpr int kRun = 4;                              // blocks of a run
 constexpr int kCB = 2;                                // blocks of 16 weight rows
 template <int TM>
@@ -479,13 +489,23 @@ __global__ __launch_bounds__(256, 2) void linear_act_stream_kernel(const ActArgs
 
 // ---------------------------------------------------------------- many rows: tiles
 //
-// BM rows x 256 weight rows of one expert, K-step 64, 4 waves side by side along the weight
+// BM rows x 256 weight rows of one expert, K-steps of BK, 4 waves side by side along the weight
 // rows, each BM x 64 in 32 x 32 blocks of v_mfma_f32_32x32x16_f16; gated, a wave's two blocks
 // are 32 outputs' gate rows and their up rows, so the product of the two needs no exchange.
+// KG = 2: a second set of 4 waves takes every other K-step, where there are few tiles.
 // Copies from global memory to LDS in a ring of three stages, two K-steps ahead, with explicit
 // waits (the compiler sees neither); weights become fp16((q - z) D) in registers.  Rows are
 // read in channel order (gathered by the copies' own addresses), so nibbles are unpacked in
 // pairs of neighbours: a byte permute and a mask per pair.
+// 128-row tiles are bound by the matrix pipe and the card's power: 4096 tokens by twos on 8 experts
+// (1924 GFLOP) 1.99 ms, 968 TFLOP/s where a large library product reaches 1054; 2048 rows of
+// 4096 <- 14336 258 us, 930 TFLOP/s, and 21 us for the rows' conversion.  Exact integers in the
+// product would take a second set of sums (128 registers), scaled per group.  32-row tiles are
+// bound by how the cache takes their copies: 64 weight rows a copy are 32 to 64 lines, and a
+// K-step is there when the wave needs it only if enough work-groups share a CU (300 tokens on 60
+// experts, 102 MB: 41 us; 333 rows of 4099 <- 1088: 18 us, a K-step of 64 1.2 us).  Fewer
+// registers by a rolled ring (23.2 against 22.2 us), two stages and a third work-group (53
+// against 48.6) or four and five stages brought nothing.
 constexpr int kTileBN = 256;
 constexpr int kTileStages = 3;
 constexpr int tile_stage_bytes(int bm, int bk) { return bm * bk * 2 + kTileBN * bk / 2; }
@@ -923,10 +943,13 @@ __global__ __launch_bounds__(256) void linear_act_prep_kernel(const ActArgs a, u
 //   streaming or tiles, experts of 2048 <- 1408, mean of 9 rows: 39 against 34; of 1024 x 2 <- 2048, 4 rows
 //     74 against 82, 8 rows 103 against 95: the border is at 6.
 //   tiles of 32, 64, 128 rows, by the K-steps that 128-row tiles would take in all: 4096 x 4096, 96 rows (1024)
-//     21 / 24 / 28, 256 rows (2048) 30 / 27 / 29.5; 4096 <- 14336, 96 rows (3584) 44 / 38 / 35.
+//     21 / 24 / 28, 256 rows (2048) 30 / 27 / 29.5; 4096 <- 14336, 96 rows (3584) 44 / 38 / 35; between
+//     4096 <- 4096, 520 rows (5120) - / 50 / 46 and 1024 rows (8192) - / 58 / 62 they change places again.
 //   K-steps of 128 or 64 in 32-row tiles: 8 experts of 14336 x 2 <- 4096, 16 rows each 153 against 170.
-//   K slices: a matrix of few tiles is split until 256 work-groups have one (a join follows); two K groups
-//     in a work-group where that leaves at most one to a CU.
+//   K slices: a matrix of few tiles is split until 256 work-groups have one (a join follows, of 34 MB of
+//     sums at most); two K groups in a work-group where that leaves at most one to a CU.  Split against not:
+//     4096 <- 14336, 1024 rows (128 tiles) 152 against 200; 4096 <- 4096, 520 / 1024 rows 46 / 61 against
+//     66 / 69; 1024 <- 4096, 2048 rows 44 against 70.
 struct ActPlan {
   bool stream;
   int tm, waves, per;          // stream: rows of a tile, waves, blocks of a wave
@@ -964,7 +987,7 @@ static ActPlan act_plan(const ActArgs& a) {
   p.bm = avg <= 32 || steps <= 1024 ? 32 : avg <= 64 || steps <= 3000 ? 64 : 128;
   p.bk = p.bm == 32 && a.g >= 64 && a.k % 128 == 0 ? 128 : 64;
   const int64_t t = tiles(p.bm) * p.ncol;
-  if (!a.offsets && t < 256 && a.rows <= 512) {
+  if (!a.offsets && t < 256) {
     int64_t ks = 256 / t;
     ks = ks > 16 ? 16 : ks;
     ks = ks > nk / 2 ? nk / 2 : ks;                    // two K-steps of 64 to a slice
