@@ -218,6 +218,24 @@ def test_route(P, t, e, topk):
             check_route(P, y, topk, scoring, renorm, 1.5)
 
 
+@pytest.mark.parametrize("dt", [torch.float32, F16, BF16])
+@pytest.mark.parametrize("e,topk", [(1, 1), (7, 3), (8, 8), (16, 16), (24, 5), (63, 16), (100, 16), (100, 17), (120, 2), (128, 16), (128, 32), (129, 4),
+                                    (200, 8), (256, 16), (256, 17), (257, 3), (400, 8), (511, 5), (512, 16)])
+def test_route_four_tokens_to_a_wave(P, dt, e, topk):
+    """Many tokens of up to 512 experts: whole and part rows of lanes, both widths of loads, ties, closed and NaN."""
+    ge = gen(e + topk)
+    for t, away in ((49, 0), (77, 1), (200, 0)):
+        x = torch.randint(-6, 7, (t, e), generator=ge).to(dt) / 2                      # many ties
+        x[torch.rand(t, e, generator=ge) < 0.3] = -math.inf
+        x[3], x[t - 1] = -math.inf, math.nan
+        x[5, e // 2] = math.nan
+        x[7, e - 1] = 40.0
+        flat = torch.zeros(t * e + away, dtype=dt, device=DEV)                         # one element past 16 bytes
+        flat[away:] = x.to(DEV).flatten()
+        for i, scoring in enumerate(("softmax", "softmax", "sigmoid", "sigmoid")):
+            check_route(P, flat[away:].view(t, e), topk, scoring, bool(i & 1), 1.5)
+
+
 def test_route_many(P):
     """More tokens than work-groups hold at 64 each: chunks of several rounds, every expert of one popular."""
     ge = gen(2)

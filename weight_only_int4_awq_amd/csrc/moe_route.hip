@@ -10,12 +10,12 @@
 //
 // What bounds it: the logits are read once and 16 bytes a slot written; up to some
 // thousand tokens that is nothing beside the launches and the chain of one token
-// (topk times a maximum over the lanes).  One wave takes a token; a work-group of 16
+// (topk times a maximum over the lanes).  One wave takes a token, or four; a work-group of 16
 // waves takes a chunk of tokens and leaves the chunk's number of slots of each expert;
 // the second launch adds the chunks before its own and places its slots.  Up to
 // kRouteSmall tokens one work-group does both in one launch.  Measured on the GPU: one token
-// of 8 experts 3.1 us; 8191 tokens, 8 of 128 experts 8.5 + 6.3 us (3.1 MB: 0.6 us of bytes; the
-// choices are 8 maxima over the lanes, one after the other, for each of the 2 tokens a wave has).
+// of 8 experts 3.1 us; 8191 tokens, 8 of 128 experts 5.4 + 6.4 us (3.1 MB: 0.6 us of bytes).
+// Chunks of 64 tokens: 13.0 us for both against 12.7, and 11.4 against 10.0 for 500 tokens.
 #include "moe_common.h"
 
 namespace awq {
@@ -34,6 +34,7 @@ struct RouteArgs {
   int32_t* slot_row;
   int32_t* counts;                    // [chunks][e]
   int32_t chunk, chunks;              // tokens of a work-group, work-groups
+  bool vec;                           // rows of logits are 16-byte chunks
 };
 
 // A float's bits in the order of the values; -0 as +0, NaN as the lowest.
@@ -125,6 +126,117 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, const float (&v)
   if (a.renorm || a.scoring == 0) w = sum > 0.0f || sum != sum ? w / sum : 0.0f;
   w = id >= 0 ? w * a.scale : 0.0f;
   if (__ballot(bad)) w = __builtin_nanf("");
+}
+
+// ---- four tokens to a wave, one to each row of 16 lanes: up to 512 experts and 16 choices.
+// Lane q of a row holds experts K q .. K q + K - 1.  With K = 8 a choice takes some 50 vector
+// instructions for four tokens, 40 for one in the form above, and it is their issue that bounds
+// many tokens (both launches, 8 choices: 8191 tokens of 128 experts 12.7 us against 15.5, 30000
+// 22.9 against 36.6; 8191 of 256 experts 17.6 against 22.1, of 512 27.0 against 33.3).
+
+#define AWQ_ROW_ALL(NAME, TYPE, OP)                                                                  \
+  __device__ __forceinline__ TYPE NAME(TYPE x) {                                                           \
+    auto other = [](TYPE v, auto ctrl) {                                                                   \
+      return __builtin_bit_cast(TYPE, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v),           \
+                                                                  decltype(ctrl)::value, 0xf, 0xf, true)); \
+    };                                                                                                     \
+    TYPE o = other(x, std::integral_constant<int, 0x128>{});                                               \
+    x = OP;                                                                                                \
+    o = other(x, std::integral_constant<int, 0x124>{});                                                    \
+    x = OP;                                                                                                \
+    o = other(x, std::integral_constant<int, 0x122>{});                                                    \
+    x = OP;                                                                                                \
+    o = other(x, std::integral_constant<int, 0x121>{});                                                    \
+    return OP;                                                                                             \
+  }
+// over the 16 lanes of a row (rotations by 8, 4, 2, 1), in every lane; sums alike in every lane
+AWQ_ROW_ALL(row_max, uint32_t, x > o ? x : o)
+AWQ_ROW_ALL(row_min, uint32_t, x < o ? x : o)
+AWQ_ROW_ALL(row_sum, float, x + o)
+#undef AWQ_ROW_ALL
+
+// Experts K q .. K q + K - 1 of token t; -inf behind the last.
+template <int K>
+__device__ __forceinline__ void load_row(const RouteArgs& a, int64_t t, int q, float (&v)[K]) {
+  const int64_t at = t * a.e + K * q;
+#pragma unroll
+  for (int i = 0; i < K; ++i) v[i] = -__builtin_inff();
+  if (!a.vec) {
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+      if (K * q + i < a.e) v[i] = load_logit(a, at + i);
+    return;
+  }
+#pragma unroll
+  for (int c = 0; c < K; c += 8) {
+    if (K * q + c >= a.e) continue;                   // experts are a multiple of 8 here
+    if (a.type == 0) {
+      const float* p = reinterpret_cast<const float*>(a.logits) + at + c;
+      const float4 l = *reinterpret_cast<const float4*>(p), h = *reinterpret_cast<const float4*>(p + 4);
+      v[c] = l.x; v[c + 1] = l.y; v[c + 2] = l.z; v[c + 3] = l.w;
+      v[c + 4] = h.x; v[c + 5] = h.y; v[c + 6] = h.z; v[c + 7] = h.w;
+    } else {
+      const uint4 r = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.logits) + at + c);
+      const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint16_t b = (uint16_t)(i & 1 ? u[i / 2] >> 16 : u[i / 2]);
+        v[c + i] = a.type == 1 ? h2f(b) : bf2f(b);
+      }
+    }
+  }
+}
+
+// The tokens of a wave's four rows, as route_token.  Lane q < topk of a row ends with choice q.
+template <int K>
+__device__ __forceinline__ void route_rows(const RouteArgs& a, const float (&v)[K], int lane, int& id, float& w) {
+  const int q = lane & 15;
+  uint32_t key[K];
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    key[i] = order_key(v[i]);
+    bad |= v[i] != v[i];
+  }
+  auto value = [](uint32_t k) {
+    return __builtin_bit_cast(float, k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+  };
+  auto largest = [&] {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < K; ++i) m = m > key[i] ? m : key[i];
+    return row_max(m);
+  };
+  float sum = 0.0f, mine = 0.0f;
+  id = -1;
+  w = 0.0f;
+  uint32_t best = largest();
+  const float top = value(best);
+  if (a.scoring == 0 && !a.renorm) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+      if (key[i] > kClosedKey) s += expf(value(key[i]) - top);
+    sum = row_sum(s);
+  }
+  for (int j = 0; j < a.topk && __ballot(best > kClosedKey); ++j) {
+    uint32_t at = 0xFFFFu;
+#pragma unroll
+    for (int i = K - 1; i >= 0; --i) at = key[i] == best ? (uint32_t)(K * q + i) : at;
+    at = row_min(at);
+#pragma unroll
+    for (int i = 0; i < K; ++i) key[i] = at == (uint32_t)(K * q + i) ? 0u : key[i];
+    if (q == j && best > kClosedKey) {
+      id = (int)at;
+      mine = value(best);
+    }
+    best = largest();
+  }
+  if (id >= 0) w = a.scoring == 0 ? expf(mine - top) : 1.0f / (1.0f + expf(-mine));
+  if (a.renorm) sum = row_sum(w);
+  if (a.renorm || a.scoring == 0) w = sum > 0.0f || sum != sum ? w / sum : 0.0f;
+  w = id >= 0 ? w * a.scale : 0.0f;
+  if ((__ballot(bad) >> (lane & 48)) & 0xFFFF) w = __builtin_nanf("");
 }
 
 // Slots [s0, s1) of the chunk, wave by wave in runs of 64: their ranks among the slots
@@ -250,6 +362,30 @@ __global__ __launch_bounds__(kRouteWaves * 64) void moe_route_kernel(const Route
   for (int i = tid; i < a.e; i += kRouteWaves * 64) a.counts[(int64_t)blockIdx.x * a.e + i] = hist[i];
 }
 
+// The same by rows of lanes.
+template <int K>
+__global__ __launch_bounds__(kRouteWaves * 64) void moe_route_rows_kernel(const RouteArgs a) {
+  __shared__ int hist[16 * K];
+  const int tid = threadIdx.x, lane = tid & 63, q = lane & 15;
+  const int t0 = blockIdx.x * a.chunk, t1 = t0 + a.chunk < a.t ? t0 + a.chunk : a.t;
+  if (tid < a.e) hist[tid] = 0;
+  __syncthreads();
+  for (int t = t0 + (tid >> 4); t - (lane >> 4) < t1; t += kRouteWaves * 4) {
+    float v[K];
+    load_row<K>(a, t < t1 ? t : t1 - 1, q, v);
+    int id;
+    float w;
+    route_rows<K>(a, v, lane, id, w);
+    if (t < t1 && q < a.topk) {
+      a.ids[(int64_t)t * a.topk + q] = id;
+      a.weights[(int64_t)t * a.topk + q] = w;
+      if (id >= 0) atomicAdd(&hist[id], 1);
+    }
+  }
+  __syncthreads();
+  if (tid < a.e) a.counts[(int64_t)blockIdx.x * a.e + tid] = hist[tid];
+}
+
 // Places the slots of chunk blockIdx.x.  LDS: hist [waves][e], before [e], total [e], start [e + 1]
 __global__ __launch_bounds__(kRouteWaves * 64) void moe_place_kernel(const RouteArgs a) {
   extern __shared__ int lds[];
@@ -342,7 +478,13 @@ static hipError_t route_npl(RouteArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL(moe_route_small_kernel<NPL>, dim3(1), dim3(threads), lds, stream, a);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL(moe_route_kernel<NPL>, dim3(a.chunks), dim3(threads), (size_t)a.e * 4, stream, a);
+  bool rows = false;
+  if constexpr (NPL <= 8) {
+    rows = a.topk <= 16;
+    constexpr int K = NPL <= 2 ? 8 : 4 * NPL;         // experts of a lane
+    if (rows) hipLaunchKernelGGL(moe_route_rows_kernel<K>, dim3(a.chunks), dim3(threads), 0, stream, a);
+  }
+  if (!rows) hipLaunchKernelGGL(moe_route_kernel<NPL>, dim3(a.chunks), dim3(threads), (size_t)a.e * 4, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const size_t lds = ((size_t)(kRouteWaves + 3) * a.e + 1) * 4;
@@ -359,7 +501,8 @@ hipError_t launch_moe_route(const void* logits, int32_t type, int64_t t, int32_t
                             bool renorm, float scale, int32_t* ids, float* weights, int32_t* offsets,
                             int32_t* row_slot, int32_t* slot_row, void* scratch, hipStream_t stream) {
   RouteArgs a{logits, type, (int32_t)t, e, topk, scoring, renorm ? 1 : 0, scale, ids, weights, offsets, row_slot,
-              slot_row, (int32_t*)scratch, 0, 0};
+              slot_row, (int32_t*)scratch, 0, 0, false};
+  a.vec = e % 8 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15) == 0;
   a.chunk = route_chunk_tokens(t);
   a.chunks = (int)((t + a.chunk - 1) / a.chunk);
   if (e <= 64) return route_npl<1>(a, stream);
