@@ -615,10 +615,10 @@ awq_status awq_attn_kv8_bf16(const awq_kv8_cache* cache, int64_t rows, int64_t m
  *   normal distribution; AWQ_ACT_GELU_TANH v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2.
  *   Sums, bias, activation, product and residual are fp32, rounded once to the
  *   type of y.  x_tilde = fp16_rn(x inv_s16) or x; bf16 x is rounded once to fp16
- *   first (see awq_linear_w4a16_bf16 for its range).  For up to four rows of a matrix
- *   what fp16_rn(x inv_s16) lost is added again, as an fp16 of its own (x_tilde within
- *   2^-22; nothing where the product is not finite).  Weights enter the products
- *   exactly or as fp16_rn((q - z) D), by the number of rows and g.
+ *   first (see awq_linear_w4a16_bf16 for its range).  Where m <= 4, what
+ *   fp16_rn(x inv_s16) lost is added again, as an fp16 of its own (x_tilde within
+ *   max(2^-22 |x inv_s16|, 2^-25); nothing where the product is not finite).  Weights
+ *   enter the products exactly or as fp16_rn((q - z) D), by the number of rows and g.
  *   Before the activation the sum is within 5e-3 * max(|v_ref|, rms of the row of
  *   v_ref) of the float64 value.
  *   x [m][k], residual, y [m][n], bias [n] ([2 n] gated): fp16 (bf16); bias and
@@ -685,7 +685,9 @@ awq_status awq_linear_w4a16_act_bf16(const uint16_t* x, const uint32_t* qweight,
  *   ascend within 0 .. rows nothing is written; a slot outside those of x gives a row
  *   of x all the same.  Rows of y that no expert has are not written.  rows: what
  *   row_slot and y hold, at least offsets[e].  The number of rows and experts chooses
- *   between kernels; results are right for any split of the rows.
+ *   between kernels; results are right for any split of the rows.  All rows of an expert
+ *   are rounded alike: as pairs (see awq_linear_w4a16_act) those of an expert with up to
+ *   four, in calls of up to six rows to an expert on average, and no others.
  *   workspace: awq_moe_linear_workspace_size(rows, x_rows, e, n, k, g, gated,
  *     inv_s16 != NULL, bf16) bytes (x_rows = rows without row_slot), 256-byte aligned.
  *   Limits: those of awq_linear_w4a16_act with rows for m, packed weights of one expert

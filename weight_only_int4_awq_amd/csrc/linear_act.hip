@@ -20,6 +20,7 @@ namespace awq {
 
 struct Place {
   int expert, row0, rows;      // rows of the tile: row0 .. row0 + rows - 1, at least one
+  int all;                     // rows of the expert
   int col, sl;                 // column block, slice of K
 };
 
@@ -131,6 +132,7 @@ struct Units {
     }
     p.col = tn;
     p.row0 += tm << lt;
+    p.all = rows;
     rows -= tm << lt;
     p.rows = rows < 1 << lt ? rows : 1 << lt;
   }
@@ -243,9 +245,10 @@ __device__ __forceinline__ void tile_barrier() {
 // registers: every byte of the weights is read once and waits for nothing but memory, all of a
 // run asked for before the first is used.  The rows of a run
 // (512 channels; 256 where TM = 16) go through the wave's own LDS: scaled, rounded to fp16 and
-// put in the order of the unpacked nibbles once, then read as operands.  Up to four rows times
-// inv_s16 enter as a pair: fp16 rounding loses 2^-11 of a product, and rows 4 .. 7 of the 8-row
-// tile, else idle, hold what was lost (one token, gate and up of 2 x 14336 x 4096: 18.0 -> 18.3 us).
+// put in the order of the unpacked nibbles once, then read as operands.  An expert's rows times
+// inv_s16, if there are four or fewer, enter as a pair: fp16 rounding loses 2^-11 of a product,
+// and rows 4 .. 7 of the 8-row tile, else idle, hold what was lost (one token, gate and up of
+// 2 x 14336 x 4096: 18.0 -> 18.3 us).
 // v_mfma_f32_16x16x32_f16, rows as A, weights as B.  g = 128: a block is one group, its
 // integers q - z enter exactly and the group's sum is scaled in fp32.  g = 32, 64: a lane's 32
 // codes are of one group and become fp16((q - z) D) before the product, as in the tiles.
@@ -294,7 +297,8 @@ __global__ __launch_bounds__(256, 2) void linear_act_stream_kernel(const ActArgs
   const int waves = blockDim.x >> 6;
   Place p;
   if (!find_place(a, lane, TM == 16 ? 4 : 3, p)) return;
-  const bool low = TM == 8 && a.inv && p.rows <= 4;    // rows 4 .. 7: what rounding rows 0 .. 3 lost
+  // rows 4 .. 7: what rounding rows 0 .. 3 lost; by the expert's rows, so that all of them are rounded alike
+  const bool low = TM == 8 && a.inv && p.all <= 4;
   const int r = lane & 15, c = lane >> 4;
   const int k = (int)a.k;
   // outputs col0 .. of the gate and the same of the up projection, or two blocks of outputs
