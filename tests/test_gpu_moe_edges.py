@@ -52,3 +52,73 @@ def test_a_row_among_its_expert(P, k, g, dt):
     for j, c in enumerate(counts):
         mine = y[at[j]:at[j + 1]]
         assert bool((mine == (few if c <= 4 else many)).all()), (j, c)
+
+
+# by tiles of 32, 64 and 128 rows, with two K groups, K slices and neither
+TILES = [(m, n, k, g) for m, n, k in ((700, 2050, 768), (2000, 4096, 192), (2000, 4096, 768), (2100, 8192, 768),
+                                      (1100, 8192, 512), (1000, 2048, 1536), (640, 4096, 1920)) for g in (128, 64, 32)]
+# streaming with 8 and 16 rows
+STREAMS = [(m, n, k, 128) for m, n, k in ((1, 48, 384), (4, 48, 512), (8, 72, 384), (16, 40, 512), (40, 40, 384),
+                                          (300, 520, 512), (300, 2050, 512))]
+
+
+def scattered_scales(ge, n, ng):
+    """Scales of all mantissas over 2^-10 .. 2^-1, every seventh of them zero, and a row of zeros."""
+    sc = (2.0 ** (-1 - 9 * torch.rand(n, ng, generator=ge))).half()
+    sc[torch.rand(n, ng, generator=ge) < 1 / 7] = 0
+    sc[3] = 0
+    return sc
+
+
+@pytest.mark.parametrize("m,n,k,g", TILES + STREAMS)
+@pytest.mark.parametrize("dt", [F16, BF16])
+def test_weights_enter_exactly(P, m, n, k, g, dt):
+    """Codes of one value in every group times a scale that leaves no code but 0, 1, 2, 4 and 8 exact in
+    fp16, rows above zero: what a weight's rounding loses adds up.  The residual takes away the result
+    rounded to its type, so that what is left shows sums off by 2^-15.
+
+    Products are exact in fp32; sums of k of them are off by k 2^-24 of the sum (k + 8 with joins), every
+    change of scale by a quotient (2^-23 + 2^-24) and a product (2^-24) more: 2^-22 a group."""
+    k = -(-k // g) * g
+    ng = k // g
+    ge = gen(m + n + k + g)
+    code = torch.randint(1, 16, (n, ng), generator=ge)
+    words = sum(code.repeat_interleave(g // 8, 1) << (4 * i) for i in range(8))
+    qw = torch.where(words >= 2 ** 31, words - 2 ** 32, words).int()
+    sc = scattered_scales(ge, n, ng)
+    qz = torch.zeros(n, -(-ng // 8), dtype=torch.int32)
+    x = (1 + torch.rand(m, k, generator=ge)).to(dt)
+    v = x.double().view(m, ng, g).sum(2) @ (code.double() * sc.double()).t()
+    res = (-v).to(dt)
+    fn = P.awq_linear_w4a16_act_bf16 if dt is BF16 else P.awq_linear_w4a16_act
+    y = fn(x.to(DEV), qw.to(DEV), sc.to(DEV), qz.to(DEV), residual=res.to(DEV), g=g)
+    left = v + res.double()
+    R.check(y, left, ((k + 8) * 2.0 ** -24 + ng * 2.0 ** -22) * v + R.HALF[dt] * 1.01 * left.abs() + 2.0 ** -25, (m, n, k, g, dt))
+    assert bool((y[:, 3] == 0).all())
+
+
+@pytest.mark.parametrize("g", [128, 64, 32])
+@pytest.mark.parametrize("m", [3, 5, 12, 40, 140, 600])
+@pytest.mark.parametrize("inv", [False, True])
+def test_rows_with_infinities(P, m, g, inv):
+    """As in float64: infinite with the weight's sign, NaN where the weight is zero; other rows as ever."""
+    n, k = 200, 384
+    ge = gen(m + g)
+    qw, sc, qz = R.packed(ge, (), n, k, g)
+    sc[5] = 0
+    sc[:9, (k - 40) // g] = 0                                           # the group of the last row's infinity
+    w = R.weights(qw, sc, qz, g)
+    x = torch.randn(m, k, generator=ge).half()
+    x[1, 7], x[m - 1, k - 40], x[0, 130] = torch.inf, -torch.inf, torch.nan
+    iv = torch.full((k,), 0.5).half() if inv else None
+    for act in ("none", "silu", "gelu"):
+        y = P.awq_linear_w4a16_act(x.to(DEV), qw.to(DEV), sc.to(DEV), qz.to(DEV), None if iv is None else iv.to(DEV),
+                                   act=act, g=g).cpu()
+        v, bound = R.linear(x, w, iv, None, act, False, None, F16)
+        odd = [0, 1, m - 1]
+        for i in odd:
+            assert torch.equal(y[i].isnan(), v[i].isnan()) and torch.equal(y[i] == torch.inf, v[i] == torch.inf), (i, act)
+            assert torch.equal(y[i] == -torch.inf, v[i] == -torch.inf), (i, act)
+        rest = [i for i in range(m) if i not in odd]
+        assert len(rest) == m - 3
+        R.check(y[rest], v[rest], bound[rest], (m, g, act))

@@ -9,8 +9,8 @@
 // upper bound.  Roundings: bf16 activations once to fp16 (exact within fp16's normal range:
 // the matrix instructions take one type, and the weights' integers need more than bf16's 8
 // bits once scaled); x inv_s once to fp16 (by pairs without loss where a few rows stream, see
-// there); weights exactly or as fp16((q - z) D), 2^-11 of a weight, as in the other linears of
-// many rows.  Sums, bias, activation and residual are fp32 with one rounding at the end.
+// there); weights exactly, but where rows stream with g = 32 or 64: as fp16((q - z) D), 2^-11 of
+// a weight.  Sums, bias, activation and residual are fp32 with one rounding at the end.
 #include "decode_common.h"
 #include "moe_common.h"
 
@@ -498,13 +498,21 @@ __global__ __launch_bounds__(256, 2) void linear_act_stream_kernel(const ActArgs
 // are 32 outputs' gate rows and their up rows, so the product of the two needs no exchange.
 // KG = 2: a second set of 4 waves takes every other K-step, where there are few tiles.
 // Copies from global memory to LDS in a ring of three stages, two K-steps ahead, with explicit
-// waits (the compiler sees neither); weights become fp16((q - z) D) in registers.  Rows are
-// read in channel order (gathered by the copies' own addresses), so nibbles are unpacked in
-// pairs of neighbours: a byte permute and a mask per pair.
+// waits (the compiler sees neither).  Rows are read in channel order (gathered by the copies' own
+// addresses), so nibbles are unpacked in pairs of neighbours: a byte permute and a mask per pair.
+//
+// The products take the integers q - z, exact in fp16, and the sums are kept in units of the
+// group's scale: where a group ends they are multiplied by its scale over the next one's (fp32: a
+// reciprocal and two products, 2^-22 a group), and at the end by the last one's.  A second set of
+// sums, scaled and added per group, would take 128 registers that 128 rows do not have.  A scale
+// of zero keeps the unit and takes the codes' bits instead (an infinity in x times it is NaN, as it
+// should be).  What it costs against weights rounded to fp16((q - z) D), 1.7e-4 of a result: g = 128
+// 4096 tokens on 8 experts 1975 -> 1993 us, down projection of 2048 rows 269 -> 277, 700 x 4096 x 4096
+// (one wave to a SIMD, nothing to cover it) 46 -> 50, 8 experts of 16 rows 158 -> 145; g = 64, gate
+// and up of 2048 rows 468 -> 482; g = 32 491 -> 570.
 // 128-row tiles are bound by the matrix pipe and the card's power: 4096 tokens by twos on 8 experts
 // (1924 GFLOP) 1.99 ms, 968 TFLOP/s where a large library product reaches 1054; 2048 rows of
-// 4096 <- 14336 258 us, 930 TFLOP/s, and 21 us for the rows' conversion.  Exact integers in the
-// product would take a second set of sums (128 registers), scaled per group.  32-row tiles are
+// 4096 <- 14336 258 us, 930 TFLOP/s, and 21 us for the rows' conversion.  32-row tiles are
 // bound by how the cache takes their copies: 64 weight rows a copy are 32 to 64 lines, and a
 // K-step is there when the wave needs it only if enough work-groups share a CU (300 tokens on 60
 // experts, 102 MB: 41 us; 333 rows of 4099 <- 1088: 18 us, a K-step of 64 1.2 us).  Fewer
@@ -538,7 +546,9 @@ __device__ __forceinline__ PairConsts pair_consts() {
 
 template <int G, int KG, int BM, int BK>
 __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_kernel(const ActArgs a) {
-  static_assert(BK == 64 || (BK == 128 && G >= 64), "a lane's half of a K-step is of one group");
+  static_assert(BK == 64 || (BK == 128 && G >= 64), "a word of scales holds those of a K-step");
+  constexpr int NG = BK > G ? BK / G : 1;             // groups of a K-step, one after the other
+  constexpr int QS = NG > 1 && G == 32 ? 2 : 4;       // a lane's half of 16 QS channels: QS words, as many sub-steps
   constexpr int BN = kTileBN;
   constexpr int CH = BK / 8, BCH = BK / 32, NS = BK / 16;   // 16-byte chunks of a row and of a weight row, sub-steps
   constexpr int BMB = BM / 32, BNB = 2;
@@ -637,40 +647,58 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
 #pragma unroll
     for (int j = 0; j < BNB; ++j) acc[i][j] = floatx16_t{};
   const PairConsts pc = pair_consts();
-  // ---- fragments: rows from chunk (CH / 2 (lane / 32) + s) ^ swizzle(row); words of column j, half c
+  // ---- fragments: sub-step s takes 8 channels of each half of the lanes, of one group:
+  // from 16 QS (s / QS) + 8 QS (lane / 32) + 8 (s % QS) on, rows and words alike
   const int bj = lane & 31, bc = lane >> 5;
   uint32_t a_base[BMB];
 #pragma unroll
   for (int bm = 0; bm < BMB; ++bm) {
     const int row = bm * 32 + bj;
-    a_base[bm] = (uint32_t)(row * BK * 2 + ((CH / 2 * bc) ^ a_swz(row)) * 16);
+    a_base[bm] = (uint32_t)(row * BK * 2 + ((QS * bc) ^ a_swz(row)) * 16);
   }
   uint32_t b_off[BNB], s_off[BNB], s_par[BNB];
 #pragma unroll
   for (int bn = 0; bn < BNB; ++bn) {
     const int lcol = wv * 64 + bn * 32 + bj;
-    b_off[bn] = (uint32_t)(kA + lcol * (BK / 2) + ((BCH / 2 * bc) ^ b_swz(lcol)) * 16);
+    b_off[bn] = (uint32_t)(kA + lcol * (BK / 2) + (QS == 4 ? (bc ^ b_swz(lcol)) * 16 : b_swz(lcol) * 16 + 8 * bc));
     s_off[bn] = (uint32_t)(lcol * 4);
     s_par[bn] = ((uint32_t)(weight_row(lcol) * a.ng) + s_odd) & 1;
   }
   struct BSet {
     uint4 wb[BNB][BCH / 2];
-    half2_t dd[BNB], off[BNB];
+    half2_t off[NG][BNB];
+    uint32_t d[BNB];                                  // scales of the K-step's groups, in halves
+    uint32_t mask[BNB];                               // one group: no bits of the codes where its scale is zero
   };
   // what a wave copied itself needs only its own wait: the step's words, scale and zero
   auto prep = [&](int rnd, int st, BSet& r) {
     const unsigned char* s = ring_g + st * KG * kStage;
-    const int g0 = (kt0 + KG * rnd + kgrp) * BK / G, grp = ((kt0 + KG * rnd + kgrp) * BK + BK / 2 * bc) / G;
+    const int g0 = (kt0 + KG * rnd + kgrp) * BK / G;
 #pragma unroll
     for (int bn = 0; bn < BNB; ++bn) {
 #pragma unroll
-      for (int h = 0; h < BCH / 2; ++h) r.wb[bn][h] = *reinterpret_cast<const uint4*>(s + (b_off[bn] ^ (uint32_t)(16 * h)));
+      for (int h = 0; h < BCH / 2; ++h) {
+        if constexpr (QS == 4) {
+          r.wb[bn][h] = *reinterpret_cast<const uint4*>(s + (b_off[bn] ^ (uint32_t)(32 * h)));
+        } else {
+          const uint2 l = *reinterpret_cast<const uint2*>(s + b_off[bn]);
+          const uint2 u = *reinterpret_cast<const uint2*>(s + (b_off[bn] ^ 16u));
+          r.wb[bn][h] = make_uint4(l.x, l.y, u.x, u.y);
+        }
+      }
       const uint32_t sw = *reinterpret_cast<const uint32_t*>(words_g + s_place(g0) * BN * 4 + s_off[bn]);
       const uint32_t zw = *reinterpret_cast<const uint32_t*>(words_g + (2 + ((g0 >> 3) & 1)) * BN * 4 + s_off[bn]);
-      const uint32_t d = (sw >> (16 * ((s_par[bn] + (uint32_t)grp) & 1))) & 0xFFFFu;
-      const uint32_t z = (zw >> (4 * (grp & 7))) & 0xFu;
-      r.dd[bn] = __builtin_bit_cast(half2_t, d | (d << 16));
-      r.off[bn] = __builtin_bit_cast(half2_t, 0xD400E400u + z + (z << 20));       // (-1024 - z, -64 - z)
+#pragma unroll
+      for (int e = 0; e < NG; ++e) {
+        const int grp = g0 + e;
+        const uint32_t d = (sw >> (16 * ((s_par[bn] + (uint32_t)grp) & 1))) & 0xFFFFu;
+        const uint32_t z = (zw >> (4 * (grp & 7))) & 0xFu;
+        r.off[e][bn] = __builtin_bit_cast(half2_t, 0xD400E400u + z + (z << 20));     // (-1024 - z, -64 - z)
+        const bool none = (d & 0x7FFFu) == 0;         // a scale of zero: its weights are zeros
+        r.d[bn] = e ? r.d[bn] | d << 16 : d;
+        r.mask[bn] = none ? 0u : pc.mask;
+        r.off[e][bn] = none ? half2_t{} : r.off[e][bn];
+      }
     }
   };
   auto dequant = [&](const BSet& r, int s, half8_t (&out)[BNB]) {
@@ -678,17 +706,37 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
     for (int bn = 0; bn < BNB; ++bn) {
       const uint4 wv4 = r.wb[bn][s >> 2];
       const uint32_t w = (s & 3) == 0 ? wv4.x : (s & 3) == 1 ? wv4.y : (s & 3) == 2 ? wv4.z : wv4.w;
+      const int e = NG > 1 ? s / QS : 0;
+      // two groups: by the offset, which is zero nowhere else (another mask would take registers that 128 rows lack)
+      const uint32_t mask = NG == 1 ? r.mask[bn] : __builtin_bit_cast(uint32_t, r.off[e][bn]) == 0 ? 0u : pc.mask;
       uint32_t q[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t u = __builtin_amdgcn_perm(w, pc.magic, pc.sel[j]) & pc.mask;
-        q[j] = __builtin_bit_cast(uint32_t, (half2_t)((__builtin_bit_cast(half2_t, u) + r.off[bn]) * r.dd[bn]));
+        const uint32_t u = __builtin_amdgcn_perm(w, pc.magic, pc.sel[j]) & mask;
+        q[j] = __builtin_bit_cast(uint32_t, (half2_t)(__builtin_bit_cast(half2_t, u) + r.off[e][bn]));
       }
       out[bn] = __builtin_bit_cast(half8_t, make_uint4(q[0], q[1], q[2], q[3]));
     }
   };
   BSet rs[2];
   half8_t bq[BNB];
+  float unit[BNB];                                    // what a one in the sums stands for
+#pragma unroll
+  for (int bn = 0; bn < BNB; ++bn) unit[bn] = 1.0f;
+  // the sums in units of the next group's scale
+  auto rescale = [&](const BSet& r, int e) {
+#pragma unroll
+    for (int bn = 0; bn < BNB; ++bn) {
+      const float d = h2f((uint16_t)(r.d[bn] >> (16 * e)));
+      const float next = d == 0.0f ? unit[bn] : d;
+      const float ratio = unit[bn] * __builtin_amdgcn_rcpf(next);
+      unit[bn] = next;
+#pragma unroll
+      for (int bm = 0; bm < BMB; ++bm)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[bm][bn][i] *= ratio;
+    }
+  };
   // Round P in stage P % ST: meet, then sub-steps of 16 channels.  Each sub-step's products run
   // while the next one's weights are unpacked; the copies of round P + ST - 1 go out after the
   // first sub-step, into the stage round P - 1 used; the last sub-step waits for the wave's
@@ -699,11 +747,17 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
     tile_barrier();
     if (KG == 1 || kt0 + KG * rnd + kgrp < kt1) {
       const unsigned char* cur = ring_g + st * KG * kStage;
+      {
+        const int kt = kt0 + KG * rnd + kgrp;
+        if (NG > 1 || KG * BK >= G || rnd == 0 || kt * BK / G != (kt - KG) * BK / G) rescale(r, 0);
+        if constexpr (G == 32 && KG == 1) __builtin_amdgcn_sched_barrier(0);   // else 128 rows lack 5 registers
+      }
       half8_t af[BMB];
 #pragma unroll
       for (int bm = 0; bm < BMB; ++bm) af[bm] = *reinterpret_cast<const half8_t*>(cur + a_base[bm]);
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
+        if (NG > 1 && s == QS) rescale(r, 1);
         half8_t bqn[BNB];
         if (s < NS - 1) {
           dequant(r, s + 1, bqn);
@@ -717,7 +771,7 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
 #pragma unroll
           for (int bn = 0; bn < BNB; ++bn)
             acc[bm][bn] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[bm], bq[bn], acc[bm][bn], 0, 0, 0);
-          if (s < NS - 1) af[bm] = *reinterpret_cast<const half8_t*>(cur + (a_base[bm] ^ (uint32_t)(16 * (s + 1))));
+          if (s < NS - 1) af[bm] = *reinterpret_cast<const half8_t*>(cur + (a_base[bm] ^ (uint32_t)(16 * ((s + 1) + ((s + 1) & QS)))));
         }
         if (s == 0) load(rnd + ST - 1, stn);
 #pragma unroll
@@ -746,6 +800,12 @@ __global__ __launch_bounds__(256 * KG, KG == 1 ? 2 : 1) void linear_act_tile_ker
     if (rp + i < nr) step(rp + i, i, rs[i & 1], rs[1 - (i & 1)]);
   wait_copies<0>();                                   // the look-ahead has landed before the LDS is used again
   tile_barrier();
+#pragma unroll
+  for (int bm = 0; bm < BMB; ++bm)
+#pragma unroll
+    for (int bn = 0; bn < BNB; ++bn)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[bm][bn][i] *= unit[bn];
 
   // ---- epilogue: value i of lane l in block (bm, bn) is row 8 (i / 4) + 4 (l / 32) + i % 4, column l % 32.
   const int outs = a.gated ? 32 : 64;                 // outputs of the wave
