@@ -58,8 +58,8 @@ def test_a_row_among_its_expert(P, k, g, dt):
 TILES = [(m, n, k, g) for m, n, k in ((700, 2050, 768), (2000, 4096, 192), (2000, 4096, 768), (2100, 8192, 768),
                                       (1100, 8192, 512), (1000, 2048, 1536), (640, 4096, 1920)) for g in (128, 64, 32)]
 # streaming with 8 and 16 rows
-STREAMS = [(m, n, k, 128) for m, n, k in ((1, 48, 384), (4, 48, 512), (8, 72, 384), (16, 40, 512), (40, 40, 384),
-                                          (300, 520, 512), (300, 2050, 512))]
+STREAMS = [(m, n, k, g) for m, n, k in ((1, 48, 384), (4, 48, 512), (8, 72, 320), (16, 40, 512), (40, 40, 384),
+                                        (300, 520, 448), (300, 2050, 512)) for g in (128, 64, 32)]
 
 
 def scattered_scales(ge, n, ng):

@@ -9,8 +9,8 @@
 // upper bound.  Roundings: bf16 activations once to fp16 (exact within fp16's normal range:
 // the matrix instructions take one type, and the weights' integers need more than bf16's 8
 // bits once scaled); x inv_s once to fp16 (by pairs without loss where a few rows stream, see
-// there); weights exactly, but where rows stream with g = 32 or 64: as fp16((q - z) D), 2^-11 of
-// a weight.  Sums, bias, activation and residual are fp32 with one rounding at the end.
+// there); weights exactly.  Sums, bias, activation and residual are fp32 with one rounding at the
+// end.
 #include "decode_common.h"
 #include "moe_common.h"
 
@@ -251,7 +251,12 @@ __device__ __forceinline__ void tile_barrier() {
 // 2 x 14336 x 4096: 18.0 -> 18.3 us).
 // v_mfma_f32_16x16x32_f16, rows as A, weights as B.  g = 128: a block is one group, its
 // integers q - z enter exactly and the group's sum is scaled in fp32.  g = 32, 64: a lane's 32
-// codes are of one group and become fp16((q - z) D) before the product, as in the tiles.
+// codes are of one group, but a product takes codes of four lanes and so of several groups; weights
+// enter as fp16((q - z) D) and, in a second product, what that lost: at most 4 bits above the last
+// bit of D, exact.  Against the first product alone: one token, gate and up of 2 x 14336 x 4096
+// 23.4 -> 26.1 us (g = 64), 24.9 -> 27.1 (32); 64 tokens on 128 experts 104 -> 116, 110 -> 121.
+// (Integers with the other groups' rows as zeros, two or four products a word: 26.2 and 31.9; 109
+// and 153.)
 // Bound by the weights' bytes: one token on two of 8 experts (122 MB) 28.0 us, 4.4 TB/s; dense
 // gate and up of one token (61 MB) 14.4 us, 4.2; 64 tokens on 128 experts (256 MB) 71 us, 3.6:
 // there 8000 work-groups of one run to a wave each pay for their plan, their rows and their
@@ -406,7 +411,7 @@ __global__ __launch_bounds__(256, 2) void linear_act_stream_kernel(const ActArgs
 #pragma unroll
   for (int cb = 0; cb < kCB; ++cb) acc[cb] = floatx4_t{};
   const unsigned char* frag = stage + (TM == 16 ? r : r & 7) * STRIDE + c * 64;
-  auto block = [&](int b, int i, const uint4 (&w)[kCB], const RunScales<G, QUADS>& rs) {
+  auto block = [&](int b, int i, const uint4 (&w)[kCB], const RunScales<G, QUADS>& rs, auto rest) {
     half8_t af[4];
 #pragma unroll
     for (int s = 0; s < 4; ++s) af[s] = *reinterpret_cast<const half8_t*>(frag + (i % SB) * 256 + s * 16);
@@ -425,14 +430,21 @@ __global__ __launch_bounds__(256, 2) void linear_act_stream_kernel(const ActArgs
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         const uint32_t word = s == 0 ? w[cb].x : s == 1 ? w[cb].y : s == 2 ? w[cb].z : w[cb].w;
-        uint32_t u[4];
+        uint32_t u[4], lo[4];
         unpack_word(word, u, uc);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           half2_t q = __builtin_bit_cast(half2_t, u[j]) + (j & 1 ? o64 : o1024);
-          if (G != 128) q = q * dd;
+          if (G != 128) {
+            const half2_t hi = q * dd;
+            lo[j] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(q, dd, -hi));
+            q = hi;
+          }
           u[j] = __builtin_bit_cast(uint32_t, q);
         }
+        if constexpr (G != 128 && rest)
+          part = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+              af[s], __builtin_bit_cast(half8_t, make_uint4(lo[0], lo[1], lo[2], lo[3])), part, 0, 0, 0);
         part = __builtin_amdgcn_mfma_f32_16x16x32_f16(af[s], __builtin_bit_cast(half8_t, make_uint4(u[0], u[1], u[2], u[3])),
                                                       part, 0, 0, 0);
       }
@@ -446,19 +458,47 @@ __global__ __launch_bounds__(256, 2) void linear_act_stream_kernel(const ActArgs
     }
   };
 
-  for (int b = b0; b < b1; b += kRun) {
-    uint4 w[kRun][kCB], x[XL], iv = make_uint4(0, 0, 0, 0);
-    RunScales<G, QUADS> rs;
-    load_x(b, x, iv);
-    load_w(b, w, rs);
-    store_x(b, x, iv);
-    if (SB == 2 && b + 2 < b1) load_x(b + 2, x, iv);
-    block(b, 0, w[0], rs);
-    if (b + 1 < b1) block(b + 1, 1, w[1], rs);
-    if (SB == 2 && b + 2 < b1) store_x(b + 2, x, iv);
-    if (b + 2 < b1) block(b + 2, 2, w[2], rs);
-    if (b + 3 < b1) block(b + 3, 3, w[3], rs);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  auto sweep = [&](auto rest) {
+    for (int b = b0; b < b1; b += kRun) {
+      uint4 w[kRun][kCB], x[XL], iv = make_uint4(0, 0, 0, 0);
+      RunScales<G, QUADS> rs;
+      load_x(b, x, iv);
+      load_w(b, w, rs);
+      store_x(b, x, iv);
+      if (SB == 2 && b + 2 < b1) load_x(b + 2, x, iv);
+      block(b, 0, w[0], rs, rest);
+      if (b + 1 < b1) block(b + 1, 1, w[1], rs, rest);
+      if (SB == 2 && b + 2 < b1) store_x(b + 2, x, iv);
+      if (b + 2 < b1) block(b + 2, 2, w[2], rs, rest);
+      if (b + 3 < b1) block(b + 3, 3, w[3], rs, rest);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+  };
+  sweep(std::true_type{});
+  if constexpr (G != 128) {
+    // an infinity in x is NaN once multiplied with a rest of zero, a weight beyond fp16 with its rest:
+    // such sums are taken once more, without the rests
+    bool odd = false;
+#pragma unroll
+    for (int cb = 0; cb < kCB; ++cb)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int row = 4 * c + j;
+        odd |= (row < p.rows || (low && row < p.rows + 4)) && acc[cb][j] != acc[cb][j];
+      }
+    if (__ballot(odd)) {
+      floatx4_t first[kCB];
+#pragma unroll
+      for (int cb = 0; cb < kCB; ++cb) {
+        first[cb] = acc[cb];
+        acc[cb] = floatx4_t{};
+      }
+      sweep(std::false_type{});
+#pragma unroll
+      for (int cb = 0; cb < kCB; ++cb)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[cb][j] = first[cb][j] == first[cb][j] ? first[cb][j] : acc[cb][j];
+    }
   }
   // ---- the waves' sums, added in wave order: [wave][block][4][lane]
   __syncthreads();
