@@ -617,7 +617,7 @@ awq_status awq_attn_kv8_bf16(const awq_kv8_cache* cache, int64_t rows, int64_t m
  *   type of y.  x_tilde = fp16_rn(x inv_s16) or x; bf16 x is rounded once to fp16
  *   first (see awq_linear_w4a16_bf16 for its range).  Where m <= 4, what
  *   fp16_rn(x inv_s16) lost is added again, as an fp16 of its own (x_tilde within
- *   max(2^-22 |x inv_s16|, 2^-25); nothing where the product is not finite).  Weights
+ *   max(2^-22 |x inv_s16|, 2^-36); nothing where the product is not finite).  Weights
  *   enter the products exactly (with g = 32 and 64 and few rows where |(q - z) D| is
  *   at most 65504).
  *   Before the activation the sum is within 5e-3 * max(|v_ref|, rms of the row of

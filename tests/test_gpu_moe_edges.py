@@ -122,3 +122,24 @@ def test_rows_with_infinities(P, m, g, inv):
         rest = [i for i in range(m) if i not in odd]
         assert len(rest) == m - 3
         R.check(y[rest], v[rest], bound[rest], (m, g, act))
+
+
+@pytest.mark.parametrize("down", [0, 3, 8, 10])
+@pytest.mark.parametrize("rows", [1, 4])
+@pytest.mark.parametrize("k,g", [(1024, 128), (320, 64), (192, 32)])
+def test_small_products_with_the_inverse_scale(P, rows, k, g, down):
+    """Rows times 2^-down: what fp16 loses of x inv_s16, 2^-20 of it, is below fp16's last place from 2^-4 on.
+
+    Even channels give (1 + 2^-10)^2, odd ones -(1 + 2^-9), times a power of two: equal once rounded, 2^-20 of
+    it apart; every sum is exact in fp32, and so is the result times scales of 2^down."""
+    n = 33
+    x, inv = torch.full((rows, k), 1 + 2.0 ** -9), torch.ones(k)
+    x[:, ::2], inv[::2] = 1 + 2.0 ** -10, 1 + 2.0 ** -10
+    x *= 2.0 ** (torch.arange(rows) - down)[:, None]
+    words = [sum(8 << (4 * j) for j in range(min(8, k // g - 8 * i))) for i in range(-(-k // (8 * g)))]
+    qz = torch.tensor([w - 2 ** 32 if w >= 2 ** 31 else w for w in words]).int().repeat(n, 1)
+    qw = torch.full((n, k // 8), 0x79797979, dtype=torch.int32)                      # q - z = 1, -1, 1 ..
+    sc = torch.full((n, k // g), 2.0 ** down).half()
+    y = P.awq_linear_w4a16_act(*(t.to(DEV) for t in (x.half(), qw, sc, qz, inv.half())), g=g)
+    want = (k * 2.0 ** -21 * 2.0 ** torch.arange(rows, dtype=torch.float64))[:, None].expand(rows, n)
+    assert torch.equal(y.cpu().double(), want)

@@ -273,13 +273,17 @@ struct StreamLds {
   static constexpr int WAVE = TM * STRIDE;
 };
 
-// What fp16 lost of hi = x s, element by element; nothing where hi left fp16's range.
+// What fp16 lost of hi = x s, element by element, times 2^kRest: at most half a unit of hi's last
+// place, so within fp16's range, and above its subnormal numbers where hi is above 2^-14.  With it
+// x s is within max(2^-22 |x s|, 2^-36).  Nothing where hi left fp16's range.
+constexpr int kRest = 11;
 __device__ __forceinline__ uint4 remainder8(const half8_t x, const half8_t s, const half8_t hi) {
   half8_t lo;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float h = (float)hi[i];
-    lo[i] = (_Float16)(__builtin_fabsf(h) <= 65504.0f ? __builtin_fmaf((float)x[i], (float)s[i], -h) : 0.0f);
+    const float r = __builtin_fmaf((float)x[i], (float)s[i], -h) * (float)(1 << kRest);
+    lo[i] = (_Float16)(__builtin_fabsf(h) <= 65504.0f ? r : 0.0f);
   }
   return __builtin_bit_cast(uint4, lo);
 }
@@ -520,8 +524,8 @@ __global__ __launch_bounds__(256, 2) void linear_act_stream_kernel(const ActArgs
       v += s[0];
       if (a.gated) u += s[outs];
       if (low) {                                       // row + 4: lane + 16
-        v += s[16];
-        if (a.gated) u += s[outs + 16];
+        v += s[16] * (1.0f / (1 << kRest));
+        if (a.gated) u += s[outs + 16] * (1.0f / (1 << kRest));
       }
     }
     const int64_t at = (int64_t)(p.row0 + row) * a.n + o;
