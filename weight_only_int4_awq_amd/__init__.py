@@ -905,20 +905,21 @@ def awq_moe_linear_workspace_size(rows, x_rows, e, n, k, g=128, gated=False, has
                                                          1 if has_inv_s16 else 0, 1 if bf16 else 0))
 
 
-def awq_moe_linear_w4a16(x, qweight, scales, qzeros, offsets, row_slot=None, topk=1, inv_s16=None, bias=None,
+def awq_moe_linear_w4a16(x, qweight, scales, qzeros, offsets, row_slot=None, topk=None, inv_s16=None, bias=None,
                          act="none", gated=False, g=128, out=None, workspace=None):
     """awq_linear_w4a16_act of every expert on its rows -> fp16 [rows, n].
 
     qweight int32 [e, nw, k/8], scales fp16 [e, nw, k/g], qzeros int32 [e, nw, ceil(k/(8g))]
     (nw = n, gated 2 n: the gate's rows first); offsets int32 [e + 1]: rows offsets[j] ..
     offsets[j + 1] - 1 are expert j's.  row_slot int32 [rows] (awq_moe_route): row r reads
-    x[row_slot[r] // topk] of x fp16 [t, k]; without it row r reads x[r].  inv_s16 fp16 [k]
+    x[row_slot[r] // topk] of x fp16 [t, k], topk that of the routing (1 when left out, where
+    row_slot is no longer than x); without row_slot row r reads x[r].  inv_s16 fp16 [k]
     for all experts, bias fp16 [e, nw].  Rows of no expert are left as they were."""
     return _moe_linear(x, qweight, scales, qzeros, offsets, row_slot, topk, inv_s16, bias, act, gated, g, out,
                        workspace, False)
 
 
-def awq_moe_linear_w4a16_bf16(x, qweight, scales, qzeros, offsets, row_slot=None, topk=1, inv_s16=None, bias=None,
+def awq_moe_linear_w4a16_bf16(x, qweight, scales, qzeros, offsets, row_slot=None, topk=None, inv_s16=None, bias=None,
                               act="none", gated=False, g=128, out=None, workspace=None):
     """awq_moe_linear_w4a16 with bf16 x, bias and out."""
     return _moe_linear(x, qweight, scales, qzeros, offsets, row_slot, topk, inv_s16, bias, act, gated, g, out,
@@ -938,6 +939,10 @@ def _moe_linear(x, qweight, scales, qzeros, offsets, row_slot, topk, inv_s16, bi
         e, nw, _ = qweight.shape
         n = nw // 2 if gated else nw
         rows = t if row_slot is None else row_slot.shape[0]
+        if topk is None:                                # slots of one choice are tokens
+            if rows > t:
+                raise ValueError(f"{rows} slots of {t} rows of x need the topk that they were routed with")
+            topk = 1
         checks = ((x, dt, (t, k), "x"), (qweight, i32, (e, nw, k // 8), "qweight"),
                   (scales, f16, (e, nw, k // g), "scales"), (qzeros, i32, (e, nw, -(-k // (8 * g))), "qzeros"),
                   (offsets, i32, (e + 1,), "offsets"), (row_slot, i32, (rows,), "row_slot"),
