@@ -939,10 +939,6 @@ def _moe_linear(x, qweight, scales, qzeros, offsets, row_slot, topk, inv_s16, bi
         e, nw, _ = qweight.shape
         n = nw // 2 if gated else nw
         rows = t if row_slot is None else row_slot.shape[0]
-        if topk is None:                                # slots of one choice are tokens
-            if rows > t:
-                raise ValueError(f"{rows} slots of {t} rows of x need the topk that they were routed with")
-            topk = 1
         checks = ((x, dt, (t, k), "x"), (qweight, i32, (e, nw, k // 8), "qweight"),
                   (scales, f16, (e, nw, k // g), "scales"), (qzeros, i32, (e, nw, -(-k // (8 * g))), "qzeros"),
                   (offsets, i32, (e + 1,), "offsets"), (row_slot, i32, (rows,), "row_slot"),
@@ -952,6 +948,10 @@ def _moe_linear(x, qweight, scales, qzeros, offsets, row_slot, topk, inv_s16, bi
         _dev_tensor(x, dt, "x", 2)
         _dev_tensor(qweight, i32, "qweight", 3)
         raise
+    if topk is None:                                    # slots of one choice are tokens
+        if rows > t:
+            raise ValueError(f"{rows} slots of {t} rows of x need the topk that they were routed with")
+        topk = 1
     if not good:
         _dev_tensor(x, dt, "x", 2)
         if gated and nw % 2:
