@@ -698,8 +698,8 @@ awq_status awq_linear_w4a16_act_bf16(const uint16_t* x, const uint32_t* qweight,
  *   y[i] = residual[i] + sum_j weights[i][j] rows[slot_row[i][j]], fp32 in the order of j,
  *   rounded once.  A slot_row outside 0 .. row_count - 1 adds its weight times zero.
  *   rows [row_count][n], residual [t][n] or NULL (may be y), y [t][n]: fp16 (bf16).
- *   Limits: t <= 2^24; 1 <= n <= 2^24; topk <= 32; row_count <= 2^27; t * n/8 (t * n where
- *   n % 8) <= 2^31.
+ *   Limits: t <= 2^24; 1 <= n <= 2^24; topk <= 32; row_count <= 2^27; t * n/8 <= 2^31, and
+ *   t * n where n % 8 or where rows, residual or y are not 16-byte aligned.
  * ------------------------------------------------------------------------- */
 enum { AWQ_LOGITS_F32 = 0, AWQ_LOGITS_F16 = 1, AWQ_LOGITS_BF16 = 2 };
 enum { AWQ_ROUTE_SOFTMAX = 0, AWQ_ROUTE_SIGMOID = 1 };

@@ -779,7 +779,7 @@ static awq_status moe_combine_impl(const char* fn, const uint16_t* rows, int64_t
   if (n < 1 || n > (1 << 24)) return err(AWQ_ERR_SHAPE, "n=%lld outside 1..2^24", n);
   if (t < 0 || t > (1 << 24)) return err(AWQ_ERR_SHAPE, "t=%lld outside 0..2^24", t);
   if (row_count < 0 || row_count > (1 << 27)) return err(AWQ_ERR_SHAPE, "rows=%lld outside 0..2^27", row_count);
-  if (t * (n % 8 ? n : n / 8) > (1ll << 31)) return err(AWQ_ERR_SHAPE, "t=%lld tokens of n=%lld are more than one launch holds", t, n);
+  if (t * (awq::moe_combine_vec(rows, residual, y, n) ? n / 8 : n) > (1ll << 31)) return err(AWQ_ERR_SHAPE, "t=%lld tokens of n=%lld are more than one launch holds", t, n);
   if (t == 0) return AWQ_OK;
   if (!weights || !slot_row || !y || (row_count > 0 && !rows)) return err(AWQ_ERR_NULL, "null pointer");
   if (!aligned(rows, 2) || !aligned(residual, 2) || !aligned(y, 2) || !aligned(weights, 4) || !aligned(slot_row, 4))

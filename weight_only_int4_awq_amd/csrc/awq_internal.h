@@ -168,6 +168,8 @@ size_t moe_route_scratch_bytes(int64_t t, int32_t e);
 hipError_t launch_moe_route(const void* logits, int32_t type, int64_t t, int32_t e, int32_t topk, int32_t scoring,
                             bool renorm, float scale, int32_t* ids, float* weights, int32_t* offsets,
                             int32_t* row_slot, int32_t* slot_row, void* scratch, hipStream_t stream);
+// Whether a thread takes 8 columns: else one.
+bool moe_combine_vec(const uint16_t* rows, const uint16_t* residual, const uint16_t* y, int64_t n);
 hipError_t launch_moe_combine(const uint16_t* rows, int64_t cap, const float* weights, const int32_t* slot_row,
                               const uint16_t* residual, int64_t t, int64_t n, int32_t topk, bool bf, uint16_t* y,
                               hipStream_t stream);

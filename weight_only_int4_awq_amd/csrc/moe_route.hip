@@ -590,11 +590,15 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const uint16_t* __rest
   }
 }
 
+bool moe_combine_vec(const uint16_t* rows, const uint16_t* residual, const uint16_t* y, int64_t n) {
+  auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+  return n % 8 == 0 && al(rows) && al(residual) && al(y);
+}
+
 hipError_t launch_moe_combine(const uint16_t* rows, int64_t cap, const float* weights, const int32_t* slot_row,
                               const uint16_t* residual, int64_t t, int64_t n, int32_t topk, bool bf, uint16_t* y,
                               hipStream_t stream) {
-  auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
-  const bool vec = n % 8 == 0 && al(rows) && al(residual) && al(y);
+  const bool vec = moe_combine_vec(rows, residual, y, n);
   const int64_t per = vec ? n / 8 : n;
   const dim3 grid((unsigned)((t * per + 255) / 256));
   auto go = [&](auto kernel) {
