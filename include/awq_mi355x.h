@@ -629,8 +629,7 @@ awq_status awq_attn_kv8_bf16(const awq_kv8_cache* cache, int64_t rows, int64_t m
  *   awq_linear_act_workspace_size(m, n, k, g, gated, inv_s16 != NULL, bf16) bytes,
  *   256-byte aligned (NULL if that is 0).
  *   Limits: g in {32, 64, 128}; k % g == 0; k % 64 == 0; k <= 2^23; 0 <= m <= 2^27; packed
- *   weights below 4 GiB; m * n/4, m * k/8 <= 2^31; what one launch holds: m * n below some
- *   2^35 (2^36 up to 512 rows).
+ *   weights below 4 GiB; m * n/4, m * k/8 <= 2^31.
  * ------------------------------------------------------------------------- */
 enum { AWQ_ACT_NONE = 0, AWQ_ACT_SILU = 1, AWQ_ACT_GELU = 2, AWQ_ACT_GELU_TANH = 3 };
 size_t awq_linear_act_workspace_size(int64_t m, int64_t n, int64_t k, int32_t g, int32_t gated,
@@ -691,8 +690,9 @@ awq_status awq_linear_w4a16_act_bf16(const uint16_t* x, const uint32_t* qweight,
  *   four, in calls of up to six rows to an expert on average, and no others.
  *   workspace: awq_moe_linear_workspace_size(rows, x_rows, e, n, k, g, gated,
  *     inv_s16 != NULL, bf16) bytes (x_rows = rows without row_slot), 256-byte aligned.
- *   Limits: those of awq_linear_w4a16_act with rows for m, packed weights of one expert
- *   below 4 GiB; 1 <= e <= 1024; 1 <= topk <= 32; with row_slot x below 4 GiB.
+ *   Limits: those of awq_linear_w4a16_act with rows for m (and x_rows * k/8 <= 2^31), packed
+ *   weights of one expert below 4 GiB; (rows/32 + min(e, rows)) ceil(n/256) < 2^22 (gated
+ *   ceil(n/128)); 1 <= e <= 1024; 1 <= topk <= 32; with row_slot x below 4 GiB.
  *
  * awq_moe_combine, _bf16:
  *   y[i] = residual[i] + sum_j weights[i][j] rows[slot_row[i][j]], fp32 in the order of j,

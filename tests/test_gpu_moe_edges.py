@@ -143,3 +143,32 @@ def test_small_products_with_the_inverse_scale(P, rows, k, g, down):
     y = P.awq_linear_w4a16_act(*(t.to(DEV) for t in (x.half(), qw, sc, qz, inv.half())), g=g)
     want = (k * 2.0 ** -21 * 2.0 ** torch.arange(rows, dtype=torch.float64))[:, None].expand(rows, n)
     assert torch.equal(y.cpu().double(), want)
+
+
+def wide_packed(lead, n, k, seed):
+    """Packed weights of many rows, made on the device (g = 64)."""
+    ge = torch.Generator(device=DEV).manual_seed(seed)
+    bits = lambda *shape: torch.randint(-2 ** 31, 2 ** 31 - 1, shape, generator=ge, dtype=torch.int32, device=DEV)
+    sc = torch.rand(*lead, n, k // 64, generator=ge, dtype=F16, device=DEV) * 0.1
+    return bits(*lead, n, k // 8), sc, bits(*lead, n, 1) & 15
+
+
+def test_few_rows_of_more_columns_than_streaming_launches(P):
+    """1024 experts of 131072 outputs and a row each; one matrix of 2^27 - 1 outputs, packed just below 4 GiB."""
+    k = 64
+    ge = gen(9)
+    for e, n in ((1024, 131072), (1, (1 << 27) - 1)):
+        rows = 1024 if e > 1 else 2
+        p = wide_packed((e,), n, k, e)
+        x = torch.randn(rows, k, generator=ge).half()
+        if e > 1:
+            y = P.awq_moe_linear_w4a16(x.to(DEV), *p, torch.arange(e + 1, dtype=torch.int32, device=DEV), g=k)
+        else:
+            y = P.awq_linear_w4a16_act(x.to(DEV), *(t[0] for t in p), g=k)
+        cols = torch.cat((torch.arange(100), torch.randint(0, n, (300,), generator=ge), torch.arange(n - 100, n)))
+        for r in (0, 1, rows // 2, rows - 1):
+            j = r if e > 1 else 0
+            w = R.weights(*(t[j][cols.to(DEV)].cpu() for t in p), k)
+            v, bound = R.linear(x[r:r + 1], w, None, None, "none", False, None, F16)
+            R.check(y[r:r + 1][:, cols.to(DEV)], v, bound, (e, r))
+        del p, y

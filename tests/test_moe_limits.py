@@ -44,3 +44,37 @@ def test_combine_limit_goes_by_the_threads_of_a_token(lib, fn):
     for off in (dict(rows=FAKE + 2), dict(residual=FAKE + 8), dict(y=FAKE + 2)):
         assert call(1 << 19, 4096, **off) == 1 and call((1 << 19) + 1, 4096, **off) == 2, off
     assert call(1 << 20, 2047) == 1 and call(1 << 20, 2049) == 2
+
+
+def test_grouped_limit_is_that_of_the_tiles(lib):
+    """(rows / 32 + min(e, rows)) column blocks of 256 outputs (gated 128), below 2^22, whatever kernel few rows
+    to an expert would take.  With inv_s16 a workspace is needed wherever sizes are taken and tiles are used."""
+    def need(rows, e, n, gated=0, k=64):
+        return lib.awq_moe_linear_workspace_size(rows, rows, e, n, k, 64, gated, 1, 0)
+    assert need(1024, 1024, 131072) >= 1024 * 128                          # few rows, wide: tiles
+    assert need(6144, 1024, 65536, 1) >= 6144 * 128
+    assert need(1024, 1024, 1 << 20) == 0                                  # 1056 * 4096
+    assert need(1024, 1024, 3971 * 256) >= 1024 * 128 and need(1024, 1024, 3972 * 256) == 0
+    assert need(1024, 1024, 3971 * 128, 1) >= 1024 * 128 and need(1024, 1024, 3972 * 128, 1) == 0
+    for fn in ("awq_moe_linear_w4a16", "awq_moe_linear_w4a16_bf16"):
+        def call(rows, e, n, gated):
+            return getattr(lib, fn)(FAKE, rows, FAKE, FAKE, FAKE, FAKE, None, 0, gated, e, FAKE, None, 1, rows, n, 64, 64,
+                                    FAKE, None, 0, None)
+        assert call(1024, 1024, 131072, 0) == 4 and call(6144, 1024, 65536, 1) == 4          # no workspace given
+        assert call(1024, 1024, 1 << 20, 0) == 2
+
+
+def test_dense_limits_are_those_of_the_sizes_alone(lib):
+    """m n / 4, m k / 8 and the packed weights' 4 GiB: nothing within them is more than a launch holds."""
+    def need(m, n, k, gated=0):
+        return lib.awq_linear_act_workspace_size(m, n, k, 64, gated, 1, 0)
+    def status(m, n, k, gated=0):                                          # without x: 1 where the sizes are taken
+        return lib.awq_linear_w4a16_act(None, FAKE, FAKE, FAKE, None, None, None, 0, gated, m, n, k, 64, FAKE, None, 0, None)
+    wide = (1 << 27) - 1                                                   # 64 channels: just below 4 GiB
+    for m in (1, 8, 9, 16, 17, 64):
+        assert status(m, wide, 64) == 1 and status(m, wide // 2, 64, 1) == 1, m
+        assert status(m, 1 << 27, 64) == 2 and status(m, 1 << 26, 64, 1) == 2, m
+    assert status(1 << 27, 64, 64) == 1 and status((1 << 27) + 1, 64, 64) == 2
+    assert status(1 << 27, 65, 64) == 2 and status(1 << 27, 64, 192) == 2  # m n / 4, m k / 8
+    assert status(1 << 20, 8192, 64) == 1 and status((1 << 20) + 1, 8192, 64) == 2
+    assert status(1 << 20, 8192, 64, 1) == 1 and need(1 << 20, 8192, 64, 1) >= 1 << 27

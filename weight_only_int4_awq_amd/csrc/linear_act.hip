@@ -34,7 +34,11 @@ __device__ __forceinline__ bool expert_rows(const ActArgs& a, int i, int& r0, in
   return s >= 0 && t >= s && t <= (int)a.rows;
 }
 
-// x / y for 0 <= x < 2^24, 0 < y: exact in fp32 and one step.
+// Units of a launch are fewer.
+constexpr int64_t kMaxUnits = 1 << 22;
+
+// x / y for 0 <= x < kMaxUnits, 0 < y < 2^24: x and y are exact in fp32; for y of 1 and 2 so is the
+// quotient, from 3 on it is below 2^21 and off by 1.5 2^-23 of it, less than one: one step either way.
 __device__ __forceinline__ int quot(int x, int y) {
   int q = (int)((float)x * __builtin_amdgcn_rcpf((float)y));
   const int rem = x - q * y;
@@ -46,7 +50,7 @@ __device__ __forceinline__ int quot(int x, int y) {
 // The units of a launch: tiles of 2^lt rows of each expert x column blocks x K slices, in an
 // order in which the tiles of an expert follow one another (bands of four row tiles, column by
 // column), so that work-groups next to one another share weights or rows.  Units are below
-// 2^24 (the host checks).
+// kMaxUnits (the host checks).
 struct Units {
   int lt;                                                // tiles of 2^lt rows
   static constexpr int KEEP = 2;                         // experts 0 .. 127 are looked up once
@@ -1077,15 +1081,17 @@ static ActPlan act_plan(const ActArgs& a) {
   const int64_t bytes = a.nw * (a.k / 2);              // packed weights of a matrix
   p.ks = 1;
   p.kg = 1;
-  if (a.offsets ? avg <= 6 : avg <= 16 || (avg <= 512 && (avg + 15) / 16 * bytes <= (36 << 20))) {
+  // streaming, unless that takes more units than a launch holds
+  const int sm = avg <= 8 ? 8 : 16, s_outs = (a.gated ? kCB / 2 : kCB) * 16;
+  const int64_t s_cols = (a.n + s_outs - 1) / s_outs, s_units = tiles(sm) * s_cols;
+  if ((a.offsets ? avg <= 6 : avg <= 16 || (avg <= 512 && (avg + 15) / 16 * bytes <= (36 << 20))) && s_units < kMaxUnits) {
     p.stream = true;
-    p.tm = avg <= 8 ? 8 : 16;
+    p.tm = sm;
     const int nb = (int)((a.k + 127) / 128), runs = (nb + kRun - 1) / kRun;
     p.per = (runs + 3) / 4 * kRun;                     // whole runs, up to 4 waves
     p.waves = (nb + p.per - 1) / p.per;
-    const int outs = (a.gated ? kCB / 2 : kCB) * 16;
-    p.ncol = (a.n + outs - 1) / outs;
-    p.units = tiles(p.tm) * p.ncol;
+    p.ncol = s_cols;
+    p.units = s_units;
     return p;
   }
   const int outs = a.gated ? 128 : 256;
@@ -1118,7 +1124,7 @@ size_t linear_act_scratch_bytes(const ActArgs& a) {
 }
 
 bool linear_act_fits(const ActArgs& a) {
-  return act_plan(a).units < (1 << 22) && a.x_rows * (a.k / 8) <= (1ll << 31) && a.rows * ((a.n + 3) / 4) <= (1ll << 31);
+  return act_plan(a).units < kMaxUnits && a.x_rows * (a.k / 8) <= (1ll << 31) && a.rows * ((a.n + 3) / 4) <= (1ll << 31);
 }
 
 template <int G, int TM>
