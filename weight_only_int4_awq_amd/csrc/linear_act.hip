@@ -167,10 +167,11 @@ __device__ __forceinline__ int slot_token(const ActArgs& a, int slot) {
 
 // ---------------------------------------------------------------- epilogue
 
-// erfc(x) = t exp(P(t) - x^2), t = 1 / (1 + |x| / 2), and 2 minus that below zero.  P: a
-// polynomial fitted at Chebyshev nodes to log(exp(x^2) erfc(x) / t) over x in [0, 14.6], off
-// by 7e-8; with the rounding of the exponent 2e-6 relative up to x = 5.  1 + erf(x) would lose
-// the lower tail's digits.
+// erfc(x) = t exp(P(t) - x^2), t = 1 / (1 + |x| / 2), and 2 minus that below zero: the form that
+// Press et al., Numerical Recipes, give for the complementary error function.  P: a polynomial
+// fitted here at Chebyshev nodes to log(exp(x^2) erfc(x) / t) over x in [0, 14.6], off by 1.2e-7;
+// with the rounding of the exponent 3e-6 relative up to x = 5, 8e-6 up to 9.2.  1 + erf(x) would
+// lose the lower tail's digits.
 __device__ __forceinline__ float erfc_tail(float x) {
   const float z = __builtin_fabsf(x);
   const float t = __builtin_amdgcn_rcpf(1.0f + 0.5f * z);
