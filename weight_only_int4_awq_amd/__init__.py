@@ -859,8 +859,10 @@ def awq_moe_route(logits, topk, scoring="softmax", renormalize=True, scale=1.0, 
     weights fp32 [t, topk], offsets int32 [e + 1], row_slot int32 [t * topk], slot_row
     int32 [t, topk]), written into ``out`` when given.
 
-    The topk largest logits, ties to the lower expert; -inf and NaN are closed (id -1,
-    weight 0, no row).  scoring: "softmax" (over all experts; renormalize: over the chosen
+    The topk largest logits, ties to the lower expert; experts at -inf are closed, and where
+    fewer than topk are open the rest of a token's choices have id -1, weight 0 and no row.
+    An expert at NaN is closed too, but makes all weights of its token NaN, those of id -1
+    among them: close experts with -inf.  With softmax a logit of +inf does the same.  scoring: "softmax" (over all experts; renormalize: over the chosen
     ones) or "sigmoid" (renormalize: divided by the chosen ones' sum); weights are times
     ``scale``.  Rows offsets[j] .. offsets[j + 1] - 1 are expert j's; row r stands for slot
     row_slot[r] = token * topk + choice; rows from offsets[e] on are left as they were."""
@@ -970,7 +972,8 @@ def _moe_linear(x, qweight, scales, qzeros, offsets, row_slot, topk, inv_s16, bi
 def awq_moe_combine(rows, weights, slot_row, residual=None, out=None):
     """y[i] = residual[i] + sum_j weights[i, j] rows[slot_row[i, j]]: rows fp16 [r, n], weights
     fp32 and slot_row int32 [t, topk] (awq_moe_route), residual fp16 [t, n] or None (may be
-    ``out``) -> fp16 [t, n], summed in fp32.  Slots without a row (-1) add nothing."""
+    ``out``) -> fp16 [t, n], summed in fp32.  A slot without a row (-1) adds its weight times
+    zero: nothing, or NaN where the weight is NaN or infinite."""
     return _moe_combine(rows, weights, slot_row, residual, out, False)
 
 
