@@ -664,8 +664,8 @@ awq_status awq_linear_w4a16_act_bf16(const uint16_t* x, const uint32_t* qweight,
  *                        renormalize: over the chosen ones;
  *     AWQ_ROUTE_SIGMOID  1 / (1 + exp(-x_j)); renormalize: divided by the sum of the
  *                        chosen ones' (0 where that is 0).
- *   0 where the id is -1.  All weights of a token with a NaN logit are NaN, and with
- *   softmax those of a token with a logit of +inf.
+ *   0 where the id is -1.  All weights of a token with a NaN logit are NaN, those of id -1
+ *   too, and with softmax those of the experts chosen beside a logit of +inf.
  *   offsets [e + 1] int32: rows offsets[j] .. offsets[j + 1] - 1 are expert j's.
  *   row_slot [t * topk] int32: row r stands for slot row_slot[r] = token * topk + choice;
  *     rows by expert, then by slot.  Rows from offsets[e] on are not written.

@@ -862,9 +862,10 @@ def awq_moe_route(logits, topk, scoring="softmax", renormalize=True, scale=1.0, 
     The topk largest logits, ties to the lower expert; experts at -inf are closed, and where
     fewer than topk are open the rest of a token's choices have id -1, weight 0 and no row.
     An expert at NaN is closed too, but makes all weights of its token NaN, those of id -1
-    among them: close experts with -inf.  With softmax a logit of +inf does the same.  scoring: "softmax" (over all experts; renormalize: over the chosen
-    ones) or "sigmoid" (renormalize: divided by the chosen ones' sum); weights are times
-    ``scale``.  Rows offsets[j] .. offsets[j + 1] - 1 are expert j's; row r stands for slot
+    among them: close experts with -inf.  With softmax a logit of +inf makes the weights of
+    the chosen experts NaN.  scoring: "softmax" (over all experts; renormalize: over the
+    chosen ones) or "sigmoid" (renormalize: divided by the chosen ones' sum); weights are
+    times ``scale``.  Rows offsets[j] .. offsets[j + 1] - 1 are expert j's; row r stands for slot
     row_slot[r] = token * topk + choice; rows from offsets[e] on are left as they were."""
     torch = _torch()
     i32 = torch.int32
