@@ -7,6 +7,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from tests import moe_ref as R  # noqa: E402
+from tests.test_gpu_moe import grouped  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -150,7 +151,11 @@ def wide_packed(lead, n, k, seed):
     ge = torch.Generator(device=DEV).manual_seed(seed)
     bits = lambda *shape: torch.randint(-2 ** 31, 2 ** 31 - 1, shape, generator=ge, dtype=torch.int32, device=DEV)
     sc = torch.rand(*lead, n, k // 64, generator=ge, dtype=F16, device=DEV) * 0.1
-    return bits(*lead, n, k // 8), sc, bits(*lead, n, 1) & 15
+    ng = k // 64
+    qz = bits(*lead, n, -(-ng // 8))
+    if ng % 8:
+        qz[..., -1] &= (1 << (4 * (ng % 8))) - 1
+    return bits(*lead, n, k // 8), sc, qz
 
 
 def test_few_rows_of_more_columns_than_streaming_launches(P):
@@ -172,3 +177,37 @@ def test_few_rows_of_more_columns_than_streaming_launches(P):
             v, bound = R.linear(x[r:r + 1], w, None, None, "none", False, None, F16)
             R.check(y[r:r + 1][:, cols.to(DEV)], v, bound, (e, r))
         del p, y
+
+
+@pytest.mark.parametrize("counts", [[0] * 20 + [70, 1, 0, 37] + [2] * 16, [33] + [0] * 9, [3] * 40 + [130] + [0] * 30,
+                                    [1, 64, 0, 0, 65] + [0] * 40], ids=lambda c: f"{len(c)}x{sum(c)}")
+@pytest.mark.parametrize("gather", [False, True])
+def test_streaming_of_experts_with_many_rows(P, counts, gather):
+    """Up to six rows to an expert on average, and more than four tiles of eight rows at some."""
+    assert sum(counts) + 3 <= 6 * len(counts)
+    grouped(P, counts, 200, 256, 128, F16, gather, "silu", True, True, False)
+    grouped(P, counts, 333, 192, 64, BF16, gather, "none", False, True, True)
+    grouped(P, counts, 264, 96 * 2, 32, F16, gather, "gelu", False, False, True, topk=3)
+
+
+@pytest.mark.parametrize("dt,inv", [(F16, False), (BF16, False), (F16, True)])
+@pytest.mark.parametrize("e,rows,n,k", [(2, (1 << 25) + 100, 8, 64), (1024, 6144, 2, 350080)])
+def test_rows_of_x_beyond_31_bits(P, e, rows, n, k, dt, inv):
+    """x of more than 2^31 elements, row by row: tiles (as it is and converted) and streaming."""
+    assert rows * k > 1 << 31
+    p = wide_packed((e,), n, k, rows)
+    ge = torch.Generator(device=DEV).manual_seed(k)
+    x = torch.empty(rows, k, dtype=dt, device=DEV)
+    for part in x.split(rows // 8):
+        part.copy_(torch.randn(part.shape, generator=ge, device=DEV).clamp_(-8, 8))
+    iv = torch.full((k,), 0.5, dtype=F16, device=DEV) if inv else None
+    offsets = torch.tensor([rows * j // e for j in range(e + 1)], dtype=torch.int32, device=DEV)
+    fn = P.awq_moe_linear_w4a16_bf16 if dt is BF16 else P.awq_moe_linear_w4a16
+    y = fn(x, *p, offsets, inv_s16=iv, g=64)
+    for j in (0, e - 1):
+        w = R.weights(*(t[j].cpu() for t in p), 64)
+        a, z = int(offsets[j]), int(offsets[j + 1])
+        at = torch.unique(torch.tensor([a, a + 1, max(a, z - 1000), z - 2, z - 1] + [r for r in ((1 << 31) // k, (1 << 31) // k + 1) if a <= r < z]))
+        # bf16 values below fp16's normal range lose up to 2^-25 each
+        v, bound = R.linear(x[at.to(DEV)].cpu(), w, None if iv is None else iv.cpu(), None, "none", False, None, dt)
+        R.check(y[at.to(DEV)], v, bound, (e, rows, dt, inv, j))
