@@ -78,3 +78,15 @@ def test_dense_limits_are_those_of_the_sizes_alone(lib):
     assert status(1 << 27, 65, 64) == 2 and status(1 << 27, 64, 192) == 2  # m n / 4, m k / 8
     assert status(1 << 20, 8192, 64) == 1 and status((1 << 20) + 1, 8192, 64) == 2
     assert status(1 << 20, 8192, 64, 1) == 1 and need(1 << 20, 8192, 64, 1) >= 1 << 27
+
+
+def test_rows_that_stream(lib):
+    """One matrix streams up to 16 rows, and up to 512 where 36 MiB of weights and 2^16 weight rows are read in
+    all, 16 rows at a time; with inv_s16 tiles need a workspace and streaming none."""
+    def streams(m, n, k, gated=0):
+        return lib.awq_linear_act_workspace_size(m, n, k, 128, gated, 1, 0) == 0
+    assert streams(16, 14336, 4096, 1) and not streams(17, 14336, 4096, 1)
+    assert streams(64, 4096, 4096) and not streams(81, 4096, 4096)         # MiB: 4 passes of 8, 6 of 8
+    assert streams(240, 4096, 512) and not streams(241, 4096, 512)         # rows: 15 passes of 4096, 16 of 4096
+    assert streams(240, 2048, 512, 1) and not streams(241, 2048, 512, 1)
+    assert streams(512, 512, 4096) and not streams(513, 512, 4096)

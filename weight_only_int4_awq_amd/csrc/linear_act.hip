@@ -1049,10 +1049,14 @@ __global__ __launch_bounds__(256) void linear_act_prep_kernel(const ActArgs a, u
 //
 // Chosen by the sizes the host knows; the rows of an expert are taken as their mean.
 // Microseconds of both sides near the borders (captured, weights cold):
-//   streaming or tiles, one matrix: 4096 x 4096, 17 / 64 rows 11.5 / 15.5 against 18.4 / 25.8; 1024 x 4096,
-//     64 / 128 rows 11.5 / 12.0 against 18 / 23; 28672 x 4096 (59 MB), 16 / 17 rows 28 against 33 / 38 (tiles
-//     28 with K-steps of 128): past 16 rows streaming reads the weights again for every 16, which pays up
-//     to some 36 MB in all.
+//   streaming or tiles, one matrix: past 16 rows streaming reads and unpacks the weights again for every 16,
+//     which pays up to 36 MiB of weights in all, unless short rows (k) make that many units: fewer than 2^16
+//     weight rows in all.  4096 <- 4096, 17 / 64 / 96 / 128 rows (16 / 32 / 48 / 64 MiB) 11.2 / 15.4 / 19.7 / 25.3
+//     against 16.4 / 18.8 / 20.5 / 21.5; 1024 <- 4096, 256 / 512 rows (32 / 64) 15.3 / 25.4 against 18.3 / 21.2;
+//     512 <- 4096, 512 rows (32) 15.7 against 18.4; 1024 <- 2048, 512 rows (32) 16.1 against 17.7; 4096 <- 1024,
+//     192 / 256 rows (24 / 32) 13.0 / 18.2 against 16.1 / 16.7; 4096 <- 512, 192 / 256 / 384 rows (12 / 16 / 24)
+//     11.3 / 12.1 / 14.5 against 13.9 / 13.5 / 11.2.  28672 <- 4096 (56 MiB a time): 16 rows streamed 28, 17 rows
+//     by tiles 28 (streamed 38).
 //   streaming or tiles, experts of 2048 <- 1408, mean of 9 rows: 39 against 34; of 1024 x 2 <- 2048, 4 rows
 //     74 against 82, 8 rows 103 against 95: the border is at 6.
 //   tiles of 32, 64, 128 rows, by the K-steps that 128-row tiles would take in all: 4096 x 4096, 96 rows (1024)
@@ -1085,7 +1089,9 @@ static ActPlan act_plan(const ActArgs& a) {
   // streaming, unless that takes more units than a launch holds
   const int sm = avg <= 8 ? 8 : 16, s_outs = (a.gated ? kCB / 2 : kCB) * 16;
   const int64_t s_cols = (a.n + s_outs - 1) / s_outs, s_units = tiles(sm) * s_cols;
-  if ((a.offsets ? avg <= 6 : avg <= 16 || (avg <= 512 && (avg + 15) / 16 * bytes <= (36 << 20))) && s_units < kMaxUnits) {
+  const int64_t passes = (avg + 15) / 16;
+  const bool again = avg <= 512 && passes * bytes <= (36 << 20) && passes * a.nw < (1 << 16);
+  if ((a.offsets ? avg <= 6 : avg <= 16 || again) && s_units < kMaxUnits) {
     p.stream = true;
     p.tm = sm;
     const int nb = (int)((a.k + 127) / 128), runs = (nb + kRun - 1) / kRun;
