@@ -618,8 +618,8 @@ awq_status awq_attn_kv8_bf16(const awq_kv8_cache* cache, int64_t rows, int64_t m
  *   first (see awq_linear_w4a16_bf16 for its range).  Where m <= 4, what
  *   fp16_rn(x inv_s16) lost is added again, as an fp16 of its own (x_tilde within
  *   max(2^-22 |x inv_s16|, 2^-36); nothing where the product is not finite).  Weights
- *   enter the products exactly (with g = 32 and 64 and few rows where |(q - z) D| is
- *   at most 65504).
+ *   enter the products exactly (with g = 32 and 64 and up to 512 rows they may be infinite
+ *   where |(q - z) D| > 65504).
  *   Before the activation the sum is within 5e-3 * max(|v_ref|, rms of the row of
  *   v_ref) of the float64 value.
  *   x [m][k], residual, y [m][n], bias [n] ([2 n] gated): fp16 (bf16); bias and
@@ -681,10 +681,10 @@ awq_status awq_linear_w4a16_act_bf16(const uint16_t* x, const uint32_t* qweight,
  *   awq_fold_inv_scale_rows).  Row r of y [rows][n] reads x[row_slot[r] / topk] of
  *   x [x_rows][k], or with row_slot NULL x[r] of x [rows][k] (x_rows is not read).
  *   offsets and row_slot are device data and not checked on the host: whatever they
- *   hold, nothing outside the tensors is read or written.  Under offsets that do not
- *   ascend within 0 .. rows nothing is written; a slot outside those of x gives a row
- *   of x all the same.  Rows of y that no expert has are not written.  rows: what
- *   row_slot and y hold, at least offsets[e].  The number of rows and experts chooses
+ *   hold, nothing outside the tensors is read (but the two bytes behind scales, as
+ *   above) or written.  Under offsets that do not ascend within 0 .. rows nothing is
+ *   written; a slot outside those of x gives a row of x all the same.  Rows of y that
+ *   no expert has are not written.  rows: what row_slot and y hold, at least offsets[e].  The number of rows and experts chooses
  *   between kernels; results are right for any split of the rows.  All rows of an expert
  *   are rounded alike: as pairs (see awq_linear_w4a16_act) those of an expert with up to
  *   four, in calls of up to six rows to an expert on average, and no others.

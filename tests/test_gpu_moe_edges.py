@@ -211,3 +211,26 @@ def test_rows_of_x_beyond_31_bits(P, e, rows, n, k, dt, inv):
         # bf16 values below fp16's normal range lose up to 2^-25 each
         v, bound = R.linear(x[at.to(DEV)].cpu(), w, None if iv is None else iv.cpu(), None, "none", False, None, dt)
         R.check(y[at.to(DEV)], v, bound, (e, rows, dt, inv, j))
+
+
+@pytest.mark.parametrize("g", [128, 64, 32])
+@pytest.mark.parametrize("m,n,k", [(2, 48, 640), (12, 40, 640), (40, 40, 640), (300, 520, 640), (2000, 4096, 640), (2000, 4096, 768)])
+def test_scales_at_their_ends(P, m, n, k, g):
+    """Groups of 2^-24, of subnormal and of large scales next to each other, one of NaN: sums of rows of each
+    alone and of all, every change of scale up to 2^36."""
+    ge = gen(m + n + k + g)
+    ng = k // g
+    qw, _, qz = R.packed(ge, (), n, k, g)
+    ends = torch.tensor([2.0 ** -24, 5 * 2.0 ** -24, 2.0 ** -14, 0.01, 1.0, 900.0, 4095.0])
+    sc = ends[torch.randint(0, len(ends), (n, ng), generator=ge)].half()
+    for i, v in enumerate(ends):
+        sc[i] = v                                                       # rows of one scale alone
+    sc[8, ng // 2], sc[9, 0], sc[10, ng - 1] = torch.nan, torch.nan, torch.nan
+    x = (torch.randn(m, k, generator=ge) / 8).to(BF16)
+    x = torch.where(x.abs() < 2.0 ** -10, torch.full_like(x, 2.0 ** -10), x)
+    y = P.awq_linear_w4a16_act_bf16(x.to(DEV), qw.to(DEV), sc.to(DEV), qz.to(DEV), g=g).cpu()
+    assert bool(y[:, 8:11].isnan().all())
+    keep = [i for i in range(n) if not 8 <= i < 11]
+    w = R.weights(qw, sc, qz, g)[keep]
+    v, mag = x.double() @ w.t(), x.double().abs() @ w.abs().t()
+    R.check(y[:, keep], v, ((k + 8) * 2.0 ** -24 + ng * 2.0 ** -22) * mag + R.HALF[BF16] * 1.01 * v.abs() + 1e-37, (m, n, k, g))
