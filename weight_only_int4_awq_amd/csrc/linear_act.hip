@@ -6,11 +6,12 @@
 //
 // Rows of expert i are offsets[i] .. offsets[i + 1] - 1 and use its weights; the row counts
 // are device data, so work-groups find their expert and rows themselves and the grid is an
-// upper bound.  Roundings: bf16 activations once to fp16 (exact within fp16's normal range:
-// the matrix instructions take one type, and the weights' integers need more than bf16's 8
-// bits once scaled); x inv_s once to fp16 (by pairs without loss where a few rows stream, see
-// there); weights exactly.  Sums, bias, activation and residual are fp32 with one rounding at the
-// end.
+// upper bound.  Roundings: bf16 activations once to fp16 (exact within fp16's normal range: the
+// matrix instructions take one type, and neither x inv_s nor weights times their scale fit bf16's
+// 8 bits); x inv_s once to fp16, which is what all linears here take (by pairs without loss where
+// four rows or fewer stream, see there; for more the rest would be a second product of its own,
+// twice the matrix work of the tiles, for 1.7e-4 of a result); weights exactly.  Sums, bias,
+// activation and residual are fp32 with one rounding at the end.
 #include "decode_common.h"
 #include "moe_common.h"
 
@@ -263,9 +264,9 @@ __device__ __forceinline__ void tile_barrier() {
 // (Integers with the other groups' rows as zeros, two or four products a word: 26.2 and 31.9; 109
 // and 153.)
 // Bound by the weights' bytes: one token on two of 8 experts (122 MB) 28.0 us, 4.4 TB/s; dense
-// gate and up of one token (61 MB) 14.4 us, 4.2; 64 tokens on 128 experts (256 MB) 71 us, 3.6:
+// gate and up of one token (61 MB) 14.4 us, 4.2; 64 tokens on 128 experts (256 MB) 69 us, 3.7:
 // there 8000 work-groups of one run to a wave each pay for their plan, their rows and their
-// first load (captured, weights cold: 78 us, without the plan 69, without rows too 54, the
+// first load (captured, weights cold: 77 us, without the plan 69, without rows too 54, the
 // weight loads alone 52).
 // Two blocks of 16 weight rows and up to 4 waves: four blocks or 8 waves leave too few work-
 // groups or registers (experts of 1 token 36 to 46 us against 33, captured, weights cold).
@@ -560,11 +561,11 @@ __global__ __launch_bounds__(256, 2) void linear_act_stream_kernel(const ActArgs
 // (one wave to a SIMD, nothing to cover it) 46 -> 50, 8 experts of 16 rows 158 -> 145; g = 64, gate
 // and up of 2048 rows 468 -> 482; g = 32 491 -> 570.
 // 128-row tiles are bound by the matrix pipe and the card's power: 4096 tokens by twos on 8 experts
-// (1924 GFLOP) 1.99 ms, 968 TFLOP/s where a large library product reaches 1054; 2048 rows of
-// 4096 <- 14336 258 us, 930 TFLOP/s, and 21 us for the rows' conversion.  32-row tiles are
+// (1924 GFLOP) 1.98 ms, 970 TFLOP/s where a large library product reaches 1054; 2048 rows of
+// 4096 <- 14336 262 us, 21 of them the rows' conversion.  32-row tiles are
 // bound by how the cache takes their copies: 64 weight rows a copy are 32 to 64 lines, and a
 // K-step is there when the wave needs it only if enough work-groups share a CU (300 tokens on 60
-// experts, 102 MB: 41 us; 333 rows of 4099 <- 1088: 18 us, a K-step of 64 1.2 us).  Fewer
+// experts, 102 MB: 43 us; 333 rows of 4099 <- 1088: 18 us, a K-step of 64 1.2 us).  Fewer
 // registers by a rolled ring (23.2 against 22.2 us), two stages and a third work-group (53
 // against 48.6) or four and five stages brought nothing.
 constexpr int kTileBN = 256;
@@ -1057,16 +1058,18 @@ __global__ __launch_bounds__(256) void linear_act_prep_kernel(const ActArgs a, u
 //     192 / 256 rows (24 / 32) 13.0 / 18.2 against 16.1 / 16.7; 4096 <- 512, 192 / 256 / 384 rows (12 / 16 / 24)
 //     11.3 / 12.1 / 14.5 against 13.9 / 13.5 / 11.2.  28672 <- 4096 (56 MiB a time): 16 rows streamed 28, 17 rows
 //     by tiles 28 (streamed 38).
-//   streaming or tiles, experts of 2048 <- 1408, mean of 9 rows: 39 against 34; of 1024 x 2 <- 2048, 4 rows
-//     74 against 82, 8 rows 103 against 95: the border is at 6.
+//   streaming or tiles, experts, by their mean of rows: 8 of 14336 x 2 <- 4096, 6 / 7 rows 125 / 138 against 130;
+//     8 of 4096 <- 14336, 6 / 7 rows 75 / 79 against 120; 128 of 1024 x 2 <- 2048, 3 / 5 / 7 rows 69 / 84 / 97
+//     against 76 / 79 / 82; 128 of 2048 <- 1024, 5 / 7 rows 44 / 51 against 44 / 46; 60 of 2048 <- 1408 (g = 64),
+//     3 / 6 rows 35 / 46 against 32 / 34: the border is at 6.
 //   tiles of 32, 64, 128 rows, by the K-steps that 128-row tiles would take in all: 4096 x 4096, 96 rows (1024)
-//     21 / 24 / 28, 256 rows (2048) 30 / 27 / 29.5; 4096 <- 14336, 96 rows (3584) 44 / 38 / 35; between
-//     4096 <- 4096, 520 rows (5120) - / 50 / 46 and 1024 rows (8192) - / 58 / 62 they change places again.
-//   K-steps of 128 or 64 in 32-row tiles: 8 experts of 14336 x 2 <- 4096, 16 rows each 153 against 170.
+//     21 / 24 / 28, 256 rows (2048) 27 / 28 / 29; 4096 <- 14336, 96 rows (3584) 33 / 37 / 36; 4096 <- 4096,
+//     520 rows (5120) 51 / 50 / 43, 1024 rows (8192) 59 / 55 / 56.
+//   K-steps of 128 or 64 in 32-row tiles: 8 experts of 14336 x 2 <- 4096, 16 rows each 143 against 170.
 //   K slices: a matrix of few tiles is split until 256 work-groups have one (a join follows, of 34 MB of
 //     sums at most); two K groups in a work-group where that leaves at most one to a CU.  Split against not:
-//     4096 <- 14336, 1024 rows (128 tiles) 152 against 200; 4096 <- 4096, 520 / 1024 rows 46 / 61 against
-//     66 / 69; 1024 <- 4096, 2048 rows 44 against 70.
+//     4096 <- 14336, 1024 rows (128 tiles) 150 against 228; 4096 <- 4096, 520 / 1024 rows 44 / 56 against
+//     65 / 65; 1024 <- 4096, 2048 rows 37 against 64.
 struct ActPlan {
   bool stream;
   int tm, waves, per;          // stream: rows of a tile, waves, blocks of a wave
