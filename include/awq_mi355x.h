@@ -615,9 +615,9 @@ awq_status awq_attn_kv8_bf16(const awq_kv8_cache* cache, int64_t rows, int64_t m
  *   normal distribution; AWQ_ACT_GELU_TANH v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2.
  *   Sums, bias, activation, product and residual are fp32, rounded once to the
  *   type of y.  x_tilde = fp16_rn(x inv_s16) or x; bf16 x is rounded once to fp16
- *   first (see awq_linear_w4a16_bf16 for its range).  Where m <= 4, what
- *   fp16_rn(x inv_s16) lost is added again, as an fp16 of its own (x_tilde within
- *   max(2^-22 |x inv_s16|, 2^-36); nothing where the product is not finite).  Weights
+ *   first (see awq_linear_w4a16_bf16 for its range).  Where m <= 4 and n < 2^27 - 32
+ *   (gated 2^26 - 16), what fp16_rn(x inv_s16) lost is added again, as an fp16 of its own
+ *   (x_tilde within max(2^-22 |x inv_s16|, 2^-36); nothing where the product is not finite).  Weights
  *   enter the products exactly (with g = 32 and 64 and up to 512 rows they may be infinite
  *   where |(q - z) D| > 65504).
  *   Before the activation the sum is within 5e-3 * max(|v_ref|, rms of the row of
@@ -687,7 +687,8 @@ awq_status awq_linear_w4a16_act_bf16(const uint16_t* x, const uint32_t* qweight,
  *   no expert has are not written.  rows: what row_slot and y hold, at least offsets[e].  The number of rows and experts chooses
  *   between kernels; results are right for any split of the rows.  All rows of an expert
  *   are rounded alike: as pairs (see awq_linear_w4a16_act) those of an expert with up to
- *   four, in calls of up to six rows to an expert on average, and no others.
+ *   four, in calls of up to six rows to an expert on average (where (rows/8 + min(e, rows))
+ *   ceil(n/32), gated ceil(n/16), is below 2^22), and no others.
  *   workspace: awq_moe_linear_workspace_size(rows, x_rows, e, n, k, g, gated,
  *     inv_s16 != NULL, bf16) bytes (x_rows = rows without row_slot), 256-byte aligned.
  *   Limits: those of awq_linear_w4a16_act with rows for m (and x_rows * k/8 <= 2^31), packed
